@@ -624,6 +624,164 @@ int mgemm_topk_sum(const void *in, int64_t T, int top_k, int64_t H, void *out, m
 int mgemm_topk_softmax(const float *gating, int64_t T, int E, int top_k, int renormalize, float *topk_weights,
                        int32_t *topk_ids, mgemm_stream_t stream);
 
+/*
+ * Choosing experts from router scores.  Where mgemm_topk_softmax takes the
+ * top_k of a softmax, mgemm_route covers the routers of layers with many
+ * experts: softmax or sigmoid scores, a balance bias that acts on the choice
+ * only, experts in groups of which the best few are kept, renormalized and
+ * scaled weights, experts that are switched off; and the gradient of the
+ * logits.  (Not on the source pages: an addition of this library.)
+ *
+ * mgemm_route -- per token t, with l = logits[t, :]:
+ *   scores   s = 1 / (1 + exp(-l)) (MGEMM_SCORE_SIGMOID) or softmax(l)
+ *            (MGEMM_SCORE_SOFTMAX).  A logit at or below MGEMM_ROUTE_MASKED
+ *            (-inf and the lowest value of either type) switches its expert
+ *            off: score 0, chosen only after every other expert of the groups
+ *            kept.
+ *   order    c = s + bias[e] (bias may be NULL).  Softmax without bias compares
+ *            the logits (the same order, without rounding ties).  Equal values
+ *            go to the lower id; a NaN is the largest (its weight is NaN).
+ *   groups   n_group > 1: experts g E / n_group .. form group g; its score is
+ *            the largest c of its experts, or with group_top = 2 the sum of the
+ *            two largest (softmax without bias: of exp(l - max l), the same
+ *            order of groups as with the scores); experts that are off add
+ *            nothing, and a group of only such experts comes last.  The
+ *            topk_group best groups are kept (equal scores: the lower group).
+ *   outputs  topk_ids[t, :] = the top_k experts by c in the groups kept, best
+ *            first; topk_weights[t, j] = scale * r_j with r = s[ids], divided by
+ *            their sum when renormalize != 0 (all 0 when that sum is 0).
+ *   logits   float32 or bf16 (logits_bf16 != 0), rows of E values ld elements
+ *            apart (ld >= E), naturally aligned;  bias float32 [E]
+ *   topk_weights  float32 [T, top_k];  topk_ids  int32 [T, top_k]
+ * Everything is computed in float32.  1 <= E <= MGEMM_MAX_EXPERTS; n_group
+ * divides E, 1 <= topk_group <= n_group <= 64; group_top is 1 or 2;
+ * 1 <= top_k <= min(MGEMM_ROUTE_MAX_TOPK, topk_group * E / n_group).
+ *
+ * mgemm_route_bwd -- grad_logits[t, e] = dL / dl for dL / dw = grad_weights[t, :]
+ * (the choice of experts is constant, as is the bias): with f = sum_i g_i w_i /
+ * scale,
+ *   sigmoid, renormalized   w_j (1 - s_j) (g_j - f) at expert ids[j], 0 elsewhere
+ *   sigmoid                 w_j (1 - s_j) g_j       likewise
+ *   softmax, renormalized   w_j (g_j - f)           likewise
+ *   softmax                 w_j g_j at ids[j], and everywhere - s_e sum_i g_i w_i
+ *   topk_weights, topk_ids, logits, scoring, renormalize, scale: as given to and
+ *   written by mgemm_route (scale != 0).  The logits are not read for softmax,
+ *   renormalized (may be NULL).  An id outside [0, E) has no gradient.
+ *   grad_logits  [T, E] of the logits' type, rows ld_grad elements apart; every
+ *                element is written.
+ */
+#define MGEMM_SCORE_SOFTMAX 0
+#define MGEMM_SCORE_SIGMOID 1
+#define MGEMM_ROUTE_MASKED (-3.3e38f)
+#define MGEMM_ROUTE_MAX_TOPK 32
+int mgemm_route(const void *logits, int logits_bf16, int64_t ld, const float *bias, int64_t T, int E, int top_k,
+                int scoring, int n_group, int topk_group, int group_top, int renormalize, float scale,
+                float *topk_weights, int32_t *topk_ids, mgemm_stream_t stream);
+int mgemm_route_bwd(const float *grad_weights, const void *logits, int logits_bf16, int64_t ld,
+                    const float *topk_weights, const int32_t *topk_ids, int64_t T, int E, int top_k, int scoring,
+                    int renormalize, float scale, void *grad_logits, int64_t ld_grad, mgemm_stream_t stream);
+
+/*
+ * 4-bit block-scaled floats.  Codes are e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives; bit 3 the sign), two to a byte, the even element in the low
+ * nibble.  (Not on the source pages: an addition of this library, beside its
+ * MXFP8 and INT4 formats; the scale rule is the same power-of-two rule.)
+ *   MGEMM_MXFP4  one e8m0 byte per 32 elements of a row:
+ *                s = 2^floor(log2(fp32(6 / max(amax, 1e-12)))), code =
+ *                e2m1_rne_sat(x s), byte = 127 - log2(s); value code 2^(byte - 127)
+ *   MGEMM_NVFP4  one e4m3 byte per 16 elements and one float32 per row:
+ *                R = 2^floor(log2(fp32(2688 / max(row amax, 1e-12)))) (2688 = 6 x
+ *                448), b = e4m3_rne(amax16 R / 6), code = e2m1_rne_sat(x R / b), 0
+ *                where b = 0; value code b / R
+ * (finite inputs; others give unspecified codes, and the sign of a zero is
+ * unspecified).
+ *
+ * Scale bytes lie in tiles of 128 rows by one 4-byte word of each row, a word
+ * being the row's scales of 128 (MXFP4) or 64 (NVFP4) consecutive elements:
+ * block q of row r at byte ((r / 128 * W + q / 4) * 128 + (r % 32) * 4 +
+ * (r % 128) / 32) * 4 + q % 4, W = ceil(K / word).  That is the order in which
+ * tensor memory holds a tile's scale factors, so a GEMM stage's scales are
+ * contiguous.  Every group of rows (an expert's weights, a group's tokens)
+ * starts a tile: its tiles follow those of the group before.
+ * mgemm_fp4_scale_bytes: bytes of the scales of `rows` rows of one group, -1 for
+ * bad sizes; E groups of N rows take E times that.
+ */
+#define MGEMM_MXFP4 2
+#define MGEMM_NVFP4 3
+int64_t mgemm_fp4_scale_bytes(int fmt, int64_t rows, int K);
+
+/*
+ * mgemm_quant_fp4 -- cast E groups of N rows (weights [E, N, K]; E = 1: a matrix).
+ *   in         bf16, row i (of E * N) at in + i * ld_in elements (ld_in >= K, % 8 == 0)
+ *   codes      uint8 [E * N, K / 2]
+ *   sf         uint8, E * mgemm_fp4_scale_bytes(fmt, N, K) bytes; every byte is
+ *              written (zeros for rows past N and blocks past K)
+ *   row_scale  float32 [E * N] (MGEMM_NVFP4), else ignored
+ * K % 32 == 0.  E, N >= 0; nothing is launched when either is 0.
+ * mgemm_dequant_fp4 -- the values the codes stand for, to bf16 (exact: a code
+ * times its scales has at most 6 significant bits; below 2^-133 they round, and
+ * past bf16's range they stay at its largest value).
+ *   out        bf16, row i at out + i * ld_out elements (ld_out >= K, % 8 == 0)
+ * Errors: -1 (sizes, format, NULL), -2 (alignment), -4 (CUDA).
+ */
+int mgemm_quant_fp4(const void *in, int E, int64_t N, int K, int64_t ld_in, int fmt, uint8_t *codes, uint8_t *sf,
+                    float *row_scale, mgemm_stream_t stream);
+int mgemm_dequant_fp4(const uint8_t *codes, const uint8_t *sf, const float *row_scale, int E, int64_t N, int K, int fmt,
+                      void *out, int64_t ld_out, mgemm_stream_t stream);
+
+/*
+ * mgemm_quant_fp4_rows -- the cast of token rows in groups whose sizes live on
+ * the device: the x operand of mgemm_fwd_fp4.
+ *   args       filled by mgemm_fill_args for these E groups; the rows are those of
+ *              its offsets, at most M
+ *   in         bf16 [M, K], row stride ld_in elements
+ *   codes      uint8 [M, K / 2];  row_scale  float32 [M] (MGEMM_NVFP4)
+ *   sf         uint8, mgemm_fp4_scale_bytes(fmt, mgemm_colwise_ld(M, E), K) bytes;
+ *              row i of group e lies at tile row poffsets[e] + i; scale rows
+ *              that no token has are not written
+ * With sorted_ids (the routed layer) the rows are gathered as by
+ * mgemm_gather_rows: row i is in[sorted_ids[i] / top_k], zeros where
+ * sorted_ids[i] >= numel or names no row below in_rows; M is then the capacity
+ * of sorted_ids and the outputs, and the args block (M = -1) bounds the rows.
+ * With gated != 0 (no sorted_ids), in is [M, 2 K] and row i is silu(in[i, :K]) *
+ * in[i, K:], rounded to bf16 once, as by mgemm_silu_and_mul.
+ */
+int mgemm_quant_fp4_rows(const void *args, int E, int64_t M, const void *in, int64_t in_rows, int K, int64_t ld_in,
+                         const int32_t *sorted_ids, int64_t numel, int top_k, int gated, int fmt, uint8_t *codes,
+                         uint8_t *sf, float *row_scale, mgemm_stream_t stream);
+
+/*
+ * mgemm_fwd_fp4 -- the grouped product of 4-bit operands: out[r, n] = sum_k
+ * xv[r, k] wv[e(r), n, k], xv and wv the values of the codes; block-scaled
+ * tensor-core MMAs, float32 accumulation, one rounding to bf16.
+ *   args       as for mgemm_fwd;  fmt  MGEMM_MXFP4 or MGEMM_NVFP4 (both operands)
+ *   x, sx, rx  token rows from mgemm_quant_fp4_rows (rx: NVFP4 only)
+ *   w, sw, rw  weights [E, N, K] from mgemm_quant_fp4 (rw: NVFP4 only)
+ *   out        bf16 [M, N]
+ *   row_map, map_limit, row_weight  NULL, or as for mgemm_fwd_scatter: row i goes
+ *              to out[row_map[i]] (not stored outside [0, map_limit)), times
+ *              row_weight[row_map[i]] before the rounding; out is [map_limit, N]
+ * K % 32 == 0, N % 8 == 0.  Errors: -1, -2 (alignment), -3 (E), -4 (CUDA).
+ */
+int mgemm_fwd_fp4(const void *args, int fmt, const uint8_t *x, const uint8_t *sx, const float *rx, const uint8_t *w,
+                  const uint8_t *sw, const float *rw, void *out, const int32_t *row_map, int64_t map_limit,
+                  const float *row_weight, int64_t M, int K, int N, int E, mgemm_stream_t stream);
+
+/*
+ * mgemm_gmm_fp4 -- mgemm_fill_args, mgemm_quant_fp4_rows and mgemm_fwd_fp4 in one
+ * call: out[rows of group e] = x[rows of group e] . w[e]^T for bf16 token rows.
+ *   group_sizes  int64 [E], device, summing to M
+ *   x            bf16 [M, K], row stride ld_x elements
+ *   workspace    mgemm_gmm_fp4_workspace_bytes(fmt, M, K, E) bytes, 16-byte
+ *                aligned, scratch of this call; it starts with the args block,
+ *                whose status word tells of errors found on the device
+ * M = 0 launches nothing.
+ */
+int64_t mgemm_gmm_fp4_workspace_bytes(int fmt, int64_t M, int K, int E);
+int mgemm_gmm_fp4(const int64_t *group_sizes, int E, int fmt, const void *x, int64_t ld_x, const uint8_t *w,
+                  const uint8_t *sw, const float *rw, void *out, int64_t M, int K, int N, void *workspace,
+                  int64_t workspace_bytes, mgemm_stream_t stream);
+
 /* Number of SMs of the current device (the persistent GEMM grid size), or < 0 on error. */
 int mgemm_num_sms(void);
 /* Static string naming a MGEMM_E* or MGEMM_STATUS_* code. */

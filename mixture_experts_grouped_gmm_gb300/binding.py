@@ -19,6 +19,11 @@ LIB_PATH = os.path.join(_PKG, "libmgemm.so")
 MGEMM_OK = 0
 MGEMM_BF16 = 0
 MGEMM_FP8_E4M3 = 1
+MGEMM_MXFP4 = 2
+MGEMM_NVFP4 = 3
+MGEMM_SCORE_SOFTMAX = 0
+MGEMM_SCORE_SIGMOID = 1
+MGEMM_ROUTE_MAX_TOPK = 32
 MGEMM_MAX_EXPERTS = 1024
 MGEMM_TILE_M = 128
 MGEMM_COL_PAD = 128
@@ -116,6 +121,33 @@ _SIGS = {
                                              ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_void_p, ctypes.c_void_p]),
+    "mgemm_route": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                   ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                   ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "mgemm_route_bwd": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                       ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_int64,
+                                       ctypes.c_void_p]),
+    "mgemm_fp4_scale_bytes": (ctypes.c_int64, [ctypes.c_int, ctypes.c_int64, ctypes.c_int]),
+    "mgemm_quant_fp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int64,
+                                       ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p]),
+    "mgemm_dequant_fp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64,
+                                         ctypes.c_void_p]),
+    "mgemm_quant_fp4_rows": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "mgemm_fwd_fp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
+                                     ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "mgemm_gmm_fp4_workspace_bytes": (ctypes.c_int64, [ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int]),
+    "mgemm_gmm_fp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64,
+                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64,
+                                     ctypes.c_void_p]),
     "mgemm_num_sms": (ctypes.c_int, []),
     "mgemm_error_string": (ctypes.c_char_p, [ctypes.c_int]),
     "mgemm_version": (ctypes.c_int, []),
@@ -422,6 +454,79 @@ def mgemm_moe_route_align(gating, T, E, top_k, renormalize, block_size, topk_wei
                                        int(block_size), _p(topk_weights), _p(topk_ids), _p(sorted_ids),
                                        _p(expert_ids), _p(num_post_padded), _p(group_sizes), _p(args),
                                        _stream(sorted_ids)), "mgemm_moe_route_align")
+
+
+def mgemm_route(logits, bias, top_k, scoring, n_group, topk_group, group_top, renormalize, scale, topk_weights,
+                topk_ids):
+    """logits float32 or bf16 [T, E] (unit column stride) -> topk_weights float32, topk_ids int32 [T, top_k]."""
+    _cuda(logits, bias, topk_weights, topk_ids)
+    T, E = logits.shape
+    _check(lib().mgemm_route(_p(logits), int(logits.dtype == torch.bfloat16), logits.stride(0), _p(bias), T, E,
+                             int(top_k), int(scoring), int(n_group), int(topk_group), int(group_top),
+                             int(bool(renormalize)), float(scale), _p(topk_weights), _p(topk_ids), _stream(logits)),
+           "mgemm_route")
+
+
+def mgemm_route_bwd(grad_weights, logits, topk_weights, topk_ids, scoring, renormalize, scale, grad_logits):
+    """grad_logits [T, E] (the logits' type) from grad_weights float32 [T, top_k]."""
+    _cuda(grad_weights, logits, topk_weights, topk_ids, grad_logits)
+    T, E = grad_logits.shape
+    ld = logits.stride(0) if logits is not None else E
+    _check(lib().mgemm_route_bwd(_p(grad_weights), _p(logits), int(grad_logits.dtype == torch.bfloat16), ld,
+                                 _p(topk_weights), _p(topk_ids), T, E, topk_ids.shape[1], int(scoring),
+                                 int(bool(renormalize)), float(scale), _p(grad_logits), grad_logits.stride(0),
+                                 _stream(grad_logits)), "mgemm_route_bwd")
+
+
+def mgemm_fp4_scale_bytes(fmt, rows, K):
+    """Bytes of the tiled scale factors of `rows` rows (one group) of K elements."""
+    return int(lib().mgemm_fp4_scale_bytes(int(fmt), int(rows), int(K)))
+
+
+def mgemm_quant_fp4(inp, fmt, codes, sf, row_scale=None):
+    """inp bf16 [E, N, K] (rows at a common stride) -> codes uint8 [E, N, K / 2], sf uint8
+    [E * mgemm_fp4_scale_bytes(fmt, N, K)], row_scale float32 [E, N] (MGEMM_NVFP4)."""
+    _cuda(inp, codes, sf, row_scale)
+    E, N, K = inp.shape
+    if E * N > 0 and (inp.stride(2) != 1 or (E > 1 and inp.stride(0) != N * inp.stride(1))):
+        raise MgemmError("mgemm_quant_fp4 takes [E, N, K] with rows (e, n) at a common stride")
+    _check(lib().mgemm_quant_fp4(_p(inp), E, N, K, inp.stride(1), int(fmt), _p(codes), _p(sf), _p(row_scale),
+                                 _stream(inp)), "mgemm_quant_fp4")
+
+
+def mgemm_dequant_fp4(codes, sf, row_scale, E, N, K, fmt, out):
+    """The values of the codes, bf16 [E, N, K] (contiguous)."""
+    _cuda(codes, sf, row_scale, out)
+    _check(lib().mgemm_dequant_fp4(_p(codes), _p(sf), _p(row_scale), int(E), int(N), int(K), int(fmt), _p(out), int(K),
+                                   _stream(out)), "mgemm_dequant_fp4")
+
+
+def mgemm_quant_fp4_rows(args, E, M, inp, K, fmt, codes, sf, row_scale=None, sorted_ids=None, numel=0, top_k=1,
+                         gated=False):
+    """Token rows in the args block's groups (gathered through sorted_ids, or gated: inp [M, 2K])."""
+    _cuda(args, inp, codes, sf, row_scale, sorted_ids)
+    _check(lib().mgemm_quant_fp4_rows(_p(args), int(E), int(M), _p(inp), inp.shape[0], int(K), inp.stride(0),
+                                      _p(sorted_ids), int(numel), int(top_k), int(bool(gated)), int(fmt), _p(codes),
+                                      _p(sf), _p(row_scale), _stream(codes)), "mgemm_quant_fp4_rows")
+
+
+def mgemm_fwd_fp4(args, fmt, x, sx, rx, w, sw, rw, out, M, K, N, E, row_map=None, map_limit=0, row_weight=None):
+    _cuda(args, x, sx, rx, w, sw, rw, out, row_map, row_weight)
+    _check(lib().mgemm_fwd_fp4(_p(args), int(fmt), _p(x), _p(sx), _p(rx), _p(w), _p(sw), _p(rw), _p(out), _p(row_map),
+                               int(map_limit), _p(row_weight), int(M), int(K), int(N), int(E), _stream(out)),
+           "mgemm_fwd_fp4")
+
+
+def mgemm_gmm_fp4_workspace_bytes(fmt, M, K, E):
+    return int(lib().mgemm_gmm_fp4_workspace_bytes(int(fmt), int(M), int(K), int(E)))
+
+
+def mgemm_gmm_fp4(group_sizes, E, fmt, x, w, sw, rw, out, M, K, N, workspace):
+    """fill + cast of the token rows + grouped product; workspace uint8 (mgemm_gmm_fp4_workspace_bytes)."""
+    _cuda(group_sizes, x, w, sw, rw, out, workspace)
+    _check(lib().mgemm_gmm_fp4(_p(group_sizes), int(E), int(fmt), _p(x), x.stride(0), _p(w), _p(sw), _p(rw), _p(out),
+                               int(M), int(K), int(N), _p(workspace), workspace.numel(), _stream(out)),
+           "mgemm_gmm_fp4")
 
 
 def mgemm_num_sms():

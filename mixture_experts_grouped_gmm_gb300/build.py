@@ -21,7 +21,7 @@ LIB_PATH = os.path.join(PKG, "libmgemm.so")
 
 SOURCES = ["args.cu", "quant.cu", "gemm_bf16.cu", "gemm_fp8.cu", "gemm_api.cu", "gemm_f8i4.cu", "gemm_sparse.cu",
            "noalloc.cu",
-           "routing.cu"]
+           "routing.cu", "route.cu", "fp4.cu", "gemm_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I" + INCLUDE]
 

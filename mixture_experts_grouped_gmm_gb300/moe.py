@@ -73,6 +73,71 @@ def route(gating_output, topk, renormalize):
     return w, i
 
 
+SCORES = {"softmax": B.MGEMM_SCORE_SOFTMAX, "sigmoid": B.MGEMM_SCORE_SIGMOID}
+
+
+def _route_logits(logits, scoring):
+    if scoring not in SCORES:
+        raise B.MgemmError(f"unknown scoring {scoring!r} (one of {', '.join(SCORES)})")
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise B.MgemmError("routing takes float32 or bf16 logits [T, E]")
+    return logits if logits.stride(1) == 1 and logits.stride(0) >= logits.shape[1] else logits.contiguous()
+
+
+def route_experts(logits, topk, scoring="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renormalize=True,
+                  scale=1.0):
+    """Experts of each token from router logits float32 or bf16 [T, E] (mgemm_route):
+    softmax or sigmoid scores, ``bias`` float32 [E] added for the choice only, the
+    best ``topk_group`` of ``n_group`` groups kept (by their best, or with
+    ``group_top=2`` their two best experts), the topk largest, weights renormalized
+    when asked and times ``scale``.  A logit of -inf (or its type's lowest value)
+    switches the expert off.  Returns (topk_weights float32 [T, topk], topk_ids
+    int32 [T, topk]); ``Router`` is the same with a gradient."""
+    logits = _route_logits(logits, scoring)
+    if bias is not None and (bias.dtype != torch.float32 or bias.numel() != logits.shape[1] or
+                             not bias.is_contiguous()):
+        raise B.MgemmError("the routing bias is a contiguous float32 [E]")
+    T = logits.shape[0]
+    w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
+    ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
+    B.mgemm_route(logits, bias, topk, SCORES[scoring], n_group, topk_group, group_top, renormalize, scale, w, ids)
+    return w, ids
+
+
+def route_experts_backward(grad_weights, logits, topk_weights, topk_ids, scoring="softmax", renormalize=True,
+                           scale=1.0):
+    """The logits' gradient [T, E] (in their type) of route_experts' weights (mgemm_route_bwd)."""
+    logits = _route_logits(logits, scoring)
+    if topk_weights.shape != topk_ids.shape or grad_weights.shape != topk_ids.shape or \
+            topk_ids.dtype != torch.int32 or topk_weights.dtype != torch.float32 or \
+            not topk_weights.is_contiguous() or not topk_ids.is_contiguous():
+        raise B.MgemmError("route_experts_backward takes route_experts' weights and ids and a gradient of their shape")
+    grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    g = grad_weights.to(torch.float32).contiguous()
+    B.mgemm_route_bwd(g, logits, topk_weights, topk_ids, SCORES[scoring], renormalize, scale, grad)
+    return grad
+
+
+class Router(torch.autograd.Function):
+    """route_experts as an autograd op: ``Router.apply(logits, topk, scoring, bias,
+    n_group, topk_group, group_top, renormalize, scale)``.  The ids and the bias
+    have no gradient."""
+
+    @staticmethod
+    def forward(ctx, logits, topk, scoring="softmax", bias=None, n_group=1, topk_group=1, group_top=1,
+                renormalize=True, scale=1.0):
+        w, ids = route_experts(logits, topk, scoring, bias, n_group, topk_group, group_top, renormalize, scale)
+        ctx.save_for_backward(logits, w, ids)
+        ctx.how = (scoring, renormalize, scale)
+        ctx.mark_non_differentiable(ids)
+        return w, ids
+
+    @staticmethod
+    def backward(ctx, grad_weights, _grad_ids):
+        logits, w, ids = ctx.saved_tensors
+        return (route_experts_backward(grad_weights, logits, w, ids, *ctx.how),) + (None,) * 8
+
+
 def route_align(gating_output, topk, renormalize, block=BLOCK):
     """mgemm_moe_route_align from gating logits [T, E], with freshly allocated
     outputs: (topk_weights, topk_ids, sorted_ids, expert_ids, num_post_padded,

@@ -34,9 +34,11 @@ Modules:
   mx     -- MXFP8: 32-element block scales (e8m0), row and per-group column block quantize, block-scaled fwd and wgrad
   f8i4   -- FP8 x INT4: 32-element INT4 block quantize (e8m0 scales), nibble packing, the grouped forward
   routing -- moe_align_block_size, gather, topk_softmax, silu_and_mul and the fused_moe layer of the routed path
+  fp4     -- 4-bit block-scaled floats (MXFP4, NVFP4): casts, scale tiles, the grouped product
+  router  -- choice of experts (softmax / sigmoid scores, bias, groups) and the logits' gradient
 
 Parity status: every function is pinned by a ``-m "not gpu"`` test in
 ``tests/test_oracle_*.py``; none is "parity unpinned".
 """
 
-from . import args, f8i4, formats, gmm, mx, quant, routing  # noqa: F401
+from . import args, f8i4, formats, fp4, gmm, mx, quant, router, routing  # noqa: F401
