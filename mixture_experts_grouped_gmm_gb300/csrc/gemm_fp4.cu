@@ -1,12 +1,32 @@
 // mgemm_fwd_fp4 / mgemm_gmm_fp4: the grouped product of 4-bit block-scaled
-// operands,
+// operands on the tensor cores,
 //
 //   out[r, n] = sum_k xv[r, k] wv[e(r), n, k]
 //
-// over the tile schedule of mgemm_fill_args.  A tile is 128 token rows of one
-// group by 64 output columns; 32 elements of the contraction at a time are
-// decoded to fp32 in shared memory and multiplied on the CUDA cores, each
-// thread 8 x 4 outputs.
+// over the tile schedule of mgemm_fill_args.  The MMAs are block-scaled
+// (kind::mxf4nvf4): D += sum over the 64 elements of a step of (a sfa)(b sfb),
+// with one scale per 32 (MXFP4, e8m0) or 16 (NVFP4, e4m3) elements of each row
+// read from tensor memory.  NVFP4's two row scales are powers of two outside
+// the sum: the epilogue multiplies by 1 / rx[r] and 1 / rw[e, n].
+//
+// A tile is 128 token rows of one group by bn columns; a stage holds 256
+// elements of the contraction (128 bytes of a row): the operands' codes,
+// 128-byte swizzled by TMA, and their scale words, which the global layout
+// keeps in the order tensor memory wants them, so the MMA thread only copies
+// them there (tcgen05.cp, 512 bytes per 128 rows and word) ahead of the
+// stage's four MMAs.
+//
+// CTA (persistent, one per SM, 320 threads):
+//   warp 0     TMA producer: a ring of stages, as many as fit
+//   warp 1     TMEM owner; one thread copies scales and issues MMAs
+//   warps 2-9  epilogue, two per TMEM lane quarter, each half of the columns:
+//              the accumulator is read, scaled and rounded into registers,
+//              handed back, and then stored (32 bytes per lane and store)
+// TMEM: accumulators in columns 0 .. 255 (one of 256 columns or two of at most
+// 128), kSfSlots slots of scales behind them.  A slot is rewritten once the
+// MMAs that read it have completed: the stage's empty barrier says so.
+// Every wait is bounded; on expiry the kernel records MGEMM_STATUS_TIMEOUT,
+// drains the copies and MMAs it issued, frees TMEM and returns.
 #include "fp4.cuh"
 
 namespace mgemm {
@@ -14,86 +34,423 @@ namespace {
 
 struct Fp4Params {
   const uint8_t *args;
-  const uint8_t *x, *sx, *w, *sw;
   const float *rx, *rw;
   __nv_bfloat16 *out;
   const int32_t *row_map;
   int64_t map_limit;
   const float *row_weight;
-  int64_t M;
-  int K, N, E, n_tiles;
+  int K, N, E;
+  int bn, n_tiles;    // columns per tile: 64, 128 or 256
+  int a_rows;         // rows of an A box: 128, or fewer when M is smaller (a multiple of 8)
+  int stages, stage_bytes;
+  int vec32;          // output rows and tiles start on 32-byte boundaries
 };
 
-constexpr int kBm = 128, kBn = 64, kBk = 32;
+constexpr int kF4Threads = 320;
+constexpr int kF4EpiWarps = 8;
+constexpr int kF4MaxStages = 20;
+constexpr int kSfSlots = 4;
+constexpr int kSfCol0 = 256;  // first TMEM column of the scales
+constexpr size_t kF4Limit = (size_t)227 * 1024;
 
 template <int FMT>
-__global__ void __launch_bounds__(256) fp4_gemm_kernel(const Fp4Params p) {
-  using F = Fp4<FMT>;
+struct F4Cfg {
+  static constexpr bool NV = FMT == MGEMM_NVFP4;
+  static constexpr int WPS = 256 / Fp4<FMT>::WORD;  // scale words of a row per stage: 4 or 2
+  // codes then scales; nt = scale tiles (128 columns) of the B tile
+  static int stage_bytes(int a_rows, int bn) {
+    const int nt = (bn + 127) / 128;
+    return (a_rows + bn) * 128 + (1 + nt) * WPS * 512;
+  }
+};
+
+struct F4Shared {
+  uint64_t full[kF4MaxStages], empty[kF4MaxStages], tfull[2], tempty[2], drain;
+  uint32_t tmem_slot;
+  int abort_flag;
+  float cinv[kF4EpiWarps][128];  // the warps' column factors
+};
+
+struct F4Tile {
+  int e, n0, rows, row0, sf_tile;
+};
+
+// The tile t: group by the row-tile prefix, row tiles fastest inside it, so
+// that CTAs running together share a weight tile through L2.
+__device__ __forceinline__ F4Tile f4_tile(int t, const Fp4Params &p, const ArgsView &av, int na) {
+  const int gm = t / p.n_tiles;
+  int lo = 0, hi = na - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(av.mtile_start + mid) <= gm) lo = mid; else hi = mid - 1;
+  }
+  const int first = __ldg(av.mtile_start + lo), mts = __ldg(av.mtile_start + lo + 1) - first;
+  F4Tile ti;
+  ti.e = __ldg(av.active + lo);
+  const int local = t - first * p.n_tiles, mt = local % mts;
+  ti.n0 = local / mts * p.bn;
+  const int64_t rs = __ldg(av.offsets + ti.e), re = __ldg(av.offsets + ti.e + 1);
+  ti.row0 = (int)rs + mt * 128;
+  ti.rows = min((int)(re - ti.row0), p.a_rows);
+  ti.sf_tile = (int)(__ldg(av.poffsets + ti.e) >> 7) + mt;
+  return ti;
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_f4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                       uint32_t accumulate) {
+  if (FMT == MGEMM_NVFP4)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of the block-scaled 4-bit MMA: e2m1 A and B (code 1),
+// K-major, M = m, N = n, scales ue4m3 (0) or ue8m0 (1); the scale-factor ids
+// (bits 4-5 and 29-30) are or-ed in per MMA.
+__device__ __forceinline__ uint32_t f4_idesc(int m, int n, uint32_t ue8m0) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (ue8m0 << 23) | ((uint32_t)(m >> 4) << 24);
+}
+
+// 1 / s of a power of two s
+__device__ __forceinline__ float f4_recip(float s) { return __uint_as_float(0x7F000000u - __float_as_uint(s)); }
+
+__device__ __forceinline__ void store_32b(void *dst, const uint32_t *v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kF4Threads, 1)
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                    const __grid_constant__ Fp4Params p) {
+  using C = F4Cfg<FMT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // [stages x (A codes | B codes)], then the stages' scales [A tile: WPS words][B tiles: WPS words each]
+  const int nst = p.stages, bn = p.bn, nt = (bn + 127) / 128;
+  const int op_bytes = (p.a_rows + bn) * 128, sf_bytes = (1 + nt) * C::WPS * 512;
+  uint8_t *sSF = smem + (size_t)nst * op_bytes;
+  F4Shared &S = *reinterpret_cast<F4Shared *>(sSF + (size_t)nst * sf_bytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nacc = bn == 256 ? 1 : 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < nst; ++i) {
+      mbar_init(&S.full[i], 1);
+      mbar_init(&S.empty[i], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&S.tfull[a], 1);
+      mbar_init(&S.tempty[a], kF4EpiWarps);
+    }
+    mbar_init(&S.drain, 1);
+    S.abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+  }
+  if (warp == 1) {
+    tmem_alloc(&S.tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = S.tmem_slot;
   pdl_wait();
   pdl_trigger();
-  __shared__ float sA[kBk][kBm + 4], sB[kBk][kBn + 4];
   const ArgsView av(p.args, p.E);
-  if (*av.status != 0) return;
-  const int na = *av.n_active;
-  const int total = __ldg(av.mtile_start + na) * p.n_tiles;
-  const int W = fp4_words(FMT, p.K);
-  const int64_t npad = (p.N + 127) / 128 * 128;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  auto load = [&](const uint8_t *codes, const uint8_t *sf, int64_t row, int64_t tile_row, int c) -> float {
-    const int q = c / F::BLOCK;
-    const uint32_t byte = sf[fp4_sf_offset(tile_row, q >> 2, W) + (q & 3)];
-    const uint32_t b = codes[row * (p.K / 2) + c / 2];
-    return e2m1_value(c & 1 ? b >> 4 : b & 15u) * (F::NV ? e4m3_value(byte) : e8m0_value(byte));
+  const int status0 = *av.status, na = *av.n_active;
+  const int total = status0 != 0 ? 0 : __ldg(av.mtile_start + na) * p.n_tiles;
+  const int kb_count = (p.K + 255) / 256;
+  volatile int *vabort = &S.abort_flag;
+  uint32_t issued = 0;  // stages armed, for the drain after an abort
+  auto timeout = [&]() {
+    set_status(av.status, MGEMM_STATUS_TIMEOUT);
+    *vabort = 1;
   };
-  for (int t = blockIdx.x; t < total; t += gridDim.x) {
-    const int gm = t / p.n_tiles, n0 = (t % p.n_tiles) * kBn;
-    int lo = 0, hi = na - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(av.mtile_start + mid) <= gm) lo = mid; else hi = mid - 1;
-    }
-    const int e = __ldg(av.active + lo);
-    const int64_t first = (int64_t)(gm - __ldg(av.mtile_start + lo)) * kBm;  // row inside the group
-    const int64_t row0 = __ldg(av.offsets + e) + first, end = __ldg(av.offsets + e + 1);
-    const int64_t prow0 = __ldg(av.poffsets + e) + first;
-    float acc[8][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += kBk) {
-      for (int i = threadIdx.x; i < kBm * kBk; i += 256) {
-        const int r = i / kBk, c = i % kBk;
-        sA[c][r] = row0 + r < end ? load(p.x, p.sx, row0 + r, prow0 + r, k0 + c) : 0.f;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      const uint32_t tx = (uint32_t)p.stage_bytes;
+      const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert's weights
+      for (int t = blockIdx.x; t < total && !*vabort; t += gridDim.x) {
+        const F4Tile ti = f4_tile(t, p, av, na);
+        const int sfb_tile = ti.e * wtiles + ti.n0 / 128;
+        for (int kb = 0; kb < kb_count; ++kb) {
+          if (!mbar_wait(&S.empty[stage], phase ^ 1, vabort)) {
+            timeout();
+            break;
+          }
+          mbar_arrive_expect_tx(&S.full[stage], tx);
+          ++issued;
+          uint8_t *a = smem + (size_t)stage * op_bytes, *sf = sSF + (size_t)stage * sf_bytes;
+          tma_load_3d(a + p.a_rows * 128, &tmB, &S.full[stage], kb * 128, ti.n0, ti.e);
+          tma_load_3d(sf + C::WPS * 512, &tmSB, &S.full[stage], 0, kb * C::WPS, sfb_tile);
+          tma_load_2d(a, &tmA, &S.full[stage], kb * 128, ti.row0);
+          tma_load_3d(sf, &tmSA, &S.full[stage], 0, kb * C::WPS, ti.sf_tile);
+          if (++stage == nst) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
       }
-      for (int i = threadIdx.x; i < kBn * kBk; i += 256) {
-        const int n = i / kBk, c = i % kBk;
-        sB[c][n] = n0 + n < p.N ? load(p.w, p.sw, (int64_t)e * p.N + n0 + n, e * npad + n0 + n, k0 + c) : 0.f;
-      }
-      __syncthreads();
-#pragma unroll 4
-      for (int c = 0; c < kBk; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sA[c][ty * 8 + i], sB[c][tx * 4 + j], acc[i][j]);
-      __syncthreads();
     }
-    for (int i = 0; i < 8; ++i) {
-      const int64_t r = row0 + ty * 8 + i;
-      if (r >= end) break;
-      int64_t dst = r;
-      float wgt = 1.f;
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0, acc = 0, slot = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      int old = 0;  // the stage of kSfSlots iterations ago, and its phase
+      uint32_t old_phase = 0, it = 0;
+      bool ok = true;
+      const int sfc = C::WPS * (4 + 4 * nt);  // TMEM columns of a slot
+      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+        const F4Tile ti = f4_tile(t, p, av, na);
+        if (!mbar_wait(&S.tempty[acc], acc_phase ^ 1, vabort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * 128;
+        const int cols = min(bn, (p.N - ti.n0 + 15) & ~15);
+        const uint32_t idesc = f4_idesc(128, cols, C::NV ? 0u : 1u);
+        // a 64-column tile may start in the middle of a 128-column scale tile
+        const uint32_t sfb_off = (ti.n0 & 64) ? 2u : 0u;
+        for (int kb = 0; kb < kb_count; ++kb) {
+          if (!mbar_wait(&S.full[stage], phase, vabort)) {
+            ok = false;
+            break;
+          }
+          // the slot's last readers have completed (a ring of no more stages than slots says so by itself)
+          if (it >= kSfSlots && nst > kSfSlots) {
+            if (!mbar_wait(&S.empty[old], old_phase, vabort)) {
+              ok = false;
+              break;
+            }
+            if (++old == nst) {
+              old = 0;
+              old_phase ^= 1;
+            }
+          }
+          ++it;
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + (size_t)stage * op_bytes), b = a + p.a_rows * 128;
+          const uint32_t sf = smem_u32(sSF + (size_t)stage * sf_bytes);
+          const uint32_t sfa_t = tmem_base + kSfCol0 + slot * sfc, sfb_t = sfa_t + 4 * C::WPS;
+          const int steps = min(4, (p.K - kb * 256 + 63) / 64);
+          const int words = C::NV ? steps : (steps + 1) / 2;
+#pragma unroll
+          for (int j = 0; j < C::WPS; ++j) {
+            if (j >= words) break;
+            tmem_cp_32x128b_warpx4(sfa_t + 4 * j, smem_desc_rows16(sf + j * 512));
+            for (int i = 0; i < nt; ++i)
+              tmem_cp_32x128b_warpx4(sfb_t + 4 * (j * nt + i), smem_desc_rows16(sf + ((1 + i) * C::WPS + j) * 512));
+          }
+          const uint64_t ad = smem_desc_sw128(a, 16, 1024), bd = smem_desc_sw128(b, 16, 1024);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k >= steps) break;
+            const int j = C::NV ? k : k / 2;
+            const uint32_t id = C::NV ? 0u : (uint32_t)(k & 1) * 2u;
+            mma_f4<FMT>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), sfa_t + 4 * j,
+                        sfb_t + 4 * j * nt + sfb_off, (kb | k) != 0);
+          }
+          mma_commit(&S.empty[stage]);
+          if (++slot == kSfSlots) slot = 0;
+          if (++stage == nst) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        mma_commit(&S.tfull[acc]);
+        if (++acc == nacc) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      if (!ok) timeout();
+      mma_commit(&S.drain);
+      mbar_wait_drain(&S.drain, 0);
+    }
+    __syncwarp();
+  } else {
+    const int ew = warp - 2, q = warp & 3, h = ew >> 2;
+    const int r = q * 32 + lane;   // the thread's row of the tile
+    const int half = bn / 2;       // columns per warp: 32, 64 or 128
+    float *cinv = S.cinv[ew];
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = blockIdx.x; t < total; t += gridDim.x) {
+      const F4Tile ti = f4_tile(t, p, av, na);
+      const int col0 = ti.n0 + h * half;
+      bool row_ok = r < ti.rows;
+      int64_t dst = (int64_t)ti.row0 + r;
+      float f = 1.f;  // the row's factor
       if (p.row_map) {
-        dst = __ldg(p.row_map + r);
-        if (dst < 0 || dst >= p.map_limit) continue;
-        if (p.row_weight) wgt = __ldg(p.row_weight + dst);
+        const int32_t d = row_ok ? __ldg(p.row_map + dst) : -1;
+        row_ok = d >= 0 && d < p.map_limit;
+        if (row_ok && p.row_weight) f = __ldg(p.row_weight + d);
+        if (C::NV && row_ok) f *= f4_recip(__ldg(p.rx + dst));
+        dst = row_ok ? d : 0;
+      } else if (C::NV && row_ok) {
+        f = f4_recip(__ldg(p.rx + dst));
       }
-      const float ri = F::NV ? 1.f / __ldg(p.rx + r) : 1.f;
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + tx * 4 + j;
-        if (n >= p.N) break;
-        const float ci = F::NV ? 1.f / __ldg(p.rw + (int64_t)e * p.N + n) : 1.f;
-        p.out[dst * p.N + n] = __float2bfloat16_rn(acc[i][j] * ri * ci * wgt);
+      if (C::NV) {
+        for (int c = lane; c < half; c += 32)
+          cinv[c] = col0 + c < p.N ? f4_recip(__ldg(p.rw + (int64_t)ti.e * p.N + col0 + c)) : 0.f;
+        __syncwarp();
       }
+      if (!mbar_wait_warp(&S.tfull[acc], acc_phase, vabort)) {
+        if (lane == 0) timeout();
+        break;
+      }
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 128 + h * half;
+      uint32_t pk[4][16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c * 32 >= half) break;
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(taddr + c * 32, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float v0 = __uint_as_float(v[2 * j]) * f, v1 = __uint_as_float(v[2 * j + 1]) * f;
+          if (C::NV) {
+            const float2 ci = *reinterpret_cast<const float2 *>(cinv + c * 32 + 2 * j);
+            v0 *= ci.x;
+            v1 *= ci.y;
+          }
+          __nv_bfloat162 b2 = __floats2bfloat162_rn(v0, v1);
+          pk[c][j] = *reinterpret_cast<uint32_t *>(&b2);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.tempty[acc]);
+      if (++acc == nacc) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+      if (row_ok) {
+        __nv_bfloat16 *o = p.out + dst * p.N + col0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c * 32 >= half) break;
+          if (p.vec32) {  // whole 32-byte sectors (N % 16 == 0)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (col0 + c * 32 + j * 16 < p.N) store_32b(o + c * 32 + j * 16, &pk[c][8 * j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (col0 + c * 32 + j * 8 < p.N)
+                *reinterpret_cast<uint4 *>(o + c * 32 + j * 8) =
+                    make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2], pk[c][4 * j + 3]);
+          }
+        }
+      }
+      __syncwarp();  // the column factors are read
     }
   }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*vabort && warp == 0 && lane == 0) {
+    // wait for the copies this CTA armed, bounded
+    for (int i = 0; i < nst; ++i) {
+      const uint32_t armed = issued / nst + ((uint32_t)i < issued % nst ? 1u : 0u);
+      if (armed) mbar_wait_drain(&S.full[i], (armed - 1) & 1);
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int FMT>
+int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, Fp4Params p, int64_t M,
+               int sms, cudaStream_t s) {
+  using C = F4Cfg<FMT>;
+  const int E = p.E, K = p.K, N = p.N;
+  // columns per tile: the fewest rounds of tiles over the SMs, weighted by the
+  // columns plus a tile's fixed cost; wider at equal cost (fewer reads of A)
+  const int64_t groups = M < E ? M : E, m_est = (M + 127) / 128 > groups ? (M + 127) / 128 : groups;
+  int bn = 256;
+  int64_t best = -1;
+  for (int c : {256, 128, 64}) {
+    const int64_t cost = (m_est * ((N + c - 1) / c) + sms - 1) / sms * (c + 32);
+    if (best < 0 || cost < best) {
+      best = cost;
+      bn = c;
+    }
+  }
+  p.bn = bn;
+  p.n_tiles = (N + bn - 1) / bn;
+  p.a_rows = M < 128 ? (int)((M + 7) / 8 * 8) : 128;
+  p.vec32 = N % 16 == 0 && ((uintptr_t)p.out & 31) == 0;
+  p.stage_bytes = C::stage_bytes(p.a_rows, bn);
+  // the MMA reads 128 A rows from a stage's start whatever the box holds: room behind the last stage
+  const size_t fixed = 1024 + sizeof(F4Shared) + (size_t)(128 - p.a_rows) * 128;
+  int st = (int)((kF4Limit - fixed) / p.stage_bytes);
+  if (st > kF4MaxStages) st = kF4MaxStages;
+  p.stages = st;
+  const size_t smem = fixed + (size_t)st * p.stage_bytes;
+  const int W = fp4_words(FMT, K), nt = (bn + 127) / 128;
+  CUtensorMap ta, tb, tsa, tsb;
+  {
+    const uint64_t d[2] = {(uint64_t)K / 2, (uint64_t)M}, str[1] = {(uint64_t)K / 2};
+    const uint32_t box[2] = {128, (uint32_t)p.a_rows};
+    if (!make_tensor_map(&ta, true, 2, x, d, str, box)) return MGEMM_ECUDA;
+  }
+  {
+    const uint64_t d[3] = {(uint64_t)K / 2, (uint64_t)N, (uint64_t)E};
+    const uint64_t str[2] = {(uint64_t)K / 2, (uint64_t)N * (K / 2)};
+    const uint32_t box[3] = {128, (uint32_t)bn, 1};
+    if (!make_tensor_map(&tb, true, 3, w, d, str, box)) return MGEMM_ECUDA;
+  }
+  // scales: 512-byte word tiles as 256 two-byte elements, {256, words, row tiles}
+  auto sf_map = [&](CUtensorMap *m, const uint8_t *base, int64_t tiles, int box_tiles) {
+    const uint64_t d[3] = {256, (uint64_t)W, (uint64_t)tiles};
+    const uint64_t str[2] = {512, (uint64_t)W * 512};
+    const uint32_t box[3] = {256, (uint32_t)C::WPS, (uint32_t)box_tiles};
+    return make_tensor_map(m, false, 3, base, d, str, box, false);
+  };
+  if (!sf_map(&tsa, sx, mgemm_colwise_ld(M, E) / 128, 1)) return MGEMM_ECUDA;
+  if (!sf_map(&tsb, sw, (int64_t)E * ((N + 127) / 128), nt)) return MGEMM_ECUDA;
+  static bool attr_done[64] = {};
+  int dev = 0;
+  int rc = cuda_rc(cudaGetDevice(&dev), "cudaGetDevice");
+  if (rc) return rc;
+  if (dev < 0 || dev >= 64) return MGEMM_EINVAL;
+  if (!attr_done[dev]) {
+    rc = cuda_rc(cudaFuncSetAttribute(fp4_gemm_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kF4Limit),
+                 "cudaFuncSetAttribute");
+    if (rc) return rc;
+    attr_done[dev] = true;
+  }
+  const int64_t upper = ((M + 127) / 128 + groups) * p.n_tiles;
+  const unsigned grid = (unsigned)(upper < sms ? upper : sms);
+  return launch_pdl(fp4_gemm_kernel<FMT>, dim3(grid), dim3(kF4Threads), smem, s, 1, "mgemm_fwd_fp4 launch", ta, tb, tsa,
+                    tsb, p);
 }
 
 bool a16(const void *p) { return ((uintptr_t)p & 15) == 0; }
@@ -138,14 +495,23 @@ extern "C" int mgemm_fwd_fp4(const void *args, int fmt, const uint8_t *x, const 
   if (!a16(args) || !a16(x) || !a16(sx) || ((uintptr_t)rx & 3) || ((uintptr_t)row_map & 3) || ((uintptr_t)row_weight & 3))
     return MGEMM_EALIGN;
   if (M == 0) return MGEMM_OK;
+  rc = ensure_context();
+  if (rc) return rc;
   const int sms = sm_count_cached();
   if (sms <= 0) return MGEMM_ECUDA;
-  const Fp4Params p{(const uint8_t *)args, x, sx, w, sw, rx, rw, (__nv_bfloat16 *)out, row_map, map_limit,
-                    row_weight, M, K, N, E, (N + kBn - 1) / kBn};
-  const int64_t upper = ((M + 127) / 128 + (M < E ? M : E)) * p.n_tiles;
-  const unsigned grid = (unsigned)(upper < sms * 4 ? upper : sms * 4);
-  return launch_pdl(fmt == MGEMM_NVFP4 ? fp4_gemm_kernel<MGEMM_NVFP4> : fp4_gemm_kernel<MGEMM_MXFP4>, dim3(grid),
-                    dim3(256), 0, (cudaStream_t)stream, 1, "mgemm_fwd_fp4 launch", p);
+  Fp4Params p{};
+  p.args = (const uint8_t *)args;
+  p.rx = rx;
+  p.rw = rw;
+  p.out = (__nv_bfloat16 *)out;
+  p.row_map = row_map;
+  p.map_limit = map_limit;
+  p.row_weight = row_weight;
+  p.K = K;
+  p.N = N;
+  p.E = E;
+  return fmt == MGEMM_NVFP4 ? launch_fp4<MGEMM_NVFP4>(x, sx, w, sw, p, M, sms, (cudaStream_t)stream)
+                            : launch_fp4<MGEMM_MXFP4>(x, sx, w, sw, p, M, sms, (cudaStream_t)stream);
 }
 
 extern "C" int64_t mgemm_gmm_fp4_workspace_bytes(int fmt, int64_t M, int K, int E) {
