@@ -171,12 +171,12 @@ def lib():
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(t=None):
-    dev = t.device if t is not None else None
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    # (torch.cuda.current_stream builds a Stream object; this is its handle alone)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if t is None else t.get_device())
 
 
 def _check(rc, what):
@@ -462,8 +462,7 @@ def mgemm_route(logits, bias, top_k, scoring, n_group, topk_group, group_top, re
     _cuda(logits, bias, topk_weights, topk_ids)
     T, E = logits.shape
     _check(lib().mgemm_route(_p(logits), int(logits.dtype == torch.bfloat16), logits.stride(0), _p(bias), T, E,
-                             int(top_k), int(scoring), int(n_group), int(topk_group), int(group_top),
-                             int(bool(renormalize)), float(scale), _p(topk_weights), _p(topk_ids), _stream(logits)),
+                             top_k, scoring, n_group, topk_group, group_top, bool(renormalize), scale, _p(topk_weights), _p(topk_ids), _stream(logits)),
            "mgemm_route")
 
 
@@ -524,8 +523,8 @@ def mgemm_gmm_fp4_workspace_bytes(fmt, M, K, E):
 def mgemm_gmm_fp4(group_sizes, E, fmt, x, w, sw, rw, out, M, K, N, workspace):
     """fill + cast of the token rows + grouped product; workspace uint8 (mgemm_gmm_fp4_workspace_bytes)."""
     _cuda(group_sizes, x, w, sw, rw, out, workspace)
-    _check(lib().mgemm_gmm_fp4(_p(group_sizes), int(E), int(fmt), _p(x), x.stride(0), _p(w), _p(sw), _p(rw), _p(out),
-                               int(M), int(K), int(N), _p(workspace), workspace.numel(), _stream(out)),
+    _check(lib().mgemm_gmm_fp4(_p(group_sizes), E, fmt, _p(x), x.stride(0), _p(w), _p(sw), _p(rw), _p(out),
+                               M, K, N, _p(workspace), workspace.numel(), _stream(out)),
            "mgemm_gmm_fp4")
 
 

@@ -6,9 +6,12 @@
 //   NVFP4  R = 2^floor(log2(2688 / row amax)),  b = e4m3(amax16 R / 6),
 //          code = e2m1(x R / b)
 //
-// Memory-bound: 2 bytes read and about 0.55 written per element.  One warp per
-// row; a lane takes whole blocks.  NVFP4 needs the row's maximum before its
-// first code, so the row is read twice, the second time from cache.
+// Memory-bound: 2 bytes read and about 0.55 written per element.  A thread
+// takes whole blocks, and 32 threads a row, or 256 where there are few rows
+// (a row of 5120 on one warp alone takes 6 us).  NVFP4 needs the row's maximum
+// before its first code, so the thread's blocks stay in registers as they were
+// read (up to NB of them; longer rows are read twice, the second time from
+// cache).  Four threads' scale bytes make a word.
 #include "fp4.cuh"
 
 namespace mgemm {
@@ -25,111 +28,202 @@ struct QuantSource {
   const int32_t *ids;
   int64_t numel, in_rows;
   int top_k, gated;
+  bool vec32;  // rows start on 32-byte boundaries
 };
 
-// One row's elements c .. c + 7 as floats (bf16 values).
+// One row's elements c .. c + 15 as they are cast: 8 pairs of bf16.
 struct RowReader {
   const __nv_bfloat16 *row;  // nullptr: a row of zeros
   const __nv_bfloat16 *up;   // gated rows: the second half
-  __device__ __forceinline__ void load8(int c, float (&v)[8]) const {
+  bool vec32;                // rows start on 32-byte boundaries
+  __device__ __forceinline__ void load16(const __nv_bfloat16 *p, uint32_t (&v)[8]) const {
+    if (vec32) {
+      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                   : "l"(p));
+    } else {
+      const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p)), b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+  }
+  __device__ __forceinline__ void load(int c, uint32_t (&v)[8]) const {
     if (!row) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int i = 0; i < 8; ++i) v[i] = 0u;
       return;
     }
-    const uint4 a = *reinterpret_cast<const uint4 *>(row + c);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_lo(w[i]);
-      v[2 * i + 1] = bf16_hi(w[i]);
-    }
+    load16(row + c, v);
     if (!up) return;
-    const uint4 b = *reinterpret_cast<const uint4 *>(up + c);
-    const uint32_t u[4] = {b.x, b.y, b.z, b.w};
+    uint32_t u[8];
+    load16(up + c, u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       // as mgemm_silu_and_mul: fp32, rounded to bf16 once
-      v[2 * i] = __bfloat162float(__float2bfloat16_rn(v[2 * i] / (1.f + expf(-v[2 * i])) * bf16_lo(u[i])));
-      v[2 * i + 1] = __bfloat162float(__float2bfloat16_rn(v[2 * i + 1] / (1.f + expf(-v[2 * i + 1])) * bf16_hi(u[i])));
+      const float g0 = bf16_lo(v[i]), g1 = bf16_hi(v[i]);
+      __nv_bfloat162 h = __floats2bfloat162_rn(g0 / (1.f + expf(-g0)) * bf16_lo(u[i]), g1 / (1.f + expf(-g1)) * bf16_hi(u[i]));
+      v[i] = *reinterpret_cast<uint32_t *>(&h);
     }
   }
 };
 
-template <int FMT>
-__device__ __forceinline__ void quant_row(const RowReader &rd, int K, int64_t tile_row, int W, uint32_t *codes,
-                                          uint8_t *sf, float *row_scale, int lane) {
+// Magnitude maximum of 16 bf16 (a NaN is passed over).
+__device__ __forceinline__ float amax16(const uint32_t (&v)[8]) {
+  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v[0]));
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v[i])));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+// A row by TPR threads (tid of them), NB blocks each at a time: block q is held
+// by thread q % TPR.
+template <int FMT, int NB, int TPR>
+struct RowCast {
   using F = Fp4<FMT>;
-  constexpr int U = F::BLOCK / 8;
-  float R = 1.f;
-  if (F::NV) {
-    float a = 0.f;
-    for (int c = lane * 8; c < K; c += 256) {
-      float v[8];
-      rd.load8(c, v);
+  static constexpr int P = F::BLOCK / 16;  // 16-element pieces of a block
+  uint32_t v[NB][P][8];
+  float amax[NB];
+
+  __device__ __forceinline__ void load(const RowReader &rd, int q0, int nblk, int tid) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
+    for (int i = 0; i < NB; ++i) {
+      const int q = q0 + i * TPR + tid;
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        if (q < nblk) {
+          rd.load(q * F::BLOCK + k * 16, v[i][k]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][k][j] = 0u;
+        }
+      }
     }
-    R = fp4_pow2_scale(kNvfp4RowMax, warp_max(a));
-    if (lane == 0) *row_scale = R;
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      amax[i] = amax16(v[i][0]);
+      if (P > 1) amax[i] = fmaxf(amax[i], amax16(v[i][P - 1]));
+    }
   }
-  for (int q = lane; q < 4 * W; q += 32) {
-    uint8_t *byte = sf + fp4_sf_offset(tile_row, q >> 2, W) + (q & 3);
-    if (q * F::BLOCK >= K) {  // past the row: an empty block of its last word
-      *byte = 0;
-      continue;
-    }
-    float v[U][8], a = 0.f;
+  __device__ __forceinline__ float most() const {
+    float a = amax[0];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rd.load8(q * F::BLOCK + u * 8, v[u]);
+    for (int i = 1; i < NB; ++i) a = fmaxf(a, amax[i]);
+    return a;
+  }
+  // codes and scale bytes of the blocks held (R: the row's power of two and its inverse, NVFP4)
+  __device__ __forceinline__ void store(int q0, int nblk, int W, float R, float Rinv, int64_t tile_row, uint8_t *codes,
+                                        uint8_t *sf, int tid) const {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[u][i]));
-    }
-    uint32_t code;
-    float s, r;
-    if (F::NV) {
-      code = (uint32_t)(cvt_e4m3x2(__fdiv_rn(a * R, 6.f), 0.f) & 0xFFu);
-      s = __fdiv_rn(e4m3_value(code), R);  // exact: R is a power of two
-      r = code ? __frcp_rn(s) : 0.f;
-    } else {
-      const float m = fp4_pow2_scale(kMxfp4Max, a);
-      code = 254u - (__float_as_uint(m) >> 23);
-      r = m;
-      s = 0.f;
-    }
-    *byte = (uint8_t)code;
+    for (int i = 0; i < NB; ++i) {
+      const int qw = q0 + i * TPR;  // uniform over the row's threads
+      if (qw >= 4 * W) break;
+      const int q = qw + tid;
+      uint32_t byte;
+      uint64_t ns = 0, r;
+      if (F::NV) {
+        byte = (uint32_t)(cvt_e4m3x2(__fdiv_rn(amax[i] * R, 6.f), 0.f) & 0xFFu);
+        const float s = e4m3_value(byte) * Rinv;  // exact
+        const float rc = byte ? __frcp_rn(s) : 0.f;
+        ns = pack_f32x2(-s, -s);
+        r = pack_f32x2(rc, rc);
+      } else {
+        const float s = fp4_pow2_scale(kMxfp4Max, amax[i]);
+        byte = 254u - (__float_as_uint(s) >> 23);
+        r = pack_f32x2(s, s);
+      }
+      uint32_t word = q < nblk ? byte << (8 * (q & 3)) : 0u;  // an empty block past the row
+      word |= __shfl_xor_sync(0xffffffffu, word, 1);
+      word |= __shfl_xor_sync(0xffffffffu, word, 2);
+      if ((q & 3) == 0 && q < 4 * W) *reinterpret_cast<uint32_t *>(sf + fp4_sf_offset(tile_row, q >> 2, W)) = word;
+      if (q < nblk) {
+        uint32_t out[2 * P];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float y[8];
+        for (int k = 0; k < 2 * P; ++k) {
+          float y[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = F::NV ? (code ? fp4_quotient(v[u][i], s, r) : 0.f) : v[u][i] * r;
-      codes[(q * F::BLOCK + u * 8) >> 3] = cvt_e2m1x8(y);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t b = v[i][k / 2][(k & 1) * 4 + j];
+            const uint64_t x = pack_f32x2(bf16_lo(b), bf16_hi(b));
+            const uint64_t t = F::NV ? fp4_quotient2(x, ns, r) : fp4_mul2(x, r);
+            y[2 * j] = __uint_as_float((uint32_t)t);
+            y[2 * j + 1] = __uint_as_float((uint32_t)(t >> 32));
+          }
+          out[k] = cvt_e2m1x8(y);
+        }
+        uint8_t *dst = codes + q * (F::BLOCK / 2);
+        if (P == 1)
+          *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0], out[1]);
+        else
+          *reinterpret_cast<uint4 *>(dst) = make_uint4(out[0], out[1], out[2 * P - 2], out[2 * P - 1]);
+      }
     }
+  }
+};
+
+constexpr int kQuantThreads = 256;
+
+// The largest of a over the TPR threads of a row (every one of them).
+template <int TPR>
+__device__ __forceinline__ float row_max(float a, float *sh) {
+  a = warp_max(a);
+  if (TPR == 32) return a;
+  __syncthreads();  // the last row's values are read
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = a;
+  __syncthreads();
+  a = sh[0];
+#pragma unroll
+  for (int i = 1; i < TPR / 32; ++i) a = fmaxf(a, sh[i]);
+  return a;
+}
+
+template <int FMT, int NB, int TPR>
+__device__ __forceinline__ void cast_row(const RowReader &rd, int K, int64_t tile_row, int W, uint8_t *codes, uint8_t *sf,
+                                         float *row_scale, int tid, float *sh) {
+  using F = Fp4<FMT>;
+  const int nblk = K / F::BLOCK;
+  RowCast<FMT, NB, TPR> c;
+  float R = 1.f, Rinv = 1.f;
+  const bool once = nblk <= NB * TPR;  // the whole row is held
+  c.load(rd, 0, nblk, tid);
+  if (F::NV) {
+    float a = c.most();
+    for (int q0 = NB * TPR; q0 < nblk; q0 += NB * TPR) {
+      c.load(rd, q0, nblk, tid);
+      a = fmaxf(a, c.most());
+    }
+    R = fp4_pow2_scale(kNvfp4RowMax, row_max<TPR>(a, sh));
+    Rinv = __frcp_rn(R);  // a power of two
+    if (tid == 0) *row_scale = R;
+    if (!once) c.load(rd, 0, nblk, tid);
+  }
+  c.store(0, nblk, W, R, Rinv, tile_row, codes, sf, tid);
+  for (int q0 = NB * TPR; q0 < 4 * W; q0 += NB * TPR) {
+    c.load(rd, q0, nblk, tid);
+    c.store(q0, nblk, W, R, Rinv, tile_row, codes, sf, tid);
   }
 }
 
-template <int FMT>
-__global__ void __launch_bounds__(256)
+template <int FMT, int NB, int TPR>
+__global__ void __launch_bounds__(kQuantThreads)
     quant_fp4_kernel(const QuantSource S, int K, uint8_t *__restrict__ codes, uint8_t *__restrict__ sf,
                      float *__restrict__ row_scale) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  const int64_t w0 = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  __shared__ float sh[kQuantThreads / 32];
+  constexpr int kRows = kQuantThreads / TPR;  // rows of a CTA at a time
+  const int lane = threadIdx.x & 31, tid = threadIdx.x % TPR;
+  const int64_t step = (int64_t)gridDim.x * kRows, first = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
   const int W = fp4_words(FMT, K);
   if (!S.args) {
     const int64_t npad = (S.N + 127) / 128 * 128;
-    for (int64_t i = w0; i < S.E * npad; i += nwarps) {
+    for (int64_t i = first; i < S.E * npad; i += step) {
       const int64_t e = i / npad, n = i - e * npad;
       if (n >= S.N) {  // scale rows that fill up the group's last tile
-        for (int j = lane; j < W; j += 32) *reinterpret_cast<uint32_t *>(sf + fp4_sf_offset(i, j, W)) = 0u;
+        for (int j = tid; j < W; j += TPR) *reinterpret_cast<uint32_t *>(sf + fp4_sf_offset(i, j, W)) = 0u;
         continue;
       }
       const int64_t row = e * S.N + n;
-      const RowReader rd{S.in + row * S.ld, nullptr};
-      quant_row<FMT>(rd, K, i, W, reinterpret_cast<uint32_t *>(codes + row * (K / 2)), sf, row_scale + row, lane);
+      const RowReader rd{S.in + row * S.ld, nullptr, S.vec32};
+      cast_row<FMT, NB, TPR>(rd, K, i, W, codes + row * (K / 2), sf, row_scale + row, tid, sh);
     }
     return;
   }
@@ -137,13 +231,13 @@ __global__ void __launch_bounds__(256)
   if (*av.status != 0) return;
   const int64_t total = __ldg(av.offsets + S.E);
   const int64_t rows = total < S.M ? total : S.M;
-  for (int64_t i = w0; i < rows; i += nwarps) {
+  for (int64_t i = first; i < rows; i += step) {
     // the group of row i: as many groups end at or before it
     int e = 0;
     for (int j = lane; j < S.E; j += 32) e += __ldg(av.offsets + j + 1) <= i;
     e = __reduce_add_sync(0xffffffffu, e);
     const int64_t tile_row = __ldg(av.poffsets + e) + (i - __ldg(av.offsets + e));
-    RowReader rd{nullptr, nullptr};
+    RowReader rd{nullptr, nullptr, S.vec32};
     if (S.ids) {
       const int32_t id = __ldg(S.ids + i);
       if (id >= 0 && id < S.numel && id / S.top_k < S.in_rows) rd.row = S.in + (int64_t)(id / S.top_k) * S.ld;
@@ -151,12 +245,34 @@ __global__ void __launch_bounds__(256)
       rd.row = S.in + i * S.ld;
       if (S.gated) rd.up = rd.row + K;
     }
-    quant_row<FMT>(rd, K, tile_row, W, reinterpret_cast<uint32_t *>(codes + i * (K / 2)), sf, row_scale + i, lane);
+    cast_row<FMT, NB, TPR>(rd, K, tile_row, W, codes + i * (K / 2), sf, row_scale + i, tid, sh);
   }
 }
 
 constexpr float kBf16Max = 3.38953139e38f;  // (2 - 2^-7) 2^127
 
+// Four e2m1 codes (16 bits) -> four bf16 in two words: the value's two bytes
+// from eight-entry tables by the code's low three bits, the sign from its top bit.
+__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint2 e2m1x4_to_bf16(uint32_t c) {
+  // 0 .. 6 in bf16: 0000 3F00 3F80 3FC0 4000 4040 4080 40C0
+  const uint32_t sel = c & 0x7777u;
+  const uint32_t hi = byte_perm(0x3F3F3F00u, 0x40404040u, sel), lo = byte_perm(0xC0800000u, 0xC0804000u, sel);
+  uint32_t a = byte_perm(lo, hi, 0x5140u), b = byte_perm(lo, hi, 0x7362u);
+  a |= ((c << 12) & 0x8000u) | ((c << 24) & 0x80000000u);
+  b |= ((c << 4) & 0x8000u) | ((c << 16) & 0x80000000u);
+  return make_uint2(a, b);
+}
+
+constexpr int kDequantUnroll = 4;
+
+// A warp per row, 8 elements per lane and step, kDequantUnroll steps' loads
+// ahead of their stores.  A block's factor b / R (2^(byte - 127)) has at most 4
+// significant bits, so code times factor is exact in bf16.
 template <int FMT>
 __global__ void __launch_bounds__(256)
     dequant_fp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ sf,
@@ -167,29 +283,39 @@ __global__ void __launch_bounds__(256)
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  const int W = fp4_words(FMT, K);
+  const int W = fp4_words(FMT, K), units = K / 8;
   const int64_t npad = (N + 127) / 128 * 128;
   for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < E * N; i += nwarps) {
     const int64_t e = i / N, tile_row = e * npad + (i - e * N);
-    const float inv = F::NV ? __fdiv_rn(1.f, __ldg(row_scale + i)) : 1.f;
+    const float inv = F::NV ? __frcp_rn(__ldg(row_scale + i)) : 1.f;
     const uint32_t *src = reinterpret_cast<const uint32_t *>(codes + i * (K / 2));
-    for (int c = lane; c < K / 8; c += 32) {
-      const uint32_t w = __ldg(src + c);
-      const int q = c * 8 / F::BLOCK;
-      const uint32_t byte = sf[fp4_sf_offset(tile_row, q >> 2, W) + (q & 3)];
-      const float s = F::NV ? e4m3_value(byte) : e8m0_value(byte);
-      // a cast can round the largest bf16 values up past bf16's range: they stay at its end
-      auto value = [&](uint32_t code) {
-        const float v = e2m1_value(code & 15u) * s * inv;
-        return fminf(fmaxf(v, -kBf16Max), kBf16Max);
-      };
-      uint32_t o[4];
+    const uint8_t *sfr = sf + fp4_sf_offset(tile_row, 0, W);
+    for (int c0 = lane; c0 < units; c0 += 32 * kDequantUnroll) {
+      uint32_t w[kDequantUnroll], byte[kDequantUnroll];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        __nv_bfloat162 h = __floats2bfloat162_rn(value(w >> (8 * k)), value(w >> (8 * k + 4)));
-        o[k] = *reinterpret_cast<uint32_t *>(&h);
+      for (int u = 0; u < kDequantUnroll; ++u) {
+        const int c = c0 + 32 * u, q = c * 8 / F::BLOCK;
+        w[u] = c < units ? __ldg(src + c) : 0u;
+        byte[u] = c < units ? __ldg(sfr + (int64_t)(q >> 2) * 512 + (q & 3)) : 0u;
       }
-      *reinterpret_cast<uint4 *>(out + i * ld + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+      for (int u = 0; u < kDequantUnroll; ++u) {
+        const int c = c0 + 32 * u;
+        if (c >= units) break;
+        const __nv_bfloat162 s = __float2bfloat162_rn(F::NV ? e4m3_value(byte[u]) * inv : e8m0_value(byte[u]));
+        // a cast can round the largest bf16 values up past bf16's range: they stay at its end
+        const __nv_bfloat162 top = __float2bfloat162_rn(kBf16Max), bottom = __float2bfloat162_rn(-kBf16Max);
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint2 v = e2m1x4_to_bf16(w[u] >> (16 * k));
+          const __nv_bfloat162 a = __hmax2(__hmin2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x), s), top), bottom);
+          const __nv_bfloat162 b = __hmax2(__hmin2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y), s), top), bottom);
+          o[2 * k] = *reinterpret_cast<const uint32_t *>(&a);
+          o[2 * k + 1] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(out + i * ld + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
 }
@@ -202,6 +328,27 @@ int rows_grid(int64_t rows) {
 }
 
 bool a16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+// rows: those of the call (device-known: at most).  A warp per row while that
+// fills the SMs with warps (4 per scheduler), else a CTA per row; NB so that the
+// row stays in registers where it can.
+template <int FMT>
+int launch_quant(QuantSource S, int64_t rows, int K, uint8_t *codes, uint8_t *sf, float *row_scale, cudaStream_t s,
+                 const char *what) {
+  const int sms = sm_count_cached();
+  if (sms <= 0) return MGEMM_ECUDA;
+  S.vec32 = ((uintptr_t)S.in & 31) == 0 && S.ld % 16 == 0 && (!S.gated || K % 16 == 0);
+  const int nblk = K / Fp4<FMT>::BLOCK;
+  const bool cta = rows < (int64_t)sms * 8 && nblk > 32;
+  const int64_t want = cta ? rows : (rows + 7) / 8, cap = (int64_t)sms * 16;
+  const unsigned grid = (unsigned)(want < cap ? want : cap);
+  constexpr int U = Fp4<FMT>::BLOCK / 16;
+  auto kernel = cta ? nblk <= 256 ? quant_fp4_kernel<FMT, 1, 256> : quant_fp4_kernel<FMT, 4 / U, 256>
+                : nblk <= 64 / U  ? quant_fp4_kernel<FMT, 2 / U, 32>
+                : nblk <= 128 / U ? quant_fp4_kernel<FMT, 4 / U, 32>
+                                  : quant_fp4_kernel<FMT, 8 / U, 32>;
+  return launch_pdl(kernel, dim3(grid), dim3(kQuantThreads), 0, s, 1, what, S, K, codes, sf, row_scale);
+}
 
 }  // namespace
 }  // namespace mgemm
@@ -220,16 +367,15 @@ extern "C" int mgemm_quant_fp4(const void *in, int E, int64_t N, int K, int64_t 
   if (E == 0 || N == 0) return MGEMM_OK;
   if (!in || !codes || !sf || (fmt == MGEMM_NVFP4 && !row_scale)) return MGEMM_EINVAL;
   if (!a16(in) || !a16(codes) || !a16(sf) || ((uintptr_t)row_scale & 3)) return MGEMM_EALIGN;
-  const int grid = rows_grid(E * ((N + 127) / 128 * 128));
-  if (grid < 0) return MGEMM_ECUDA;
   QuantSource S{};
   S.in = (const __nv_bfloat16 *)in;
   S.ld = ld_in;
   S.E = E;
   S.N = N;
-  return launch_pdl(fmt == MGEMM_NVFP4 ? quant_fp4_kernel<MGEMM_NVFP4> : quant_fp4_kernel<MGEMM_MXFP4>,
-                    dim3((unsigned)grid), dim3(256), 0, (cudaStream_t)stream, 1, "mgemm_quant_fp4 launch", S, K, codes,
-                    sf, row_scale);
+  const int64_t rows = E * ((N + 127) / 128 * 128);
+  return fmt == MGEMM_NVFP4
+             ? launch_quant<MGEMM_NVFP4>(S, rows, K, codes, sf, row_scale, (cudaStream_t)stream, "mgemm_quant_fp4 launch")
+             : launch_quant<MGEMM_MXFP4>(S, rows, K, codes, sf, row_scale, (cudaStream_t)stream, "mgemm_quant_fp4 launch");
 }
 
 extern "C" int mgemm_dequant_fp4(const uint8_t *codes, const uint8_t *sf, const float *row_scale, int E, int64_t N,
@@ -258,8 +404,6 @@ extern "C" int mgemm_quant_fp4_rows(const void *args, int E, int64_t M, const vo
   if (!args || !in || !codes || !sf || (fmt == MGEMM_NVFP4 && !row_scale)) return MGEMM_EINVAL;
   if (!a16(args) || !a16(in) || !a16(codes) || !a16(sf) || ((uintptr_t)row_scale & 3) || ((uintptr_t)sorted_ids & 3))
     return MGEMM_EALIGN;
-  const int grid = rows_grid(M);
-  if (grid < 0) return MGEMM_ECUDA;
   QuantSource S{};
   S.in = (const __nv_bfloat16 *)in;
   S.ld = ld_in;
@@ -271,7 +415,7 @@ extern "C" int mgemm_quant_fp4_rows(const void *args, int E, int64_t M, const vo
   S.in_rows = in_rows;
   S.top_k = top_k;
   S.gated = gated;
-  return launch_pdl(fmt == MGEMM_NVFP4 ? quant_fp4_kernel<MGEMM_NVFP4> : quant_fp4_kernel<MGEMM_MXFP4>,
-                    dim3((unsigned)grid), dim3(256), 0, (cudaStream_t)stream, 1, "mgemm_quant_fp4_rows launch", S, K,
-                    codes, sf, row_scale);
+  return fmt == MGEMM_NVFP4
+             ? launch_quant<MGEMM_NVFP4>(S, M, K, codes, sf, row_scale, (cudaStream_t)stream, "mgemm_quant_fp4_rows launch")
+             : launch_quant<MGEMM_MXFP4>(S, M, K, codes, sf, row_scale, (cudaStream_t)stream, "mgemm_quant_fp4_rows launch");
 }

@@ -60,14 +60,28 @@ __device__ __forceinline__ float fp4_pow2_scale(float num, float amax) {
 }
 constexpr float kMxfp4Max = 6.f, kNvfp4RowMax = 2688.f;  // 6 x 448
 
-// x / s rounded so that a quotient halfway between two e2m1 values comes out
-// as exactly that: r is 1 / s rounded, the remainder x - y s is exact in one
-// fma, and adding remainder x r makes a representable quotient exact (any
-// other quotient of a bf16 x and an s of 4 significant bits is at least 2^-9
-// of itself away from a midpoint, far more than the error left here).
-__device__ __forceinline__ float fp4_quotient(float x, float s, float r) {
-  const float y = x * r;
-  return __fmaf_rn(__fmaf_rn(-y, s, x), r, y);
+// Two quotients x / s at a time (packed fp32), rounded so that one halfway
+// between two e2m1 values comes out as exactly that: r is 1 / s rounded, the
+// remainder x - y s is exact in one fma, and adding remainder x r makes a
+// representable quotient exact (any other quotient of a bf16 x and an s of 4
+// significant bits is at least 2^-9 of itself away from a midpoint, far more
+// than the error left here).  neg_s is -s.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t fp4_mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fp4_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t fp4_quotient2(uint64_t x, uint64_t neg_s, uint64_t r) {
+  const uint64_t y = fp4_mul2(x, r);
+  return fp4_fma2(fp4_fma2(y, neg_s, x), r, y);
 }
 
 }  // namespace mgemm

@@ -10,6 +10,14 @@
 // as 32-bit order keys (order_key below): a warp maximum is then one integer
 // redux instruction, and a NaN, an expert that is off and one outside the groups
 // kept have keys of their own.
+//
+// Bound by instruction issue, not by memory: a score costs about 15
+// instructions an expert and lane, against 4 bytes read.  So a lane keeps its
+// two best experts: a choice takes a maximum over the lanes' best and promotes
+// the second, and only a lane chosen from a third time scans its experts again.
+// Where groups are whole lanes (NV divides the group, a power of two of lanes)
+// their two best come from the same pairs by shuffles; otherwise the groups are
+// scanned in turn.
 #include "common.cuh"
 
 namespace mgemm {
@@ -46,14 +54,101 @@ __device__ __forceinline__ float warp_sum(float a) {
   return a;
 }
 
+constexpr int kRouteThreads = 256;
+
 struct RouteParams {
   int64_t T, ld;
   int E, top_k, sigmoid, n_group, topk_group, group_top, renormalize;
   float scale;
+  int vec, vec_bias;     // rows of logits / the bias start on 16-byte boundaries
+  int lanes_per_group;   // whole-lane groups: a power of two
 };
 
-template <int NV, typename L>
-__global__ void __launch_bounds__(256)
+// The float of an order key of a number.
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+// N consecutive values; vec: p has the alignment of lane * N values from a 16-byte boundary.
+template <int N>
+__device__ __forceinline__ void load_values(const float *p, bool vec, float (&v)[N]) {
+  if (N % 4 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i + 3 < N; i += 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4 *>(p + i));
+      v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+    }
+  } else if (N % 2 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+      const float2 f = __ldg(reinterpret_cast<const float2 *>(p + i));
+      v[i] = f.x, v[i + 1] = f.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __ldg(p + i);
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_values(const __nv_bfloat16 *p, bool vec, float (&v)[N]) {
+  if (N % 8 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i + 7 < N; i += 8) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p + i));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[i + 2 * k] = bf16_lo(w[k]), v[i + 2 * k + 1] = bf16_hi(w[k]);
+    }
+  } else if (N % 4 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i + 3 < N; i += 4) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p + i));
+      v[i] = bf16_lo(u.x), v[i + 1] = bf16_hi(u.x), v[i + 2] = bf16_lo(u.y), v[i + 3] = bf16_hi(u.y);
+    }
+  } else if (N % 2 == 0 && vec) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+      const uint32_t u = __ldg(reinterpret_cast<const uint32_t *>(p + i));
+      v[i] = bf16_lo(u), v[i + 1] = bf16_hi(u);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __bfloat162float(p[i]);
+  }
+}
+// The lane's N values of a row of E, `fill` past its end.
+template <int N, typename L>
+__device__ __forceinline__ void load_lane(const L *row, int e0, int E, bool vec, float fill, float (&v)[N]) {
+  if (e0 + N <= E) {
+    load_values<N>(row + e0, vec, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = e0 + j < E ? load_logit(row + e0 + j) : fill;
+  }
+}
+
+// A lane's two largest keys and the places of both; equal keys: the lower place first.
+struct Best {
+  uint32_t k1, k2;
+  int j1, j2;
+};
+template <int N>
+__device__ __forceinline__ Best two_best(const uint32_t (&key)[N]) {
+  Best b{key[0], kKeyOut, 0, 0};
+#pragma unroll
+  for (int j = 1; j < N; ++j) {
+    const bool first = key[j] > b.k1, second = key[j] > b.k2;
+    b.k2 = first ? b.k1 : second ? key[j] : b.k2;
+    b.j2 = first ? b.j1 : second ? j : b.j2;
+    b.k1 = first ? key[j] : b.k1;
+    b.j1 = first ? j : b.j1;
+  }
+  return b;
+}
+
+// GROUPS: 0 none; 1 groups of p.lanes_per_group whole lanes; 2 any groups.
+template <int NV, int GROUPS, typename L>
+__global__ void __launch_bounds__(kRouteThreads)
     route_kernel(const L *__restrict__ logits, const float *__restrict__ bias, const RouteParams p,
                  float *__restrict__ weights, int32_t *__restrict__ ids) {
   pdl_wait();
@@ -61,85 +156,98 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31;
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.T) return;  // whole warps leave together
-  const L *row = logits + t * p.ld;
   const int e0 = lane * NV;
-  float s[NV];       // the scores (0 where off)
+  float s[NV];       // logits, then scores, of softmax times their sum (0 where off)
   uint32_t key[NV];  // the order of the choice
-  float m = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    s[j] = e0 + j < p.E ? load_logit(row + e0 + j) : -INFINITY;
-    m = fmaxf(m, s[j]);
-  }
-  // the group score's terms where they are not the choice's: softmax without bias, two per group
-  const bool by_exp = !p.sigmoid && !bias && p.group_top == 2;
-  float term[NV];
+  load_lane<NV>(logits + t * p.ld, e0, p.E, p.vec, -INFINITY, s);
+  float m = 0.f, sum = 1.f;
   if (p.sigmoid) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const bool off = s[j] <= MGEMM_ROUTE_MASKED;
       s[j] = off ? 0.f : sigmoidf(s[j]);
-      term[j] = bias && e0 + j < p.E ? s[j] + __ldg(bias + e0 + j) : s[j];
-      key[j] = off ? kKeyOff : order_key(term[j]);
+      key[j] = off ? kKeyOff : 2u;
     }
   } else {
+    m = s[0];
+#pragma unroll
+    for (int j = 1; j < NV; ++j) m = fmaxf(m, s[j]);
     m = warp_max(m);
     if (m <= MGEMM_ROUTE_MASKED) m = 0.f;
-    float sum = 0.f;
-    uint32_t off = 0;
+    sum = 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if (s[j] <= MGEMM_ROUTE_MASKED) off |= 1u << j;
-      term[j] = s[j];
-      s[j] = (off >> j) & 1u ? 0.f : expf(s[j] - m);
+      const bool off = s[j] <= MGEMM_ROUTE_MASKED;
+      key[j] = off ? kKeyOff : order_key(s[j]);
+      s[j] = off ? 0.f : expf(s[j] - m);
       sum += s[j];
     }
     sum = warp_sum(sum);
+    if (sum == 0.f) sum = 1.f;  // every expert is off
+  }
+  if (p.sigmoid || bias) {
+    float b[NV];
+    if (bias) load_lane<NV>(bias, e0, p.E, p.vec_bias, 0.f, b);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const float e = s[j];
-      s[j] = sum == 0.f ? 0.f : e / sum;
-      if (bias) term[j] = e0 + j < p.E ? s[j] + __ldg(bias + e0 + j) : s[j];
-      key[j] = (off >> j) & 1u ? kKeyOff : order_key(term[j]);
-      if (by_exp) term[j] = e;
+      const float c = p.sigmoid ? s[j] : s[j] / sum;
+      if (key[j] != kKeyOff) key[j] = order_key(bias ? c + b[j] : c);
     }
   }
+  if (p.E < 32 * NV) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (e0 + j >= p.E) key[j] = kKeyOut;
+    for (int j = 0; j < NV; ++j)
+      if (e0 + j >= p.E) key[j] = kKeyOut;
+  }
 
-  if (p.n_group > 1) {
-    // each group's best one or two terms over the warp; lane g % 32 keeps the
-    // score key of group g (g < 64)
+  // a group's score from its best keys: the largest, or the sum of two terms
+  // (softmax without bias: of exp(l - max))
+  const bool by_exp = !p.sigmoid && !bias;
+  auto group_score = [&](uint32_t k1, uint32_t k2) -> uint32_t {
+    if (k1 <= kKeyOff) return kKeyOff;
+    if (p.group_top == 1) return k1;
+    auto term = [&](uint32_t k) { return k <= kKeyOff ? 0.f : by_exp ? expf(key_value(k) - m) : key_value(k); };
+    return order_key(term(k1) + term(k2));
+  };
+  Best best;
+  if constexpr (GROUPS == 1) {
+    best = two_best(key);
+    uint32_t k1 = best.k1, k2 = best.k2;
+    for (int o = 1; o < p.lanes_per_group; o <<= 1) {
+      const uint32_t a = __shfl_xor_sync(kFull, k1, o), b = __shfl_xor_sync(kFull, k2, o);
+      k2 = max(min(k1, a), max(k2, b));
+      k1 = max(k1, a);
+    }
+    const uint32_t mine = group_score(k1, k2);
+    const int g = lane / p.lanes_per_group;
+    int rank = 0;
+    for (int o = 0; o < p.n_group; ++o) {
+      const uint32_t other = __shfl_sync(kFull, mine, o * p.lanes_per_group);
+      rank += other > mine || (other == mine && o < g);
+    }
+    if (rank >= p.topk_group) {  // (lanes past the groups hold no keys)
+      best.k1 = best.k2 = kKeyOut;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) key[j] = kKeyOut;
+    }
+  } else if constexpr (GROUPS == 2) {
+    // each group's best one or two keys over the warp; lane g % 32 keeps the
+    // score of group g (g < 64)
     const int gs = p.E / p.n_group;
     uint32_t gkey[2] = {kKeyOut, kKeyOut};
     for (int g = 0; g < p.n_group; ++g) {
       const int lo = g * gs, hi = lo + gs;
-      float score = 0.f;
-      uint32_t first = kKeyOff;
-      int skip = -1;  // the expert already counted
-      for (int r = 0; r < p.group_top; ++r) {
-        uint32_t bk = kKeyOut;
-        float bt = 0.f;
-        int be = 0x7FFFFFFF;
+      uint32_t k1 = kKeyOut, k2 = kKeyOut;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const int e = e0 + j;
-          const uint32_t k = e < lo || e >= hi || e == skip ? kKeyOut : key[j] == kKeyOff ? kKeyOff : order_key(term[j]);
-          if (k > bk) {
-            bk = k;
-            bt = term[j];
-            be = e;
-          }
-        }
-        const uint32_t best = __reduce_max_sync(kFull, bk);
-        const uint32_t who = __ballot_sync(kFull, bk == best);
-        const int src = __ffs(who) - 1;
-        if (best > kKeyOff) score += __shfl_sync(kFull, bt, src);
-        skip = __shfl_sync(kFull, be, src);
-        if (r == 0) first = best;
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t k = e0 + j < lo || e0 + j >= hi ? kKeyOut : key[j];
+        k2 = max(k2, min(k1, k));
+        k1 = max(k1, k);
       }
-      const uint32_t k = first <= kKeyOff ? kKeyOff : order_key(score);
+      const uint32_t first = __reduce_max_sync(kFull, k1);
+      const int src = __ffs(__ballot_sync(kFull, k1 == first)) - 1;
+      const uint32_t second = __reduce_max_sync(kFull, lane == src ? k2 : k1);
+      const uint32_t k = group_score(first, second);
       if (lane == (g & 31)) {
         if (g < 32) gkey[0] = k;
         else gkey[1] = k;
@@ -148,9 +256,8 @@ __global__ void __launch_bounds__(256)
     // the best groups, equal scores to the lower one
     uint64_t kept = 0;
     for (int r = 0; r < p.topk_group; ++r) {
-      const uint32_t bk = max(gkey[0], gkey[1]);
-      const uint32_t best = __reduce_max_sync(kFull, bk);
-      const uint32_t a = __ballot_sync(kFull, gkey[0] == best), b = __ballot_sync(kFull, gkey[1] == best);
+      const uint32_t top = __reduce_max_sync(kFull, max(gkey[0], gkey[1]));
+      const uint32_t a = __ballot_sync(kFull, gkey[0] == top), b = __ballot_sync(kFull, gkey[1] == top);
       const int g = a ? __ffs(a) - 1 : 32 + __ffs(b) - 1;
       kept |= 1ull << g;
       if (lane == (g & 31)) {
@@ -161,26 +268,24 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (e0 + j < p.E && !((kept >> ((e0 + j) / gs)) & 1ull)) key[j] = kKeyOut;
+    best = two_best(key);
+  } else {
+    best = two_best(key);
   }
 
-  // the top_k keys, largest first; lane r keeps pick r (top_k <= 32)
-  float my_s = 0.f;
+  // the top_k keys, largest first; lane r keeps the id of pick r (top_k <= 32),
+  // the lane that holds an expert marks it
   int my_id = 0;
+  float my_s = 0.f;
+  bool spare = true;  // best.k2 is the lane's second best
   for (int r = 0; r < p.top_k; ++r) {
-    uint32_t bk = kKeyOut;
-    int bj = 0;
-    float bs = 0.f;
+    const uint32_t top = __reduce_max_sync(kFull, best.k1);
+    const int src = __ffs(__ballot_sync(kFull, best.k1 == top)) - 1;
+    float sc = s[0];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (key[j] > bk) {
-        bk = key[j];
-        bj = j;
-        bs = s[j];
-      }
-    const uint32_t best = __reduce_max_sync(kFull, bk);
-    const int src = __ffs(__ballot_sync(kFull, bk == best)) - 1;
-    const int id = __shfl_sync(kFull, e0 + bj, src);
-    const float sc = __shfl_sync(kFull, bs, src);
+    for (int j = 1; j < NV; ++j) sc = best.j1 == j ? s[j] : sc;
+    const int id = __shfl_sync(kFull, e0 + best.j1, src);
+    sc = __shfl_sync(kFull, sc, src);
     if (lane == r) {
       my_id = id;
       my_s = sc;
@@ -188,12 +293,21 @@ __global__ void __launch_bounds__(256)
     if (lane == src) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (j == bj) key[j] = kKeyOut;
+        if (best.j1 == j) key[j] = kKeyOut;
+      if (spare) {
+        best.k1 = best.k2;
+        best.j1 = best.j2;
+        spare = false;
+      } else {
+        best = two_best(key);
+        spare = true;
+      }
     }
   }
+  if (!p.sigmoid) my_s /= sum;
   if (p.renormalize) {
-    const float sum = warp_sum(my_s);  // lanes past top_k hold 0
-    my_s = sum == 0.f ? 0.f : my_s / sum;
+    const float total = warp_sum(my_s);  // lanes past top_k hold 0
+    my_s = total == 0.f ? 0.f : my_s / total;
   }
   if (lane < p.top_k) {
     weights[t * p.top_k + lane] = my_s * p.scale;
@@ -205,18 +319,34 @@ struct RouteBwdParams {
   int64_t T, ld, ld_grad;
   int E, top_k, sigmoid, renormalize;
   float scale;
+  int vec, vec_grad;  // rows start on 16-byte boundaries
 };
 
 __device__ __forceinline__ void store_grad(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_grad(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// One warp per token: lane j < top_k takes pick j's coefficient; the row of
-// zeros (softmax without renormalization: of -s_e sum g w) is written first,
-// then the picks over it.
+// One 16-byte unit of gradients.
+__device__ __forceinline__ void store_unit(float *p, const float (&v)[4]) {
+  *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store_unit(__nv_bfloat16 *p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+    w[k] = *reinterpret_cast<uint32_t *>(&h);
+  }
+  *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One warp per token: lane j < top_k takes pick j's coefficient; the row's
+// other values (zeros; softmax without renormalization: -s_e sum g w) are
+// written first, then the picks over them.  Bound by the E gradients written.
 template <typename L>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kRouteThreads)
     route_bwd_kernel(const float *__restrict__ grad_w, const L *__restrict__ logits, const float *__restrict__ weights,
                      const int32_t *__restrict__ ids, const RouteBwdParams p, L *__restrict__ grad) {
+  constexpr int U = 16 / sizeof(L);  // values per 16-byte unit
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -224,6 +354,7 @@ __global__ void __launch_bounds__(256)
   if (t >= p.T) return;
   const L *row = logits ? logits + t * p.ld : nullptr;
   L *out = grad + t * p.ld_grad;
+  const bool plain = p.sigmoid || p.renormalize;  // gradients at the picks only
   float g = 0.f, w = 0.f;
   int id = -1;
   if (lane < p.top_k) {
@@ -232,6 +363,12 @@ __global__ void __launch_bounds__(256)
     id = __ldg(ids + t * p.top_k + lane);
     if (id < 0 || id >= p.E) id = -1;
   }
+  const int units = p.vec_grad ? p.E / U : 0;  // whole units, then single values
+  if (plain) {
+    float z[U] = {};
+    for (int u = lane; u < units; u += 32) store_unit(out + u * U, z);
+    for (int e = units * U + lane; e < p.E; e += 32) store_grad(out + e, 0.f);
+  }
   const float r = p.renormalize ? w / p.scale : w;
   const float f = warp_sum(id >= 0 ? g * r : 0.f);
   float d = p.renormalize ? w * (g - f) : w * g;
@@ -239,27 +376,41 @@ __global__ void __launch_bounds__(256)
     const float l = load_logit(row + id);
     d *= l <= MGEMM_ROUTE_MASKED ? 0.5f : 1.f / (1.f + expf(l));  // 1 - s; w is 0 where the expert is off
   }
-  if (p.sigmoid || p.renormalize) {
-    for (int e = lane; e < p.E; e += 32) store_grad(out + e, 0.f);
-    __syncwarp();
-    if (id >= 0) store_grad(out + id, d);
-    return;
+  if (!plain) {  // every expert's probability is needed
+    float m = -INFINITY, sum = 0.f;
+    const bool vec = p.vec && p.vec_grad;
+    const int n = vec ? units : 0;
+    for (int u = lane; u < n; u += 32) {
+      float v[U];
+      load_values<U>(row + u * U, true, v);
+#pragma unroll
+      for (int i = 0; i < U; ++i) m = fmaxf(m, v[i]);
+    }
+    for (int e = n * U + lane; e < p.E; e += 32) m = fmaxf(m, load_logit(row + e));
+    m = warp_max(m);
+    if (m <= MGEMM_ROUTE_MASKED) m = 0.f;
+    auto term = [&](float l) { return l <= MGEMM_ROUTE_MASKED ? 0.f : expf(l - m); };
+    for (int u = lane; u < n; u += 32) {
+      float v[U];
+      load_values<U>(row + u * U, true, v);
+#pragma unroll
+      for (int i = 0; i < U; ++i) sum += term(v[i]);
+    }
+    for (int e = n * U + lane; e < p.E; e += 32) sum += term(load_logit(row + e));
+    sum = warp_sum(sum);
+    const float c = sum == 0.f ? 0.f : -f / sum;
+    for (int u = lane; u < n; u += 32) {
+      float v[U];
+      load_values<U>(row + u * U, true, v);
+#pragma unroll
+      for (int i = 0; i < U; ++i) v[i] = term(v[i]) * c;
+      store_unit(out + u * U, v);
+    }
+    for (int e = n * U + lane; e < p.E; e += 32) store_grad(out + e, term(load_logit(row + e)) * c);
+    if (id >= 0) d += term(load_logit(row + id)) * c;
   }
-  // softmax, raw weights: every expert's probability is needed
-  float m = -INFINITY;
-  for (int e = lane; e < p.E; e += 32) m = fmaxf(m, load_logit(row + e));
-  m = warp_max(m);
-  if (m <= MGEMM_ROUTE_MASKED) m = 0.f;
-  float sum = 0.f;
-  for (int e = lane; e < p.E; e += 32) {
-    const float l = load_logit(row + e);
-    sum += l <= MGEMM_ROUTE_MASKED ? 0.f : expf(l - m);
-  }
-  sum = warp_sum(sum);
-  auto prob = [&](float l) { return l <= MGEMM_ROUTE_MASKED || sum == 0.f ? 0.f : expf(l - m) / sum; };
-  for (int e = lane; e < p.E; e += 32) store_grad(out + e, -prob(load_logit(row + e)) * f);
   __syncwarp();
-  if (id >= 0) store_grad(out + id, d - prob(load_logit(row + id)) * f);
+  if (id >= 0) store_grad(out + id, d);
 }
 
 bool route_sizes_ok(int64_t T, int E, int top_k, int64_t ld) {
@@ -268,20 +419,47 @@ bool route_sizes_ok(int64_t T, int E, int top_k, int64_t ld) {
 }
 
 template <typename L>
-int launch_route(const void *logits, const float *bias, const RouteParams &p, float *weights, int32_t *ids,
-                 cudaStream_t s) {
-  const unsigned blocks = (unsigned)((p.T + 7) / 8);
-  const int nv = (p.E + 31) / 32;
-#define MGEMM_ROUTE_LAUNCH(NV)                                                                                  \
-  return launch_pdl(route_kernel<NV, L>, dim3(blocks), dim3(256), 0, s, 1, "mgemm_route launch", (const L *)logits, \
-                    bias, p, weights, ids)
-  if (nv <= 1) MGEMM_ROUTE_LAUNCH(1);
-  if (nv <= 2) MGEMM_ROUTE_LAUNCH(2);
-  if (nv <= 4) MGEMM_ROUTE_LAUNCH(4);
-  if (nv <= 8) MGEMM_ROUTE_LAUNCH(8);
-  if (nv <= 16) MGEMM_ROUTE_LAUNCH(16);
+int launch_route(const void *logits, const float *bias, RouteParams p, float *weights, int32_t *ids, cudaStream_t s) {
+  const int warps = kRouteThreads / 32;
+  const unsigned blocks = (unsigned)((p.T + warps - 1) / warps);
+  p.vec = ((uintptr_t)logits & 15) == 0 && p.ld * (int64_t)sizeof(L) % 16 == 0;
+  p.vec_bias = ((uintptr_t)bias & 15) == 0;
+  const int nv = (p.E + 31) / 32, gs = p.E / p.n_group;
+  // experts per lane: the fewest that are compiled, and for groups of whole lanes the fewest of
+  // those that divide a group into a power of two of lanes
+  static constexpr int kNv[] = {1, 2, 3, 4, 5, 6, 8, 12, 16, 32};
+  int pick = 0, groups = 0;
+  for (int c : kNv) {
+    if (c < nv) continue;
+    if (!pick) pick = c;
+    const int lanes = gs / c;
+    if (p.n_group > 1 && gs % c == 0 && (lanes & (lanes - 1)) == 0) {
+      pick = c;
+      groups = 1;
+      p.lanes_per_group = lanes;
+      break;
+    }
+  }
+  if (p.n_group > 1 && !groups) groups = 2;
+#define MGEMM_ROUTE_LAUNCH(NV)                                                                                       \
+  if (pick == NV)                                                                                                    \
+  return launch_pdl(groups == 0   ? route_kernel<NV, 0, L>                                                           \
+                    : groups == 1 ? route_kernel<NV, 1, L>                                                           \
+                                  : route_kernel<NV, 2, L>,                                                          \
+                    dim3(blocks), dim3(kRouteThreads), 0, s, 1, "mgemm_route launch", (const L *)logits, bias, p,     \
+                    weights, ids)
+  MGEMM_ROUTE_LAUNCH(1);
+  MGEMM_ROUTE_LAUNCH(2);
+  MGEMM_ROUTE_LAUNCH(3);
+  MGEMM_ROUTE_LAUNCH(4);
+  MGEMM_ROUTE_LAUNCH(5);
+  MGEMM_ROUTE_LAUNCH(6);
+  MGEMM_ROUTE_LAUNCH(8);
+  MGEMM_ROUTE_LAUNCH(12);
+  MGEMM_ROUTE_LAUNCH(16);
   MGEMM_ROUTE_LAUNCH(32);
 #undef MGEMM_ROUTE_LAUNCH
+  return MGEMM_EINVAL;
 }
 
 }  // namespace
@@ -302,7 +480,7 @@ extern "C" int mgemm_route(const void *logits, int logits_bf16, int64_t ld, cons
   if (((uintptr_t)logits & (logits_bf16 ? 1 : 3)) || ((uintptr_t)bias & 3) || ((uintptr_t)topk_weights & 3) ||
       ((uintptr_t)topk_ids & 3))
     return MGEMM_EALIGN;
-  const RouteParams p{T, ld, E, top_k, scoring == MGEMM_SCORE_SIGMOID, n_group, topk_group, group_top, renormalize, scale};
+  const RouteParams p{T, ld, E, top_k, scoring == MGEMM_SCORE_SIGMOID, n_group, topk_group, group_top, renormalize, scale, 0, 0, 0};
   cudaStream_t s = (cudaStream_t)stream;
   return logits_bf16 ? launch_route<__nv_bfloat16>(logits, bias, p, topk_weights, topk_ids, s)
                      : launch_route<float>(logits, bias, p, topk_weights, topk_ids, s);
@@ -321,7 +499,10 @@ extern "C" int mgemm_route_bwd(const float *grad_weights, const void *logits, in
   if (((uintptr_t)logits & (logits_bf16 ? 1 : 3)) || ((uintptr_t)grad_logits & (logits_bf16 ? 1 : 3)) ||
       ((uintptr_t)grad_weights & 3) || ((uintptr_t)topk_weights & 3) || ((uintptr_t)topk_ids & 3))
     return MGEMM_EALIGN;
-  const RouteBwdParams p{T, ld, ld_grad, E, top_k, scoring == MGEMM_SCORE_SIGMOID, renormalize, scale};
+  const int es = logits_bf16 ? 2 : 4;
+  const RouteBwdParams p{T, ld, ld_grad, E, top_k, scoring == MGEMM_SCORE_SIGMOID, renormalize, scale,
+                         ((uintptr_t)logits & 15) == 0 && ld * es % 16 == 0,
+                         ((uintptr_t)grad_logits & 15) == 0 && ld_grad * es % 16 == 0};
   const unsigned blocks = (unsigned)((T + 7) / 8);
   cudaStream_t s = (cudaStream_t)stream;
   if (logits_bf16)

@@ -11,6 +11,8 @@ This module only allocates outputs with torch and calls the binding; every
 step runs in the CUDA library.
 """
 
+import functools
+
 import torch
 
 from . import binding as B
@@ -18,10 +20,15 @@ from . import binding as B
 FORMATS = {"mxfp4": B.MGEMM_MXFP4, "nvfp4": B.MGEMM_NVFP4}
 
 
+_scale_bytes = functools.lru_cache(maxsize=4096)(B.mgemm_fp4_scale_bytes)
+_workspace_bytes = functools.lru_cache(maxsize=4096)(B.mgemm_gmm_fp4_workspace_bytes)
+
+
 def _format(fmt):
-    if fmt not in FORMATS:
+    code = FORMATS.get(fmt)
+    if code is None:
         raise B.MgemmError(f"unknown 4-bit format {fmt!r} (one of {', '.join(FORMATS)})")
-    return FORMATS[fmt]
+    return code
 
 
 class Fp4Tensor:
@@ -39,7 +46,7 @@ class Fp4Tensor:
         self.shape = (E, N, 2 * half)
         if not codes.is_contiguous() or not scales.is_contiguous():
             raise B.MgemmError("Fp4Tensor takes contiguous codes and scales")
-        if scales.numel() != E * B.mgemm_fp4_scale_bytes(self.code, N, 2 * half):
+        if scales.numel() != E * _scale_bytes(self.code, N, 2 * half):
             raise B.MgemmError(f"Fp4Tensor: {scales.numel()} scale bytes do not fit codes {tuple(codes.shape)}")
         if fmt == "nvfp4":
             if row_scale is None or row_scale.dtype != torch.float32 or row_scale.numel() != E * N or \
@@ -48,6 +55,13 @@ class Fp4Tensor:
         elif row_scale is not None:
             raise B.MgemmError("mxfp4 has no row scales")
         self.codes, self.scales, self.row_scale, self.fmt = codes, scales, row_scale, fmt
+
+    @classmethod
+    def _of(cls, codes, scales, row_scale, fmt, code, shape):
+        """Of parts laid out here (nothing to check)."""
+        q = cls.__new__(cls)
+        q.codes, q.scales, q.row_scale, q.fmt, q.code, q.shape = codes, scales, row_scale, fmt, code, shape
+        return q
 
 
 def quantize_fp4(x, fmt):
@@ -60,11 +74,12 @@ def quantize_fp4(x, fmt):
     if x.stride(2) != 1 or x.stride(1) % 8 or x.stride(1) < K or x.data_ptr() % 16 or \
             (E > 1 and x.stride(0) != N * x.stride(1)):
         x = x.contiguous()
-    codes = torch.empty(E, N, K // 2, dtype=torch.uint8, device=x.device)
-    scales = torch.empty(max(0, E * B.mgemm_fp4_scale_bytes(code, N, K)), dtype=torch.uint8, device=x.device)
-    rows = torch.empty(E, N, dtype=torch.float32, device=x.device) if fmt == "nvfp4" else None
+    dev = x.device
+    codes = torch.empty((E, N, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty(E * _scale_bytes(code, N, K), dtype=torch.uint8, device=dev)
+    rows = torch.empty((E, N), dtype=torch.float32, device=dev) if fmt == "nvfp4" else None
     B.mgemm_quant_fp4(x, code, codes, scales, rows)
-    return Fp4Tensor(codes, scales, rows, fmt)
+    return Fp4Tensor._of(codes, scales, rows, fmt, code, (E, N, K))
 
 
 def dequantize_fp4(q):
@@ -95,10 +110,10 @@ def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
     if x.stride(1) != 1 or x.stride(0) % 8 or x.stride(0) < K or x.data_ptr() % 16:
         x = x.contiguous()
     if out is None:
-        out = torch.empty(M, N, dtype=torch.bfloat16, device=x.device)
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
     elif out.dtype != torch.bfloat16 or out.shape != (M, N) or not out.is_contiguous():
         raise B.MgemmError("gmm_fp4: out must be contiguous bf16 [M, N]")
     if workspace is None:
-        workspace = torch.empty(B.mgemm_gmm_fp4_workspace_bytes(w.code, M, K, E), dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(_workspace_bytes(w.code, M, K, E), dtype=torch.uint8, device=x.device)
     B.mgemm_gmm_fp4(group_sizes, E, w.code, x, w.codes, w.scales, w.row_scale, out, M, K, N, workspace)
     return out

@@ -79,9 +79,10 @@ SCORES = {"softmax": B.MGEMM_SCORE_SOFTMAX, "sigmoid": B.MGEMM_SCORE_SIGMOID}
 def _route_logits(logits, scoring):
     if scoring not in SCORES:
         raise B.MgemmError(f"unknown scoring {scoring!r} (one of {', '.join(SCORES)})")
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+    if logits.dim() != 2 or (logits.dtype != torch.float32 and logits.dtype != torch.bfloat16):
         raise B.MgemmError("routing takes float32 or bf16 logits [T, E]")
-    return logits if logits.stride(1) == 1 and logits.stride(0) >= logits.shape[1] else logits.contiguous()
+    ld, unit = logits.stride()
+    return logits if unit == 1 and ld >= logits.shape[1] else logits.contiguous()
 
 
 def route_experts(logits, topk, scoring="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renormalize=True,
@@ -97,9 +98,9 @@ def route_experts(logits, topk, scoring="softmax", bias=None, n_group=1, topk_gr
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != logits.shape[1] or
                              not bias.is_contiguous()):
         raise B.MgemmError("the routing bias is a contiguous float32 [E]")
-    T = logits.shape[0]
-    w = torch.empty(T, topk, dtype=torch.float32, device=logits.device)
-    ids = torch.empty(T, topk, dtype=torch.int32, device=logits.device)
+    shape, dev = (logits.shape[0], topk), logits.device
+    w = torch.empty(shape, dtype=torch.float32, device=dev)
+    ids = torch.empty(shape, dtype=torch.int32, device=dev)
     B.mgemm_route(logits, bias, topk, SCORES[scoring], n_group, topk_group, group_top, renormalize, scale, w, ids)
     return w, ids
 
@@ -113,8 +114,9 @@ def route_experts_backward(grad_weights, logits, topk_weights, topk_ids, scoring
             not topk_weights.is_contiguous() or not topk_ids.is_contiguous():
         raise B.MgemmError("route_experts_backward takes route_experts' weights and ids and a gradient of their shape")
     grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-    g = grad_weights.to(torch.float32).contiguous()
-    B.mgemm_route_bwd(g, logits, topk_weights, topk_ids, SCORES[scoring], renormalize, scale, grad)
+    if grad_weights.dtype != torch.float32 or not grad_weights.is_contiguous():
+        grad_weights = grad_weights.to(torch.float32).contiguous()
+    B.mgemm_route_bwd(grad_weights, logits, topk_weights, topk_ids, SCORES[scoring], renormalize, scale, grad)
     return grad
 
 
