@@ -96,6 +96,19 @@ __device__ __forceinline__ F4Tile f4_tile(int t, const Fp4Params &p, const ArgsV
   return ti;
 }
 
+// One lane of a converged warp.  The instructions that take uniform registers
+// (MMAs, scale copies, TMA, commits) are issued under it, with operands every
+// lane has computed alike: behind a test of the lane number the compiler cannot
+// know that, and moves each operand through a loop over the active lanes (an
+// MMA then takes 170 to 220 clocks to issue; here a 128 x 256 x 64 one takes
+// the 128 that it computes, scale copies hidden beneath).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 template <int FMT>
 __device__ __forceinline__ void mma_f4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                        uint32_t accumulate) {
@@ -142,8 +155,9 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   const int op_bytes = (p.a_rows + bn) * 128, sf_bytes = (1 + nt) * C::WPS * 512;
   uint8_t *sSF = smem + (size_t)nst * op_bytes;
   F4Shared &S = *reinterpret_cast<F4Shared *>(sSF + (size_t)nst * sf_bytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int nacc = bn == 256 ? 1 : 2;
+  const uint32_t op0 = (uint32_t)uniform((int)smem_u32(smem)), sf0 = op0 + (uint32_t)(nst * op_bytes);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < nst; ++i) {
@@ -169,12 +183,12 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem_base = S.tmem_slot;
+  const uint32_t tmem_base = (uint32_t)uniform((int)S.tmem_slot);
   pdl_wait();
   pdl_trigger();
   const ArgsView av(p.args, p.E);
   const int status0 = *av.status, na = *av.n_active;
-  const int total = status0 != 0 ? 0 : __ldg(av.mtile_start + na) * p.n_tiles;
+  const int total = uniform(status0 != 0 ? 0 : __ldg(av.mtile_start + na) * p.n_tiles);
   const int kb_count = (p.K + 255) / 256;
   volatile int *vabort = &S.abort_flag;
   uint32_t issued = 0;  // stages armed, for the drain after an abort
@@ -184,107 +198,120 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      const uint32_t tx = (uint32_t)p.stage_bytes;
-      const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert's weights
-      for (int t = blockIdx.x; t < total && !*vabort; t += gridDim.x) {
-        const F4Tile ti = f4_tile(t, p, av, na);
-        const int sfb_tile = ti.e * wtiles + ti.n0 / 128;
-        for (int kb = 0; kb < kb_count; ++kb) {
-          if (!mbar_wait(&S.empty[stage], phase ^ 1, vabort)) {
-            timeout();
-            break;
-          }
-          mbar_arrive_expect_tx(&S.full[stage], tx);
-          ++issued;
-          uint8_t *a = smem + (size_t)stage * op_bytes, *sf = sSF + (size_t)stage * sf_bytes;
-          tma_load_3d(a + p.a_rows * 128, &tmB, &S.full[stage], kb * 128, ti.n0, ti.e);
-          tma_load_3d(sf + C::WPS * 512, &tmSB, &S.full[stage], 0, kb * C::WPS, sfb_tile);
-          tma_load_2d(a, &tmA, &S.full[stage], kb * 128, ti.row0);
-          tma_load_3d(sf, &tmSA, &S.full[stage], 0, kb * C::WPS, ti.sf_tile);
-          if (++stage == nst) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0, acc = 0, slot = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      int old = 0;  // the stage of kSfSlots iterations ago, and its phase
-      uint32_t old_phase = 0, it = 0;
-      bool ok = true;
-      const int sfc = C::WPS * (4 + 4 * nt);  // TMEM columns of a slot
-      for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-        const F4Tile ti = f4_tile(t, p, av, na);
-        if (!mbar_wait(&S.tempty[acc], acc_phase ^ 1, vabort)) {
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint32_t tx = (uint32_t)p.stage_bytes;
+    const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert's weights
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const F4Tile ti = f4_tile(t, p, av, na);
+      const int e = uniform(ti.e), n0 = uniform(ti.n0), row0 = uniform(ti.row0), sfa_tile = uniform(ti.sf_tile);
+      const int sfb_tile = e * wtiles + n0 / 128;
+      for (int kb = 0; kb < kb_count; ++kb) {
+        if (!mbar_wait_warp(&S.empty[stage], phase ^ 1, vabort)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * 128;
-        const int cols = min(bn, (p.N - ti.n0 + 15) & ~15);
-        const uint32_t idesc = f4_idesc(128, cols, C::NV ? 0u : 1u);
-        // a 64-column tile may start in the middle of a 128-column scale tile
-        const uint32_t sfb_off = (ti.n0 & 64) ? 2u : 0u;
-        for (int kb = 0; kb < kb_count; ++kb) {
-          if (!mbar_wait(&S.full[stage], phase, vabort)) {
+        if (elect_one()) {
+          uint8_t *a = smem + (size_t)stage * op_bytes, *sf = sSF + (size_t)stage * sf_bytes;
+          mbar_arrive_expect_tx(&S.full[stage], tx);
+          tma_load_3d(a + p.a_rows * 128, &tmB, &S.full[stage], kb * 128, n0, e);
+          tma_load_3d(sf + C::WPS * 512, &tmSB, &S.full[stage], 0, kb * C::WPS, sfb_tile);
+          tma_load_2d(a, &tmA, &S.full[stage], kb * 128, row0);
+          tma_load_3d(sf, &tmSA, &S.full[stage], 0, kb * C::WPS, sfa_tile);
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == nst) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) timeout();
+  } else if (warp == 1) {
+    int stage = 0, acc = 0, slot = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    int old = 0;  // the stage of kSfSlots iterations ago, and its phase
+    uint32_t old_phase = 0, it = 0;
+    bool ok = true;
+    const uint32_t sfc = (uint32_t)(C::WPS * (4 + 4 * nt));  // TMEM columns of a slot
+    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
+      const F4Tile ti = f4_tile(t, p, av, na);
+      const int n0 = uniform(ti.n0);
+      if (!mbar_wait_warp(&S.tempty[acc], acc_phase ^ 1, vabort)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + acc * 128;
+      const int cols = min(bn, (p.N - n0 + 15) & ~15);
+      const uint32_t idesc = f4_idesc(128, cols, C::NV ? 0u : 1u);
+      // a 64-column tile may start in the middle of a 128-column scale tile
+      const uint32_t sfb_off = (n0 & 64) ? 2u : 0u;
+      for (int kb = 0; kb < kb_count; ++kb) {
+        if (!mbar_wait_warp(&S.full[stage], phase, vabort)) {
+          ok = false;
+          break;
+        }
+        // the slot's last readers have completed (a ring of no more stages than slots says so by itself)
+        if (it >= kSfSlots && nst > kSfSlots) {
+          if (!mbar_wait_warp(&S.empty[old], old_phase, vabort)) {
             ok = false;
             break;
           }
-          // the slot's last readers have completed (a ring of no more stages than slots says so by itself)
-          if (it >= kSfSlots && nst > kSfSlots) {
-            if (!mbar_wait(&S.empty[old], old_phase, vabort)) {
-              ok = false;
-              break;
-            }
-            if (++old == nst) {
-              old = 0;
-              old_phase ^= 1;
-            }
+          if (++old == nst) {
+            old = 0;
+            old_phase ^= 1;
           }
-          ++it;
-          tc_fence_after();
-          const uint32_t a = smem_u32(smem + (size_t)stage * op_bytes), b = a + p.a_rows * 128;
-          const uint32_t sf = smem_u32(sSF + (size_t)stage * sf_bytes);
+        }
+        ++it;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t a = op0 + (uint32_t)(stage * op_bytes), sf = sf0 + (uint32_t)(stage * sf_bytes);
           const uint32_t sfa_t = tmem_base + kSfCol0 + slot * sfc, sfb_t = sfa_t + 4 * C::WPS;
-          const int steps = min(4, (p.K - kb * 256 + 63) / 64);
-          const int words = C::NV ? steps : (steps + 1) / 2;
-#pragma unroll
-          for (int j = 0; j < C::WPS; ++j) {
-            if (j >= words) break;
-            tmem_cp_32x128b_warpx4(sfa_t + 4 * j, smem_desc_rows16(sf + j * 512));
-            for (int i = 0; i < nt; ++i)
-              tmem_cp_32x128b_warpx4(sfb_t + 4 * (j * nt + i), smem_desc_rows16(sf + ((1 + i) * C::WPS + j) * 512));
-          }
-          const uint64_t ad = smem_desc_sw128(a, 16, 1024), bd = smem_desc_sw128(b, 16, 1024);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k >= steps) break;
+          const uint64_t ad = smem_desc_sw128(a, 16, 1024), bd = smem_desc_sw128(a + p.a_rows * 128, 16, 1024);
+          const uint64_t sd = smem_desc_rows16(sf);  // (descriptors advance by bytes >> 4)
+          auto copy_scales = [&](int j) {
+            tmem_cp_32x128b_warpx4(sfa_t + 4 * j, sd + 32 * j);
+            tmem_cp_32x128b_warpx4(sfb_t + 4 * j * nt, sd + 32 * (C::WPS + j));
+            if (nt == 2) tmem_cp_32x128b_warpx4(sfb_t + 4 * j * nt + 4, sd + 32 * (2 * C::WPS + j));
+          };
+          auto step = [&](int k) {
             const int j = C::NV ? k : k / 2;
             const uint32_t id = C::NV ? 0u : (uint32_t)(k & 1) * 2u;
             mma_f4<FMT>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), sfa_t + 4 * j,
                         sfb_t + 4 * j * nt + sfb_off, (kb | k) != 0);
+          };
+          if (kb * 256 + 256 <= p.K) {
+#pragma unroll
+            for (int j = 0; j < C::WPS; ++j) copy_scales(j);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) step(k);
+          } else {  // the contraction ends inside this stage
+            const int steps = (p.K - kb * 256 + 63) / 64, words = C::NV ? steps : (steps + 1) / 2;
+            for (int j = 0; j < words; ++j) copy_scales(j);
+            for (int k = 0; k < steps; ++k) step(k);
           }
           mma_commit(&S.empty[stage]);
-          if (++slot == kSfSlots) slot = 0;
-          if (++stage == nst) {
-            stage = 0;
-            phase ^= 1;
-          }
         }
-        if (!ok) break;
-        mma_commit(&S.tfull[acc]);
-        if (++acc == nacc) {
-          acc = 0;
-          acc_phase ^= 1;
+        __syncwarp();
+        if (++slot == kSfSlots) slot = 0;
+        if (++stage == nst) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      if (!ok) timeout();
+      if (!ok) break;
+      if (elect_one()) mma_commit(&S.tfull[acc]);
+      __syncwarp();
+      if (++acc == nacc) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+    if (!ok && lane == 0) timeout();
+    if (elect_one()) {
       mma_commit(&S.drain);
       mbar_wait_drain(&S.drain, 0);
     }
