@@ -118,18 +118,17 @@ struct RowCast {
       if (qw >= 4 * W) break;
       const int q = qw + tid;
       uint32_t byte;
-      uint64_t ns = 0, r;
+      float r;
       if (F::NV) {
-        byte = (uint32_t)(cvt_e4m3x2(__fdiv_rn(amax[i] * R, 6.f), 0.f) & 0xFFu);
-        const float s = e4m3_value(byte) * Rinv;  // exact
-        const float rc = byte ? __frcp_rn(s) : 0.f;
-        ns = pack_f32x2(-s, -s);
-        r = pack_f32x2(rc, rc);
+        // a R / 6: the product with 1 / 6 rounded is exact where the quotient is a tie of e4m3
+        byte = (uint32_t)(cvt_e4m3x2(amax[i] * R * (1.f / 6.f), 0.f) & 0xFFu);
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e4m3_value(byte) * Rinv));
+        r = byte ? r : 0.f;
       } else {
-        const float s = fp4_pow2_scale(kMxfp4Max, amax[i]);
-        byte = 254u - (__float_as_uint(s) >> 23);
-        r = pack_f32x2(s, s);
+        r = fp4_pow2_scale(kMxfp4Max, amax[i]);
+        byte = 254u - (__float_as_uint(r) >> 23);
       }
+      const uint64_t r2 = ((uint64_t)__float_as_uint(r) << 32) | __float_as_uint(r);
       uint32_t word = q < nblk ? byte << (8 * (q & 3)) : 0u;  // an empty block past the row
       word |= __shfl_xor_sync(0xffffffffu, word, 1);
       word |= __shfl_xor_sync(0xffffffffu, word, 2);
@@ -137,18 +136,7 @@ struct RowCast {
       if (q < nblk) {
         uint32_t out[2 * P];
 #pragma unroll
-        for (int k = 0; k < 2 * P; ++k) {
-          float y[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t b = v[i][k / 2][(k & 1) * 4 + j];
-            const uint64_t x = pack_f32x2(bf16_lo(b), bf16_hi(b));
-            const uint64_t t = F::NV ? fp4_quotient2(x, ns, r) : fp4_mul2(x, r);
-            y[2 * j] = __uint_as_float((uint32_t)t);
-            y[2 * j + 1] = __uint_as_float((uint32_t)(t >> 32));
-          }
-          out[k] = cvt_e2m1x8(y);
-        }
+        for (int k = 0; k < 2 * P; ++k) out[k] = fp4_codes8(&v[i][k / 2][(k & 1) * 4], r2);
         uint8_t *dst = codes + q * (F::BLOCK / 2);
         if (P == 1)
           *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0], out[1]);
@@ -166,12 +154,14 @@ template <int TPR>
 __device__ __forceinline__ float row_max(float a, float *sh) {
   a = warp_max(a);
   if (TPR == 32) return a;
-  __syncthreads();  // the last row's values are read
+  // (the rows of a CTA go on by themselves: a barrier each; an even and an odd set of values, so
+  // one barrier a row does)
+  const int row = threadIdx.x / TPR, w0 = row * (TPR / 32);
   if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = a;
-  __syncthreads();
-  a = sh[0];
+  asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "n"(TPR) : "memory");
+  a = sh[w0];
 #pragma unroll
-  for (int i = 1; i < TPR / 32; ++i) a = fmaxf(a, sh[i]);
+  for (int i = 1; i < TPR / 32; ++i) a = fmaxf(a, sh[w0 + i]);
   return a;
 }
 
@@ -208,7 +198,8 @@ __global__ void __launch_bounds__(kQuantThreads)
                      float *__restrict__ row_scale) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float sh[kQuantThreads / 32];
+  __shared__ float sh[2][kQuantThreads / 32];
+  int odd = 0;
   constexpr int kRows = kQuantThreads / TPR;  // rows of a CTA at a time
   const int lane = threadIdx.x & 31, tid = threadIdx.x % TPR;
   const int64_t step = (int64_t)gridDim.x * kRows, first = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
@@ -223,7 +214,7 @@ __global__ void __launch_bounds__(kQuantThreads)
       }
       const int64_t row = e * S.N + n;
       const RowReader rd{S.in + row * S.ld, nullptr, S.vec32};
-      cast_row<FMT, NB, TPR>(rd, K, i, W, codes + row * (K / 2), sf, row_scale + row, tid, sh);
+      cast_row<FMT, NB, TPR>(rd, K, i, W, codes + row * (K / 2), sf, row_scale + row, tid, sh[odd ^= 1]);
     }
     return;
   }
@@ -245,76 +236,72 @@ __global__ void __launch_bounds__(kQuantThreads)
       rd.row = S.in + i * S.ld;
       if (S.gated) rd.up = rd.row + K;
     }
-    cast_row<FMT, NB, TPR>(rd, K, tile_row, W, codes + i * (K / 2), sf, row_scale + i, tid, sh);
+    cast_row<FMT, NB, TPR>(rd, K, tile_row, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1]);
   }
 }
 
 constexpr float kBf16Max = 3.38953139e38f;  // (2 - 2^-7) 2^127
 
-// Four e2m1 codes (16 bits) -> four bf16 in two words: the value's two bytes
-// from eight-entry tables by the code's low three bits, the sign from its top bit.
-__device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-  return d;
-}
-__device__ __forceinline__ uint2 e2m1x4_to_bf16(uint32_t c) {
-  // 0 .. 6 in bf16: 0000 3F00 3F80 3FC0 4000 4040 4080 40C0
-  const uint32_t sel = c & 0x7777u;
-  const uint32_t hi = byte_perm(0x3F3F3F00u, 0x40404040u, sel), lo = byte_perm(0xC0800000u, 0xC0804000u, sel);
-  uint32_t a = byte_perm(lo, hi, 0x5140u), b = byte_perm(lo, hi, 0x7362u);
-  a |= ((c << 12) & 0x8000u) | ((c << 24) & 0x80000000u);
-  b |= ((c << 4) & 0x8000u) | ((c << 16) & 0x80000000u);
-  return make_uint2(a, b);
+// A code byte -> its two values in f16.
+__device__ __forceinline__ uint32_t e2m1x2_to_f16(uint32_t byte) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(byte));
+  return r;
 }
 
-constexpr int kDequantUnroll = 4;
-
-// A warp per row, 8 elements per lane and step, kDequantUnroll steps' loads
-// ahead of their stores.  A block's factor b / R (2^(byte - 127)) has at most 4
-// significant bits, so code times factor is exact in bf16.
+// A warp per row, 16 elements per lane and step.  NVFP4: code times the block's
+// e4m3 scale is exact in f16 (6 significant bits, at most 2688), then times the
+// power of two 1 / R; MXFP4: code times the block's power of two.  Both exact.
 template <int FMT>
 __global__ void __launch_bounds__(256)
     dequant_fp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ sf,
                        const float *__restrict__ row_scale, int64_t E, int64_t N, int K, __nv_bfloat16 *__restrict__ out,
-                       int64_t ld) {
+                       int64_t ld, bool vec32) {
   using F = Fp4<FMT>;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
-  const int W = fp4_words(FMT, K), units = K / 8;
+  const int W = fp4_words(FMT, K), units = K / 16;
   const int64_t npad = (N + 127) / 128 * 128;
   for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < E * N; i += nwarps) {
     const int64_t e = i / N, tile_row = e * npad + (i - e * N);
     const float inv = F::NV ? __frcp_rn(__ldg(row_scale + i)) : 1.f;
-    const uint32_t *src = reinterpret_cast<const uint32_t *>(codes + i * (K / 2));
+    const uint2 *src = reinterpret_cast<const uint2 *>(codes + i * (K / 2));
     const uint8_t *sfr = sf + fp4_sf_offset(tile_row, 0, W);
-    for (int c0 = lane; c0 < units; c0 += 32 * kDequantUnroll) {
-      uint32_t w[kDequantUnroll], byte[kDequantUnroll];
+    __nv_bfloat16 *dst = out + i * ld;
+#pragma unroll 2
+    for (int c = lane; c < units; c += 32) {
+      const int q = F::NV ? c : c >> 1;  // the block
+      const uint2 w = __ldg(src + c);
+      const uint32_t byte = __ldg(sfr + (int64_t)(q >> 2) * 512 + (q & 3));
+      const float f = F::NV ? inv : e8m0_value(byte);
+      const __half2 h = __half2half2(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
+      // a cast can round the largest bf16 values up past bf16's range: they stay at its end
+      const bool far = F::NV ? f > 0x1p114f : f > 0x1p124f;
+      uint32_t o[8];
 #pragma unroll
-      for (int u = 0; u < kDequantUnroll; ++u) {
-        const int c = c0 + 32 * u, q = c * 8 / F::BLOCK;
-        w[u] = c < units ? __ldg(src + c) : 0u;
-        byte[u] = c < units ? __ldg(sfr + (int64_t)(q >> 2) * 512 + (q & 3)) : 0u;
-      }
-#pragma unroll
-      for (int u = 0; u < kDequantUnroll; ++u) {
-        const int c = c0 + 32 * u;
-        if (c >= units) break;
-        const __nv_bfloat162 s = __float2bfloat162_rn(F::NV ? e4m3_value(byte[u]) * inv : e8m0_value(byte[u]));
-        // a cast can round the largest bf16 values up past bf16's range: they stay at its end
-        const __nv_bfloat162 top = __float2bfloat162_rn(kBf16Max), bottom = __float2bfloat162_rn(-kBf16Max);
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint2 v = e2m1x4_to_bf16(w[u] >> (16 * k));
-          const __nv_bfloat162 a = __hmax2(__hmin2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x), s), top), bottom);
-          const __nv_bfloat162 b = __hmax2(__hmin2(__hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y), s), top), bottom);
-          o[2 * k] = *reinterpret_cast<const uint32_t *>(&a);
-          o[2 * k + 1] = *reinterpret_cast<const uint32_t *>(&b);
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t v = e2m1x2_to_f16((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
+        __half2 v2 = *reinterpret_cast<const __half2 *>(&v);
+        if (F::NV) v2 = __hmul2(v2, h);
+        float2 y = __half22float2(v2);
+        y.x *= f;
+        y.y *= f;
+        if (far) {
+          y.x = fminf(fmaxf(y.x, -kBf16Max), kBf16Max);
+          y.y = fminf(fmaxf(y.y, -kBf16Max), kBf16Max);
         }
-        *reinterpret_cast<uint4 *>(out + i * ld + c * 8) = make_uint4(o[0], o[1], o[2], o[3]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
+        o[k] = *reinterpret_cast<const uint32_t *>(&b);
+      }
+      if (vec32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c * 16), "r"(o[0]), "r"(o[1]),
+                     "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                     : "memory");
+      } else {
+        reinterpret_cast<uint4 *>(dst + c * 16)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        reinterpret_cast<uint4 *>(dst + c * 16)[1] = make_uint4(o[4], o[5], o[6], o[7]);
       }
     }
   }
@@ -329,9 +316,9 @@ int rows_grid(int64_t rows) {
 
 bool a16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// rows: those of the call (device-known: at most).  A warp per row while that
-// fills the SMs with warps (4 per scheduler), else a CTA per row; NB so that the
-// row stays in registers where it can.
+// rows: those of the call (device-known: at most).  Below two CTAs' worth of rows
+// for every SM, a CTA takes a row; else a warp does, or two for NVFP4 rows past
+// 2048 (of which a warp would need twice the registers).
 template <int FMT>
 int launch_quant(QuantSource S, int64_t rows, int K, uint8_t *codes, uint8_t *sf, float *row_scale, cudaStream_t s,
                  const char *what) {
@@ -340,13 +327,22 @@ int launch_quant(QuantSource S, int64_t rows, int K, uint8_t *codes, uint8_t *sf
   S.vec32 = ((uintptr_t)S.in & 31) == 0 && S.ld % 16 == 0 && (!S.gated || K % 16 == 0);
   const int nblk = K / Fp4<FMT>::BLOCK;
   const bool cta = rows < (int64_t)sms * 8 && nblk > 32;
-  const int64_t want = cta ? rows : (rows + 7) / 8, cap = (int64_t)sms * 16;
-  const unsigned grid = (unsigned)(want < cap ? want : cap);
   constexpr int U = Fp4<FMT>::BLOCK / 16;
-  auto kernel = cta ? nblk <= 256 ? quant_fp4_kernel<FMT, 1, 256> : quant_fp4_kernel<FMT, 4 / U, 256>
-                : nblk <= 64 / U  ? quant_fp4_kernel<FMT, 2 / U, 32>
-                : nblk <= 128 / U ? quant_fp4_kernel<FMT, 4 / U, 32>
-                                  : quant_fp4_kernel<FMT, 8 / U, 32>;
+  int per_cta = 8;
+  auto kernel = quant_fp4_kernel<FMT, 4 / U, 32>;
+  if (cta) {
+    per_cta = 1;
+    kernel = nblk <= 256 ? quant_fp4_kernel<FMT, 1, 256> : quant_fp4_kernel<FMT, 4 / U, 256>;
+  } else if (nblk <= 64 / U) {
+    kernel = quant_fp4_kernel<FMT, 2 / U, 32>;
+  } else if constexpr (Fp4<FMT>::NV) {
+    if (nblk > 128) {
+      per_cta = 4;
+      kernel = quant_fp4_kernel<FMT, 4, 64>;
+    }
+  }
+  const int64_t want = (rows + per_cta - 1) / per_cta, cap = (int64_t)sms * 16;
+  const unsigned grid = (unsigned)(want < cap ? want : cap);
   return launch_pdl(kernel, dim3(grid), dim3(kQuantThreads), 0, s, 1, what, S, K, codes, sf, row_scale);
 }
 
@@ -389,7 +385,8 @@ extern "C" int mgemm_dequant_fp4(const uint8_t *codes, const uint8_t *sf, const 
   if (grid < 0) return MGEMM_ECUDA;
   return launch_pdl(fmt == MGEMM_NVFP4 ? dequant_fp4_kernel<MGEMM_NVFP4> : dequant_fp4_kernel<MGEMM_MXFP4>,
                     dim3((unsigned)grid), dim3(256), 0, (cudaStream_t)stream, 1, "mgemm_dequant_fp4 launch", codes, sf,
-                    row_scale, (int64_t)E, N, K, (__nv_bfloat16 *)out, ld_out);
+                    row_scale, (int64_t)E, N, K, (__nv_bfloat16 *)out, ld_out,
+                    ((uintptr_t)out & 31) == 0 && ld_out % 16 == 0);
 }
 
 extern "C" int mgemm_quant_fp4_rows(const void *args, int E, int64_t M, const void *in, int64_t in_rows, int K,

@@ -23,26 +23,30 @@ __device__ __forceinline__ int64_t fp4_sf_offset(int64_t r, int j, int W) {
   return ((r >> 7) * W + j) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 }
 
-// Eight floats -> eight e2m1 codes (round to nearest even, saturating), the first in the low nibble.
-__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
+// Eight products x r of 4 pairs of bf16 -> eight e2m1 codes (round to nearest
+// even, saturating), the first in the low nibble.  The products go through f16
+// on the way.  That settles the ties: x and 1 / r have 8 and 4 significant bits,
+// so a quotient that is no midpoint of two e2m1 values is at least 2^-9 of
+// itself away from one, f16 moves it by at most 2^-12, and one that is a midpoint,
+// off by r's and the product's rounding (2^-22), comes back to it.
+__device__ __forceinline__ uint32_t fp4_codes8(const uint32_t *x, uint64_t r2) {
+  uint32_t h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint64_t y = ((uint64_t)(x[j] & 0xFFFF0000u) << 32) | (x[j] << 16);
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(r2));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[j]) : "f"(__uint_as_float((uint32_t)(y >> 32))), "f"(__uint_as_float((uint32_t)y)));
+  }
   uint32_t r;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 a, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 b, %2;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 c, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f16x2 d, %4;\n\t"
       "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+      : "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]));
   return r;
-}
-
-// The value of an e2m1 code: sign, 2 exponent bits (bias 1), 1 mantissa bit.
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-  const uint32_t m = code & 7u;
-  // 0, .5 are below the normal range; 1 .. 6 have exponent (m >> 1) - 1 and mantissa bit m & 1
-  const float a = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-  return code & 8u ? -a : a;
 }
 
 // e4m3 byte (no sign here) -> value; e8m0 byte -> value (byte 0: 2^-127, below the normal range)
@@ -59,29 +63,5 @@ __device__ __forceinline__ float fp4_pow2_scale(float num, float amax) {
   return __uint_as_float(__float_as_uint(__fdiv_rn(num, fmaxf(amax, 1e-12f))) & 0x7F800000u);
 }
 constexpr float kMxfp4Max = 6.f, kNvfp4RowMax = 2688.f;  // 6 x 448
-
-// Two quotients x / s at a time (packed fp32), rounded so that one halfway
-// between two e2m1 values comes out as exactly that: r is 1 / s rounded, the
-// remainder x - y s is exact in one fma, and adding remainder x r makes a
-// representable quotient exact (any other quotient of a bf16 x and an s of 4
-// significant bits is at least 2^-9 of itself away from a midpoint, far more
-// than the error left here).  neg_s is -s.
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  return ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
-}
-__device__ __forceinline__ uint64_t fp4_mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fp4_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t fp4_quotient2(uint64_t x, uint64_t neg_s, uint64_t r) {
-  const uint64_t y = fp4_mul2(x, r);
-  return fp4_fma2(fp4_fma2(y, neg_s, x), r, y);
-}
 
 }  // namespace mgemm

@@ -31,8 +31,8 @@ constexpr uint32_t kKeyOut = 0u, kKeyOff = 1u;
 // Unsigned integers in the order of the floats: -0 equals +0, a NaN is the largest.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return kFull;
-  return (u >> 31) ? ~u : u | 0x80000000u;
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return v != v ? kFull : k;
 }
 
 template <typename T>
@@ -46,7 +46,8 @@ __device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16 *
   return __bfloat162float(*p);
 }
 
-__device__ __forceinline__ float sigmoidf(float l) { return 1.f / (1.f + expf(-l)); }
+// (a correctly rounded reciprocal is the correctly rounded quotient 1 / x)
+__device__ __forceinline__ float sigmoidf(float l) { return __frcp_rn(1.f + expf(-l)); }
 
 __device__ __forceinline__ float warp_sum(float a) {
 #pragma unroll
@@ -138,10 +139,10 @@ __device__ __forceinline__ Best two_best(const uint32_t (&key)[N]) {
 #pragma unroll
   for (int j = 1; j < N; ++j) {
     const bool first = key[j] > b.k1, second = key[j] > b.k2;
-    b.k2 = first ? b.k1 : second ? key[j] : b.k2;
     b.j2 = first ? b.j1 : second ? j : b.j2;
-    b.k1 = first ? key[j] : b.k1;
     b.j1 = first ? j : b.j1;
+    b.k2 = max(b.k2, min(b.k1, key[j]));
+    b.k1 = max(b.k1, key[j]);
   }
   return b;
 }
@@ -157,41 +158,45 @@ __global__ void __launch_bounds__(kRouteThreads)
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= p.T) return;  // whole warps leave together
   const int e0 = lane * NV;
-  float s[NV];       // logits, then scores, of softmax times their sum (0 where off)
+  const L *row = logits + t * p.ld;
   uint32_t key[NV];  // the order of the choice
-  load_lane<NV>(logits + t * p.ld, e0, p.E, p.vec, -INFINITY, s);
   float m = 0.f, sum = 1.f;
-  if (p.sigmoid) {
+  {
+    float s[NV];  // logits, then scores, of softmax times their sum (0 where off)
+    load_lane<NV>(row, e0, p.E, p.vec, -INFINITY, s);
+    if (p.sigmoid) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool off = s[j] <= MGEMM_ROUTE_MASKED;
-      s[j] = off ? 0.f : sigmoidf(s[j]);
-      key[j] = off ? kKeyOff : 2u;
+      for (int j = 0; j < NV; ++j) {
+        key[j] = s[j] <= MGEMM_ROUTE_MASKED ? kKeyOff : 2u;
+        s[j] = sigmoidf(s[j]);
+      }
+    } else {
+      uint32_t most = kKeyOff;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        key[j] = s[j] <= MGEMM_ROUTE_MASKED ? kKeyOff : order_key(s[j]);
+        most = max(most, key[j]);
+      }
+      most = __reduce_max_sync(kFull, most);
+      m = most == kKeyOff ? 0.f : key_value(most);
+      sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        s[j] = key[j] == kKeyOff ? 0.f : expf(s[j] - m);
+        sum += s[j];
+      }
+      sum = warp_sum(sum);
+      if (sum == 0.f) sum = 1.f;  // every expert is off
     }
-  } else {
-    m = s[0];
+    if (bias) {
+      float b[NV];
+      load_lane<NV>(bias, e0, p.E, p.vec_bias, 0.f, b);
 #pragma unroll
-    for (int j = 1; j < NV; ++j) m = fmaxf(m, s[j]);
-    m = warp_max(m);
-    if (m <= MGEMM_ROUTE_MASKED) m = 0.f;
-    sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const bool off = s[j] <= MGEMM_ROUTE_MASKED;
-      key[j] = off ? kKeyOff : order_key(s[j]);
-      s[j] = off ? 0.f : expf(s[j] - m);
-      sum += s[j];
+      for (int j = 0; j < NV; ++j) s[j] = (p.sigmoid ? s[j] : s[j] / sum) + b[j];
     }
-    sum = warp_sum(sum);
-    if (sum == 0.f) sum = 1.f;  // every expert is off
-  }
-  if (p.sigmoid || bias) {
-    float b[NV];
-    if (bias) load_lane<NV>(bias, e0, p.E, p.vec_bias, 0.f, b);
+    if (p.sigmoid || bias) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const float c = p.sigmoid ? s[j] : s[j] / sum;
-      if (key[j] != kKeyOff) key[j] = order_key(bias ? c + b[j] : c);
+      for (int j = 0; j < NV; ++j) key[j] = key[j] == kKeyOff ? kKeyOff : order_key(s[j]);
     }
   }
   if (p.E < 32 * NV) {
@@ -226,9 +231,7 @@ __global__ void __launch_bounds__(kRouteThreads)
       rank += other > mine || (other == mine && o < g);
     }
     if (rank >= p.topk_group) {  // (lanes past the groups hold no keys)
-      best.k1 = best.k2 = kKeyOut;
-#pragma unroll
-      for (int j = 0; j < NV; ++j) key[j] = kKeyOut;
+      best.k1 = best.k2 = kKeyOut;  // none of the lane's experts is chosen, so none is looked over again
     }
   } else if constexpr (GROUPS == 2) {
     // each group's best one or two keys over the warp; lane g % 32 keeps the
@@ -273,44 +276,43 @@ __global__ void __launch_bounds__(kRouteThreads)
     best = two_best(key);
   }
 
-  // the top_k keys, largest first; lane r keeps the id of pick r (top_k <= 32),
-  // the lane that holds an expert marks it
+  // the top_k keys, largest first; lane r keeps the id of pick r (top_k <= 32).
+  // A lane's own picks are bits of `taken`; its second best steps in for the
+  // first, and then its other experts are looked over again.
   int my_id = 0;
-  float my_s = 0.f;
+  uint32_t taken = 0;
   bool spare = true;  // best.k2 is the lane's second best
   for (int r = 0; r < p.top_k; ++r) {
     const uint32_t top = __reduce_max_sync(kFull, best.k1);
     const int src = __ffs(__ballot_sync(kFull, best.k1 == top)) - 1;
-    float sc = s[0];
-#pragma unroll
-    for (int j = 1; j < NV; ++j) sc = best.j1 == j ? s[j] : sc;
     const int id = __shfl_sync(kFull, e0 + best.j1, src);
-    sc = __shfl_sync(kFull, sc, src);
-    if (lane == r) {
-      my_id = id;
-      my_s = sc;
-    }
+    if (lane == r) my_id = id;
     if (lane == src) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (best.j1 == j) key[j] = kKeyOut;
+      taken |= 1u << best.j1;
       if (spare) {
         best.k1 = best.k2;
         best.j1 = best.j2;
-        spare = false;
       } else {
-        best = two_best(key);
-        spare = true;
+        uint32_t rest[NV];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) rest[j] = (taken >> j) & 1u ? kKeyOut : key[j];
+        best = two_best(rest);
       }
+      spare = !spare;
     }
   }
-  if (!p.sigmoid) my_s /= sum;
+  // the picks' scores, one per lane
+  float s = 0.f;
+  if (lane < p.top_k) {
+    const float l = load_logit(row + my_id);
+    if (!(l <= MGEMM_ROUTE_MASKED)) s = p.sigmoid ? sigmoidf(l) : expf(l - m) / sum;
+  }
   if (p.renormalize) {
-    const float total = warp_sum(my_s);  // lanes past top_k hold 0
-    my_s = total == 0.f ? 0.f : my_s / total;
+    const float total = warp_sum(s);
+    s = total == 0.f ? 0.f : s / total;
   }
   if (lane < p.top_k) {
-    weights[t * p.top_k + lane] = my_s * p.scale;
+    weights[t * p.top_k + lane] = s * p.scale;
     ids[t * p.top_k + lane] = my_id;
   }
 }
