@@ -12,6 +12,7 @@
 // before its first code, so the thread's blocks stay in registers as they were
 // read (up to NB of them; longer rows are read twice, the second time from
 // cache).  Four threads' scale bytes make a word.
+#include "fill_args.cuh"
 #include "fp4.cuh"
 
 namespace mgemm {
@@ -240,6 +241,49 @@ __global__ void __launch_bounds__(kQuantThreads)
   }
 }
 
+// mgemm_fill_args and the cast of the token rows in one launch, for at most
+// kQuantThreads groups: CTA 0 fills the args block, the others scan the group
+// sizes themselves (a thread per group, two block scans) for the rows' places, so
+// that they need not wait for it.  Rows are cast as above, and under the same
+// conditions: none when the sizes are not valid.
+template <int FMT, int NB, int TPR>
+__global__ void __launch_bounds__(kQuantThreads)
+    fill_quant_fp4_kernel(const int64_t *__restrict__ sizes, uint8_t *__restrict__ args, const QuantSource S, int K,
+                          uint8_t *__restrict__ codes, uint8_t *__restrict__ sf, float *__restrict__ row_scale) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t m = (int)threadIdx.x < S.E ? sizes[threadIdx.x] : 0;
+  if (blockIdx.x == 0) {
+    fill_args_body<kQuantThreads>(m, S.E, S.M, args);
+    return;
+  }
+  __shared__ int ends[kQuantThreads], starts[kQuantThreads];  // a group's last row + 1, its first tile row
+  __shared__ int64_t tot[kQuantThreads / 32];
+  __shared__ int64_t all;
+  __shared__ float sh[2][kQuantThreads / 32];
+  const bool bad = __syncthreads_or(m < 0);
+  const int64_t end = block_inclusive_scan<int64_t, kQuantThreads>(m, tot);
+  const int64_t padded = (m + kColPad - 1) / kColPad * kColPad;
+  const int64_t pend = block_inclusive_scan<int64_t, kQuantThreads>(padded, tot);
+  if (threadIdx.x == kQuantThreads - 1) all = end;
+  ends[threadIdx.x] = (int)end;
+  starts[threadIdx.x] = (int)(pend - padded);
+  __syncthreads();
+  if (bad || all != S.M) return;
+  constexpr int kRows = kQuantThreads / TPR;
+  const int lane = threadIdx.x & 31, tid = threadIdx.x % TPR;
+  const int W = fp4_words(FMT, K);
+  int odd = 0;
+  for (int64_t i = (int64_t)(blockIdx.x - 1) * kRows + threadIdx.x / TPR; i < S.M; i += (int64_t)(gridDim.x - 1) * kRows) {
+    int e = 0;
+    for (int j = lane; j < S.E; j += 32) e += ends[j] <= (int)i;
+    e = __reduce_add_sync(0xffffffffu, e);
+    const int64_t tile_row = starts[e] + (i - (e > 0 ? ends[e - 1] : 0));
+    const RowReader rd{S.in + i * S.ld, nullptr, S.vec32};
+    cast_row<FMT, NB, TPR>(rd, K, tile_row, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1]);
+  }
+}
+
 constexpr float kBf16Max = 3.38953139e38f;  // (2 - 2^-7) 2^127
 
 // A code byte -> its two values in f16.
@@ -321,32 +365,48 @@ bool a16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 // 2048 (of which a warp would need twice the registers).
 template <int FMT>
 int launch_quant(QuantSource S, int64_t rows, int K, uint8_t *codes, uint8_t *sf, float *row_scale, cudaStream_t s,
-                 const char *what) {
+                 const char *what, const int64_t *sizes = nullptr, uint8_t *args = nullptr) {
   const int sms = sm_count_cached();
   if (sms <= 0) return MGEMM_ECUDA;
   S.vec32 = ((uintptr_t)S.in & 31) == 0 && S.ld % 16 == 0 && (!S.gated || K % 16 == 0);
   const int nblk = K / Fp4<FMT>::BLOCK;
-  const bool cta = rows < (int64_t)sms * 8 && nblk > 32;
   constexpr int U = Fp4<FMT>::BLOCK / 16;
-  int per_cta = 8;
-  auto kernel = quant_fp4_kernel<FMT, 4 / U, 32>;
-  if (cta) {
-    per_cta = 1;
-    kernel = nblk <= 256 ? quant_fp4_kernel<FMT, 1, 256> : quant_fp4_kernel<FMT, 4 / U, 256>;
-  } else if (nblk <= 64 / U) {
-    kernel = quant_fp4_kernel<FMT, 2 / U, 32>;
-  } else if constexpr (Fp4<FMT>::NV) {
-    if (nblk > 128) {
-      per_cta = 4;
-      kernel = quant_fp4_kernel<FMT, 4, 64>;
-    }
+  auto go = [&](auto kernel, auto fill_kernel, int per_cta) {
+    const int64_t want = (rows + per_cta - 1) / per_cta, cap = (int64_t)sms * 16;
+    const unsigned grid = (unsigned)(want < cap ? want : cap);
+    if (sizes)
+      return launch_pdl(fill_kernel, dim3(grid + 1), dim3(kQuantThreads), 0, s, 1, what, sizes, args, S, K, codes, sf,
+                        row_scale);
+    return launch_pdl(kernel, dim3(grid), dim3(kQuantThreads), 0, s, 1, what, S, K, codes, sf, row_scale);
+  };
+#define MGEMM_QUANT_LAUNCH(NB, TPR) \
+  return go(quant_fp4_kernel<FMT, NB, TPR>, fill_quant_fp4_kernel<FMT, NB, TPR>, kQuantThreads / TPR)
+  if (rows < (int64_t)sms * 8 && nblk > 32) {
+    if (nblk <= 256) MGEMM_QUANT_LAUNCH(1, 256);
+    MGEMM_QUANT_LAUNCH(4 / U, 256);
   }
-  const int64_t want = (rows + per_cta - 1) / per_cta, cap = (int64_t)sms * 16;
-  const unsigned grid = (unsigned)(want < cap ? want : cap);
-  return launch_pdl(kernel, dim3(grid), dim3(kQuantThreads), 0, s, 1, what, S, K, codes, sf, row_scale);
+  if (nblk <= 64 / U) MGEMM_QUANT_LAUNCH(2 / U, 32);
+  if constexpr (Fp4<FMT>::NV) {
+    if (nblk > 128) MGEMM_QUANT_LAUNCH(4, 64);
+  }
+  MGEMM_QUANT_LAUNCH(4 / U, 32);
+#undef MGEMM_QUANT_LAUNCH
 }
 
 }  // namespace
+
+int fp4_fill_quant_rows(const int64_t *sizes, int E, int64_t M, uint8_t *args, const __nv_bfloat16 *x, int K,
+                        int64_t ld_x, int fmt, uint8_t *codes, uint8_t *sf, float *row_scale, cudaStream_t s) {
+  QuantSource S{};
+  S.in = x;
+  S.ld = ld_x;
+  S.E = E;
+  S.M = M;
+  const char *what = "mgemm_gmm_fp4 fill + cast launch";
+  return fmt == MGEMM_NVFP4 ? launch_quant<MGEMM_NVFP4>(S, M, K, codes, sf, row_scale, s, what, sizes, args)
+                            : launch_quant<MGEMM_MXFP4>(S, M, K, codes, sf, row_scale, s, what, sizes, args);
+}
+
 }  // namespace mgemm
 
 using namespace mgemm;

@@ -64,4 +64,9 @@ __device__ __forceinline__ float fp4_pow2_scale(float num, float amax) {
 }
 constexpr float kMxfp4Max = 6.f, kNvfp4RowMax = 2688.f;  // 6 x 448
 
+// mgemm_fill_args and mgemm_quant_fp4_rows (plain rows) in one launch; E <= kFp4FillMaxE.
+constexpr int kFp4FillMaxE = 256;
+int fp4_fill_quant_rows(const int64_t *sizes, int E, int64_t M, uint8_t *args, const __nv_bfloat16 *x, int K,
+                        int64_t ld_x, int fmt, uint8_t *codes, uint8_t *sf, float *row_scale, cudaStream_t s);
+
 }  // namespace mgemm

@@ -557,10 +557,15 @@ extern "C" int mgemm_gmm_fp4(const int64_t *group_sizes, int E, int fmt, const v
   const Workspace ws = fp4_workspace(fmt, M, K, E);
   if (workspace_bytes < (int64_t)ws.bytes) return MGEMM_EINVAL;
   uint8_t *b = (uint8_t *)workspace;
-  rc = mgemm_fill_args(group_sizes, E, M, b, stream);
-  if (rc) return rc;
   float *rx = fmt == MGEMM_NVFP4 ? (float *)(b + ws.rows) : nullptr;
-  rc = mgemm_quant_fp4_rows(b, E, M, x, M, K, ld_x, nullptr, 0, 1, 0, fmt, b + ws.codes, b + ws.sf, rx, stream);
+  if (E <= kFp4FillMaxE) {
+    rc = fp4_fill_quant_rows(group_sizes, E, M, b, (const __nv_bfloat16 *)x, K, ld_x, fmt, b + ws.codes, b + ws.sf, rx,
+                             (cudaStream_t)stream);
+  } else {
+    rc = mgemm_fill_args(group_sizes, E, M, b, stream);
+    if (!rc)
+      rc = mgemm_quant_fp4_rows(b, E, M, x, M, K, ld_x, nullptr, 0, 1, 0, fmt, b + ws.codes, b + ws.sf, rx, stream);
+  }
   if (rc) return rc;
   return mgemm_fwd_fp4(b, fmt, b + ws.codes, b + ws.sf, rx, w, sw, rw, out, nullptr, 0, nullptr, M, K, N, E, stream);
 }
