@@ -8,17 +8,21 @@ product runs on the block-scaled tensor-core path.  It is a serving operator:
 the weights are laid out once, and no gradient flows through it.
 
 This module only allocates outputs with torch and calls the binding; every
-step runs in the CUDA library.
+step runs in the CUDA library.  At decode sizes a call's time is the host's: an
+allocation costs it about 4 us next to 3 us for a launch.  So a cast makes one
+allocation for its three parts (their tensors are made when asked for), and
+gmm_fp4 keeps a small workspace per stream.
 """
 
 import functools
+import threading
 
 import torch
 
 from . import binding as B
 
 FORMATS = {"mxfp4": B.MGEMM_MXFP4, "nvfp4": B.MGEMM_NVFP4}
-
+BF16 = torch.bfloat16
 
 _scale_bytes = functools.lru_cache(maxsize=4096)(B.mgemm_fp4_scale_bytes)
 _workspace_bytes = functools.lru_cache(maxsize=4096)(B.mgemm_gmm_fp4_workspace_bytes)
@@ -34,9 +38,7 @@ def _format(fmt):
 class Fp4Tensor:
     """A [E, N, K] tensor in 4-bit codes: ``codes`` uint8 [E, N, K / 2], ``scales``
     uint8 (the tiled scale factors of mgemm.h), ``row_scale`` float32 [E, N] for
-    "nvfp4" and None for "mxfp4"."""
-
-    __slots__ = ("codes", "scales", "row_scale", "fmt", "code", "shape")
+    "nvfp4" and None for "mxfp4"; ``fmt``, ``shape`` and ``device``."""
 
     def __init__(self, codes, scales, row_scale, fmt):
         self.code = _format(fmt)
@@ -48,72 +50,128 @@ class Fp4Tensor:
             raise B.MgemmError("Fp4Tensor takes contiguous codes and scales")
         if scales.numel() != E * _scale_bytes(self.code, N, 2 * half):
             raise B.MgemmError(f"Fp4Tensor: {scales.numel()} scale bytes do not fit codes {tuple(codes.shape)}")
+        rows = None
         if fmt == "nvfp4":
             if row_scale is None or row_scale.dtype != torch.float32 or row_scale.numel() != E * N or \
                     not row_scale.is_contiguous():
                 raise B.MgemmError("nvfp4 takes a contiguous float32 row_scale [E, N]")
+            rows = row_scale.data_ptr()
         elif row_scale is not None:
             raise B.MgemmError("mxfp4 has no row scales")
-        self.codes, self.scales, self.row_scale, self.fmt = codes, scales, row_scale, fmt
+        for t in (codes, scales, row_scale):
+            if t is not None and (not t.is_cuda or t.device != codes.device):
+                raise B.MgemmError("mgemm kernels take device tensors only, of one device")
+        self.fmt, self.device = fmt, codes.device
+        self._parts = (codes, scales, row_scale)
+        self._storage = None
+        self._ptrs = (codes.data_ptr(), scales.data_ptr(), rows)
 
     @classmethod
-    def _of(cls, codes, scales, row_scale, fmt, code, shape):
-        """Of parts laid out here (nothing to check)."""
+    def _empty(cls, fmt, code, E, N, K, device):
+        """Unwritten parts, one after another in one allocation."""
         q = cls.__new__(cls)
-        q.codes, q.scales, q.row_scale, q.fmt, q.code, q.shape = codes, scales, row_scale, fmt, code, shape
+        q.fmt, q.code, q.shape, q.device = fmt, code, (E, N, K), device
+        n_codes = (E * N * (K // 2) + 255) & ~255
+        n_scales = E * _scale_bytes(code, N, K)  # a multiple of 512
+        q._storage = torch.empty(n_codes + n_scales + (4 * E * N if fmt == "nvfp4" else 0), dtype=torch.uint8,
+                                 device=device)
+        q._parts = None
+        p = q._storage.data_ptr()
+        q._ptrs = (p, p + n_codes, p + n_codes + n_scales if fmt == "nvfp4" else None)
         return q
+
+    def _part(self, i):
+        if self._parts is None:
+            E, N, K = self.shape
+            n, s, base = E * N * (K // 2), E * _scale_bytes(self.code, N, K), self._storage
+            o = (n + 255) & ~255
+            rows = base[o + s:].view(torch.float32).view(E, N) if self.fmt == "nvfp4" else None
+            self._parts = (base[:n].view(E, N, K // 2), base[o:o + s], rows)
+        return self._parts[i]
+
+    codes = property(lambda self: self._part(0))
+    scales = property(lambda self: self._part(1))
+    row_scale = property(lambda self: self._part(2))
 
 
 def quantize_fp4(x, fmt):
     """bf16 [E, N, K] or [N, K] on the GPU (rows at a common stride, else copied) -> Fp4Tensor; K % 32 == 0."""
     code = _format(fmt)
-    if x.dtype != torch.bfloat16 or x.dim() not in (2, 3):
+    dim = x.dim()
+    if x.dtype != BF16 or (dim != 2 and dim != 3):
         raise B.MgemmError("quantize_fp4 takes a bf16 [E, N, K] or [N, K]")
-    x = x if x.dim() == 3 else x.unsqueeze(0)
-    E, N, K = x.shape
-    if x.stride(2) != 1 or x.stride(1) % 8 or x.stride(1) < K or x.data_ptr() % 16 or \
-            (E > 1 and x.stride(0) != N * x.stride(1)):
+    B._cuda(x)
+    E, N, K = x.shape if dim == 3 else (1, *x.shape)
+    st = x.stride()
+    ld = st[-2]
+    if st[-1] != 1 or ld % 8 or ld < K or x.data_ptr() % 16 or (E > 1 and st[0] != N * ld):
         x = x.contiguous()
-    dev = x.device
-    codes = torch.empty((E, N, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty(E * _scale_bytes(code, N, K), dtype=torch.uint8, device=dev)
-    rows = torch.empty((E, N), dtype=torch.float32, device=dev) if fmt == "nvfp4" else None
-    B.mgemm_quant_fp4(x, code, codes, scales, rows)
-    return Fp4Tensor._of(codes, scales, rows, fmt, code, (E, N, K))
+        ld = K
+    q = Fp4Tensor._empty(fmt, code, E, N, K, x.device)
+    B._check(B.lib().mgemm_quant_fp4(x.data_ptr(), E, N, K, ld, code, *q._ptrs, B._stream(x)), "mgemm_quant_fp4")
+    return q
 
 
 def dequantize_fp4(q):
     """The values an Fp4Tensor stands for, bf16 [E, N, K]."""
-    out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.codes.device)
-    B.mgemm_dequant_fp4(q.codes, q.scales, q.row_scale, *q.shape, q.code, out)
+    out = torch.empty(q.shape, dtype=BF16, device=q.device)
+    E, N, K = q.shape
+    B._check(B.lib().mgemm_dequant_fp4(*q._ptrs, E, N, K, q.code, out.data_ptr(), K, B._stream(out)),
+             "mgemm_dequant_fp4")
     return out
+
+
+# Workspaces of at most this many bytes are kept, one per thread, device and
+# stream (work of one stream runs in order, so its calls can share one).  Larger
+# ones are allocated per call, and so are those of a call that is being captured
+# into a graph, which goes on using the memory.
+KEPT_WORKSPACE = 16 << 20
+_kept = threading.local()
+
+
+def _workspace(nbytes, x, stream):
+    if nbytes > KEPT_WORKSPACE or torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    kept = _kept.__dict__
+    key = (x.get_device(), stream)
+    ws = kept.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = kept[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
+    return ws
 
 
 def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
     """out[rows of group e] = x[rows of group e] @ w[e]^T with 4-bit operands.
 
     x: bf16 [M, K] on the GPU, rows contiguous by expert; w: Fp4Tensor [E, N, K];
-    group_sizes: int64 [E] on the GPU, summing to M.  ``out`` (bf16 [M, N]) and
-    ``workspace`` (uint8, see mgemm_gmm_fp4_workspace_bytes; it starts with the
-    args block, for ``binding.args_status``) are allocated when not given.
-    Returns bf16 [M, N]."""
-    if not isinstance(w, Fp4Tensor):
+    group_sizes: int64 [E] on the GPU, summing to M.  ``out`` (bf16 [M, N]) is
+    allocated when not given.  ``workspace`` (uint8, see
+    mgemm_gmm_fp4_workspace_bytes): scratch that starts with the args block, for
+    ``binding.args_status``; by default the stream's own.  Returns bf16 [M, N]."""
+    if type(w) is not Fp4Tensor:
         raise B.MgemmError("gmm_fp4 takes an Fp4Tensor (see quantize_fp4)")
-    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != w.shape[2]:
-        raise B.MgemmError(f"gmm_fp4 takes bf16 x [M, {w.shape[2]}]")
+    E, N, K = w.shape
+    if x.dtype != BF16 or x.dim() != 2 or x.shape[1] != K:
+        raise B.MgemmError(f"gmm_fp4 takes bf16 x [M, {K}]")
     if x.requires_grad and torch.is_grad_enabled():
         raise B.MgemmError("gmm_fp4 has no gradient: call it under torch.no_grad() or on x.detach()")
-    E, N, K = w.shape
-    M = x.shape[0]
     if group_sizes.dtype != torch.int64 or group_sizes.numel() != E or not group_sizes.is_contiguous():
         raise B.MgemmError("group_sizes must be contiguous int64 [E]")
-    if x.stride(1) != 1 or x.stride(0) % 8 or x.stride(0) < K or x.data_ptr() % 16:
+    B._cuda(x, group_sizes, out, workspace)
+    M = x.shape[0]
+    ld, unit = x.stride()
+    if unit != 1 or ld % 8 or ld < K or x.data_ptr() % 16:
         x = x.contiguous()
+        ld = K
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    elif out.dtype != torch.bfloat16 or out.shape != (M, N) or not out.is_contiguous():
+        out = torch.empty((M, N), dtype=BF16, device=x.device)
+    elif out.dtype != BF16 or out.shape != (M, N) or not out.is_contiguous():
         raise B.MgemmError("gmm_fp4: out must be contiguous bf16 [M, N]")
+    stream = B._stream(x)
     if workspace is None:
-        workspace = torch.empty(_workspace_bytes(w.code, M, K, E), dtype=torch.uint8, device=x.device)
-    B.mgemm_gmm_fp4(group_sizes, E, w.code, x, w.codes, w.scales, w.row_scale, out, M, K, N, workspace)
+        workspace = _workspace(_workspace_bytes(w.code, M, K, E), x, stream)
+    codes, scales, rows = w._ptrs
+    B._check(B.lib().mgemm_gmm_fp4(group_sizes.data_ptr(), E, w.code, x.data_ptr(), ld, codes, scales, rows,
+                                   out.data_ptr(), M, K, N, workspace.data_ptr(), workspace.numel(), stream),
+             "mgemm_gmm_fp4")
     return out
