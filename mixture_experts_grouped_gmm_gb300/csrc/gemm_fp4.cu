@@ -22,9 +22,17 @@
 //   warps 2-9  epilogue, two per TMEM lane quarter, each half of the columns:
 //              the accumulator is read, scaled and rounded into registers,
 //              handed back, and then stored (32 bytes per lane and store)
-// TMEM: accumulators in columns 0 .. 255 (one of 256 columns or two of at most
-// 128), kSfSlots slots of scales behind them.  A slot is rewritten once the
-// MMAs that read it have completed: the stage's empty barrier says so.
+// TMEM: one accumulator of 256 columns or two narrower ones, then slots of
+// scales (four, or two beside two accumulators of 192 columns).  A slot is
+// rewritten once the MMAs that read it have completed: the stage's empty barrier
+// says so.
+// PAIR (groups of 256 rows and more): a cluster of two CTAs computes 256 rows by
+// bn columns with cta_group::2 MMAs of the even CTA.  Each CTA copies its 128
+// rows of A, half of B's columns and the scales of its rows and of all columns;
+// the odd CTA's copies complete on the even CTA's barriers, and commits free a
+// stage and publish the accumulator in both.  A CTA then fetches 38 KB per
+// stage instead of 54: what bounds large products is the rate at which L2 feeds
+// the SMs (about 48 bytes a clock each), not the MMAs (512 clocks a stage).
 // Every wait is bounded; on expiry the kernel records MGEMM_STATUS_TIMEOUT,
 // drains the copies and MMAs it issued, frees TMEM and returns.
 #include "fp4.cuh"
@@ -40,7 +48,7 @@ struct Fp4Params {
   int64_t map_limit;
   const float *row_weight;
   int K, N, E;
-  int bn, n_tiles;    // columns per tile: 64, 128 or 256
+  int bn, n_tiles;    // columns per tile: 64, 128, 192 or 256 (pairs: 128 or 256)
   int a_rows;         // rows of an A box: 128, or fewer when M is smaller (a multiple of 8)
   int stages, stage_bytes;
   int vec32;          // output rows and tiles start on 32-byte boundaries
@@ -49,18 +57,17 @@ struct Fp4Params {
 constexpr int kF4Threads = 320;
 constexpr int kF4EpiWarps = 8;
 constexpr int kF4MaxStages = 20;
-constexpr int kSfSlots = 4;
-constexpr int kSfCol0 = 256;  // first TMEM column of the scales
+constexpr int kF4Groups = 256;  // active groups whose places are kept in shared memory
 constexpr size_t kF4Limit = (size_t)227 * 1024;
 
-template <int FMT>
+template <int FMT, bool kPair>
 struct F4Cfg {
-  static constexpr bool NV = FMT == MGEMM_NVFP4;
+  static constexpr bool NV = FMT == MGEMM_NVFP4, PAIR = kPair;
   static constexpr int WPS = 256 / Fp4<FMT>::WORD;  // scale words of a row per stage: 4 or 2
-  // codes then scales; nt = scale tiles (128 columns) of the B tile
+  // a CTA's codes and scales; nt = scale tiles (128 columns) of the B tile
   static int stage_bytes(int a_rows, int bn) {
     const int nt = (bn + 127) / 128;
-    return (a_rows + bn) * 128 + (1 + nt) * WPS * 512;
+    return (a_rows + (PAIR ? bn / 2 : bn)) * 128 + (1 + nt) * WPS * 512;
   }
 };
 
@@ -69,30 +76,51 @@ struct F4Shared {
   uint32_t tmem_slot;
   int abort_flag;
   float cinv[kF4EpiWarps][128];  // the warps' column factors
+  // the active groups' first tile, expert, rows and first scale tile
+  int start[kF4Groups + 1], expert[kF4Groups], row[kF4Groups], end[kF4Groups], sf[kF4Groups];
 };
 
 struct F4Tile {
   int e, n0, rows, row0, sf_tile;
 };
 
-// The tile t: group by the row-tile prefix, row tiles fastest inside it, so
-// that CTAs running together share a weight tile through L2.
-__device__ __forceinline__ F4Tile f4_tile(int t, const Fp4Params &p, const ArgsView &av, int na) {
+// The tile t: group by the row-tile prefix (of 256-row tiles for pairs), row
+// tiles fastest inside it, so that CTAs running together share a weight tile
+// through L2.  A pair's rank takes the tile's rows 128 rank ..; the odd one's may
+// lie past the group (loaded, never stored).  Every role asks for rising tiles,
+// so the group `g` is stepped on from the last one.  The groups' places come from
+// shared memory: from the args block they are a chain of loads that mostly miss
+// L1 (shared memory takes nearly all of it), 5000 clocks a tile and role.
+template <bool PAIR>
+__device__ __forceinline__ F4Tile f4_tile(int t, int &g, const Fp4Params &p, const F4Shared &S, const ArgsView &av,
+                                          int na, int rank) {
   const int gm = t / p.n_tiles;
-  int lo = 0, hi = na - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(av.mtile_start + mid) <= gm) lo = mid; else hi = mid - 1;
-  }
-  const int first = __ldg(av.mtile_start + lo), mts = __ldg(av.mtile_start + lo + 1) - first;
   F4Tile ti;
-  ti.e = __ldg(av.active + lo);
-  const int local = t - first * p.n_tiles, mt = local % mts;
+  int first, mts, end, sf;
+  if (na <= kF4Groups) {
+    while (S.start[g + 1] <= gm) ++g;
+    first = S.start[g];
+    mts = S.start[g + 1] - first;
+    ti.e = S.expert[g];
+    ti.row0 = S.row[g];
+    end = S.end[g];
+    sf = S.sf[g];
+  } else {
+    const int *start = PAIR ? av.ptile_start : av.mtile_start;
+    while (__ldg(start + g + 1) <= gm) ++g;
+    first = __ldg(start + g);
+    mts = __ldg(start + g + 1) - first;
+    ti.e = __ldg(av.active + g);
+    ti.row0 = (int)__ldg(av.offsets + ti.e);
+    end = (int)__ldg(av.offsets + ti.e + 1);
+    sf = (int)(__ldg(av.poffsets + ti.e) >> 7);
+  }
+  const int local = t - first * p.n_tiles;
+  const int mt = PAIR ? 2 * (local % mts) + rank : local % mts;
   ti.n0 = local / mts * p.bn;
-  const int64_t rs = __ldg(av.offsets + ti.e), re = __ldg(av.offsets + ti.e + 1);
-  ti.row0 = (int)rs + mt * 128;
-  ti.rows = min((int)(re - ti.row0), p.a_rows);
-  ti.sf_tile = (int)(__ldg(av.poffsets + ti.e) >> 7) + mt;
+  ti.row0 += mt * 128;
+  ti.rows = max(0, min(end - ti.row0, p.a_rows));
+  ti.sf_tile = sf + mt;
   return ti;
 }
 
@@ -109,21 +137,33 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-template <int FMT>
+template <int FMT, bool PAIR>
 __device__ __forceinline__ void mma_f4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                        uint32_t accumulate) {
-  if (FMT == MGEMM_NVFP4)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+#define MGEMM_F4_MMA(GROUP, VEC)                                                                                      \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                     \
+               "tcgen05.mma.cta_group::" GROUP ".kind::mxf4nvf4.block_scale.scale_vec::" VEC                         \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),                                                    \
+               "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)                                       \
+               : "memory")
+  if constexpr (PAIR) {
+    if constexpr (FMT == MGEMM_NVFP4) MGEMM_F4_MMA("2", "4X");
+    else MGEMM_F4_MMA("2", "2X");
+  } else {
+    if constexpr (FMT == MGEMM_NVFP4) MGEMM_F4_MMA("1", "4X");
+    else MGEMM_F4_MMA("1", "2X");
+  }
+#undef MGEMM_F4_MMA
+}
+
+// 512 bytes of scales (32 rows of 16) to four columns of every lane quarter; a
+// pair's copy does so in both CTAs, each from its own shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void copy_scale_tile(uint32_t taddr, uint64_t sdesc) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
   else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    tmem_cp_32x128b_warpx4(taddr, sdesc);
 }
 
 // Instruction descriptor of the block-scaled 4-bit MMA: e2m1 A and B (code 1),
@@ -142,21 +182,27 @@ __device__ __forceinline__ void store_32b(void *dst, const uint32_t *v) {
                : "memory");
 }
 
-template <int FMT>
+template <int FMT, bool PAIR>
 __global__ void __launch_bounds__(kF4Threads, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                     const __grid_constant__ Fp4Params p) {
-  using C = F4Cfg<FMT>;
+  using C = F4Cfg<FMT, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // [stages x (A codes | B codes)], then the stages' scales [A tile: WPS words][B tiles: WPS words each]
   const int nst = p.stages, bn = p.bn, nt = (bn + 127) / 128;
-  const int op_bytes = (p.a_rows + bn) * 128, sf_bytes = (1 + nt) * C::WPS * 512;
+  const int b_rows = PAIR ? bn / 2 : bn;
+  const int op_bytes = (p.a_rows + b_rows) * 128, sf_bytes = (1 + nt) * C::WPS * 512;
   uint8_t *sSF = smem + (size_t)nst * op_bytes;
   F4Shared &S = *reinterpret_cast<F4Shared *>(sSF + (size_t)nst * sf_bytes);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int nacc = bn == 256 ? 1 : 2;
+  // accumulators, the columns from one to the next, and the slots of scales behind them
+  const int nacc = bn == 256 ? 1 : 2, acc_cols = bn == 192 ? 192 : 128, sf_col0 = bn == 192 ? 384 : 256;
+  const int slots = bn == 192 ? 2 : 4;
+  const int rank = PAIR ? uniform((int)cluster_ctarank()) : 0;
+  const int t_first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+  const int t_step = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
   const uint32_t op0 = (uint32_t)uniform((int)smem_u32(smem)), sf0 = op0 + (uint32_t)(nst * op_bytes);
 
   if (threadIdx.x == 0) {
@@ -166,7 +212,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&S.tfull[a], 1);
-      mbar_init(&S.tempty[a], kF4EpiWarps);
+      mbar_init(&S.tempty[a], PAIR ? 2 * kF4EpiWarps : kF4EpiWarps);
     }
     mbar_init(&S.drain, 1);
     S.abort_flag = 0;
@@ -177,36 +223,59 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     tma_prefetch_desc(&tmSB);
   }
   if (warp == 1) {
-    tmem_alloc(&S.tmem_slot, 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(&S.tmem_slot, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&S.tmem_slot, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // both CTAs' barriers are initialised before either signals the other's
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = (uint32_t)uniform((int)S.tmem_slot);
   pdl_wait();
   pdl_trigger();
   const ArgsView av(p.args, p.E);
-  const int status0 = *av.status, na = *av.n_active;
-  const int total = uniform(status0 != 0 ? 0 : __ldg(av.mtile_start + na) * p.n_tiles);
+  const int status0 = *av.status, na = uniform(*av.n_active);
+  const int total = uniform(status0 != 0 ? 0 : __ldg((PAIR ? av.ptile_start : av.mtile_start) + na) * p.n_tiles);
   const int kb_count = (p.K + 255) / 256;
+  if (total > 0 && na <= kF4Groups) {
+    const int *start = PAIR ? av.ptile_start : av.mtile_start;
+    for (int i = threadIdx.x; i < na; i += kF4Threads) {
+      const int e = __ldg(av.active + i);
+      S.start[i] = __ldg(start + i);
+      S.expert[i] = e;
+      S.row[i] = (int)__ldg(av.offsets + e);
+      S.end[i] = (int)__ldg(av.offsets + e + 1);
+      S.sf[i] = (int)(__ldg(av.poffsets + e) >> 7);
+    }
+    if (threadIdx.x == 0) S.start[na] = __ldg(start + na);
+  }
+  __syncthreads();
+  int g = 0;  // the group of the last tile
   volatile int *vabort = &S.abort_flag;
   uint32_t issued = 0;  // stages armed, for the drain after an abort
   auto timeout = [&]() {
     set_status(av.status, MGEMM_STATUS_TIMEOUT);
     *vabort = 1;
+    if constexpr (PAIR) st_cluster_u32(cluster_addr(&S.abort_flag, (uint32_t)rank ^ 1u), 1u);
   };
+  // the MMA's columns of the tile at n0 (a pair's halves stay multiples of 32)
+  auto tile_cols = [&](int n0) { return PAIR ? min(bn, (p.N - n0 + 63) & ~63) : min(bn, (p.N - n0 + 15) & ~15); };
 
   if (warp == 0) {
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    const uint32_t tx = (uint32_t)p.stage_bytes;
+    const uint32_t tx = (PAIR ? 2u : 1u) * (uint32_t)p.stage_bytes;
     const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert's weights
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const F4Tile ti = f4_tile(t, p, av, na);
+    for (int t = t_first; t < total && ok; t += t_step) {
+      const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
       const int e = uniform(ti.e), n0 = uniform(ti.n0), row0 = uniform(ti.row0), sfa_tile = uniform(ti.sf_tile);
-      const int sfb_tile = e * wtiles + n0 / 128;
+      const int sfb_tile = e * wtiles + n0 / 128, b_row = n0 + rank * (tile_cols(n0) / 2);
       for (int kb = 0; kb < kb_count; ++kb) {
         if (!mbar_wait_warp(&S.empty[stage], phase ^ 1, vabort)) {
           ok = false;
@@ -214,11 +283,19 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         }
         if (elect_one()) {
           uint8_t *a = smem + (size_t)stage * op_bytes, *sf = sSF + (size_t)stage * sf_bytes;
-          mbar_arrive_expect_tx(&S.full[stage], tx);
-          tma_load_3d(a + p.a_rows * 128, &tmB, &S.full[stage], kb * 128, n0, e);
-          tma_load_3d(sf + C::WPS * 512, &tmSB, &S.full[stage], 0, kb * C::WPS, sfb_tile);
-          tma_load_2d(a, &tmA, &S.full[stage], kb * 128, row0);
-          tma_load_3d(sf, &tmSA, &S.full[stage], 0, kb * C::WPS, sfa_tile);
+          if (!PAIR || rank == 0) {
+            mbar_arrive_expect_tx(&S.full[stage], tx);
+            tma_load_3d(a + p.a_rows * 128, &tmB, &S.full[stage], kb * 128, b_row, e);
+            tma_load_3d(sf + C::WPS * 512, &tmSB, &S.full[stage], 0, kb * C::WPS, sfb_tile);
+            tma_load_2d(a, &tmA, &S.full[stage], kb * 128, row0);
+            tma_load_3d(sf, &tmSA, &S.full[stage], 0, kb * C::WPS, sfa_tile);
+          } else {  // complete on the even CTA's barrier
+            const uint32_t bar = cluster_addr(&S.full[stage], 0);
+            tma_load_3d_pair(a + p.a_rows * 128, &tmB, bar, kb * 128, b_row, e);
+            tma_load_3d_pair(sf + C::WPS * 512, &tmSB, bar, 0, kb * C::WPS, sfb_tile);
+            tma_load_2d_pair(a, &tmA, bar, kb * 128, row0);
+            tma_load_3d_pair(sf, &tmSA, bar, 0, kb * C::WPS, sfa_tile);
+          }
         }
         __syncwarp();
         ++issued;
@@ -232,22 +309,23 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   } else if (warp == 1) {
     int stage = 0, acc = 0, slot = 0;
     uint32_t phase = 0, acc_phase = 0;
-    int old = 0;  // the stage of kSfSlots iterations ago, and its phase
-    uint32_t old_phase = 0, it = 0;
+    int old = 0;  // the stage of `slots` iterations ago, and its phase
+    uint32_t old_phase = 0;
+    int it = 0;
     bool ok = true;
     const uint32_t sfc = (uint32_t)(C::WPS * (4 + 4 * nt));  // TMEM columns of a slot
-    for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-      const F4Tile ti = f4_tile(t, p, av, na);
+    // (a pair: the even CTA issues for both)
+    for (int t = t_first; t < total && ok && rank == 0; t += t_step) {
+      const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
       const int n0 = uniform(ti.n0);
       if (!mbar_wait_warp(&S.tempty[acc], acc_phase ^ 1, vabort)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * 128;
-      const int cols = min(bn, (p.N - n0 + 15) & ~15);
-      const uint32_t idesc = f4_idesc(128, cols, C::NV ? 0u : 1u);
-      // a 64-column tile may start in the middle of a 128-column scale tile
+      const uint32_t d_tmem = tmem_base + acc * acc_cols;
+      const uint32_t idesc = f4_idesc(PAIR ? 256 : 128, tile_cols(n0), C::NV ? 0u : 1u);
+      // a tile of 64 or 192 columns may start in the middle of a 128-column scale tile
       const uint32_t sfb_off = (n0 & 64) ? 2u : 0u;
       for (int kb = 0; kb < kb_count; ++kb) {
         if (!mbar_wait_warp(&S.full[stage], phase, vabort)) {
@@ -255,7 +333,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
           break;
         }
         // the slot's last readers have completed (a ring of no more stages than slots says so by itself)
-        if (it >= kSfSlots && nst > kSfSlots) {
+        if (it >= slots && nst > slots) {
           if (!mbar_wait_warp(&S.empty[old], old_phase, vabort)) {
             ok = false;
             break;
@@ -265,22 +343,22 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             old_phase ^= 1;
           }
         }
-        ++it;
+        it += it < slots;
         tc_fence_after();
         if (elect_one()) {
           const uint32_t a = op0 + (uint32_t)(stage * op_bytes), sf = sf0 + (uint32_t)(stage * sf_bytes);
-          const uint32_t sfa_t = tmem_base + kSfCol0 + slot * sfc, sfb_t = sfa_t + 4 * C::WPS;
+          const uint32_t sfa_t = tmem_base + sf_col0 + slot * sfc, sfb_t = sfa_t + 4 * C::WPS;
           const uint64_t ad = smem_desc_sw128(a, 16, 1024), bd = smem_desc_sw128(a + p.a_rows * 128, 16, 1024);
           const uint64_t sd = smem_desc_rows16(sf);  // (descriptors advance by bytes >> 4)
           auto copy_scales = [&](int j) {
-            tmem_cp_32x128b_warpx4(sfa_t + 4 * j, sd + 32 * j);
-            tmem_cp_32x128b_warpx4(sfb_t + 4 * j * nt, sd + 32 * (C::WPS + j));
-            if (nt == 2) tmem_cp_32x128b_warpx4(sfb_t + 4 * j * nt + 4, sd + 32 * (2 * C::WPS + j));
+            copy_scale_tile<PAIR>(sfa_t + 4 * j, sd + 32 * j);
+            copy_scale_tile<PAIR>(sfb_t + 4 * j * nt, sd + 32 * (C::WPS + j));
+            if (nt == 2) copy_scale_tile<PAIR>(sfb_t + 4 * j * nt + 4, sd + 32 * (2 * C::WPS + j));
           };
           auto step = [&](int k) {
             const int j = C::NV ? k : k / 2;
             const uint32_t id = C::NV ? 0u : (uint32_t)(k & 1) * 2u;
-            mma_f4<FMT>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), sfa_t + 4 * j,
+            mma_f4<FMT, PAIR>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), sfa_t + 4 * j,
                         sfb_t + 4 * j * nt + sfb_off, (kb | k) != 0);
           };
           if (kb * 256 + 256 <= p.K) {
@@ -293,17 +371,21 @@ __global__ void __launch_bounds__(kF4Threads, 1)
             for (int j = 0; j < words; ++j) copy_scales(j);
             for (int k = 0; k < steps; ++k) step(k);
           }
-          mma_commit(&S.empty[stage]);
+          if constexpr (PAIR) mma_commit_pair(&S.empty[stage], 0x3);
+          else mma_commit(&S.empty[stage]);
         }
         __syncwarp();
-        if (++slot == kSfSlots) slot = 0;
+        if (++slot == slots) slot = 0;
         if (++stage == nst) {
           stage = 0;
           phase ^= 1;
         }
       }
       if (!ok) break;
-      if (elect_one()) mma_commit(&S.tfull[acc]);
+      if (elect_one()) {
+        if constexpr (PAIR) mma_commit_pair(&S.tfull[acc], 0x3);
+        else mma_commit(&S.tfull[acc]);
+      }
       __syncwarp();
       if (++acc == nacc) {
         acc = 0;
@@ -311,20 +393,21 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       }
     }
     if (!ok && lane == 0) timeout();
-    if (elect_one()) {
-      mma_commit(&S.drain);
+    if (rank == 0 && elect_one()) {
+      if constexpr (PAIR) mma_commit_pair(&S.drain, 0x1);
+      else mma_commit(&S.drain);
       mbar_wait_drain(&S.drain, 0);
     }
     __syncwarp();
   } else {
     const int ew = warp - 2, q = warp & 3, h = ew >> 2;
     const int r = q * 32 + lane;   // the thread's row of the tile
-    const int half = bn / 2;       // columns per warp: 32, 64 or 128
+    const int half = bn / 2;       // columns per warp: 32, 64, 96 or 128
     float *cinv = S.cinv[ew];
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = blockIdx.x; t < total; t += gridDim.x) {
-      const F4Tile ti = f4_tile(t, p, av, na);
+    for (int t = t_first; t < total; t += t_step) {
+      const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
       const int col0 = ti.n0 + h * half;
       bool row_ok = r < ti.rows;
       int64_t dst = (int64_t)ti.row0 + r;
@@ -348,7 +431,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * 128 + h * half;
+      const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * acc_cols + h * half;
       uint32_t pk[4][16];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -370,7 +453,10 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&S.tempty[acc]);
+      if (lane == 0) {
+        if (rank == 0) mbar_arrive(&S.tempty[acc]);
+        else mbar_arrive_cluster(cluster_addr(&S.tempty[acc], 0));
+      }
       if (++acc == nacc) {
         acc = 0;
         acc_phase ^= 1;
@@ -401,35 +487,31 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   __syncthreads();
   if (*vabort && warp == 0 && lane == 0) {
     // wait for the copies this CTA armed, bounded
-    for (int i = 0; i < nst; ++i) {
+    for (int i = 0; i < nst && rank == 0; ++i) {
       const uint32_t armed = issued / nst + ((uint32_t)i < issued % nst ? 1u : 0u);
       if (armed) mbar_wait_drain(&S.full[i], (armed - 1) & 1);
     }
-  }
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, 512);
-  }
-}
-
-template <int FMT>
-int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, Fp4Params p, int64_t M,
-               int sms, cudaStream_t s) {
-  using C = F4Cfg<FMT>;
-  const int E = p.E, K = p.K, N = p.N;
-  // columns per tile: the fewest rounds of tiles over the SMs, weighted by the
-  // columns plus a tile's fixed cost; wider at equal cost (fewer reads of A)
-  const int64_t groups = M < E ? M : E, m_est = (M + 127) / 128 > groups ? (M + 127) / 128 : groups;
-  int bn = 256;
-  int64_t best = -1;
-  for (int c : {256, 128, 64}) {
-    const int64_t cost = (m_est * ((N + c - 1) / c) + sms - 1) / sms * (c + 32);
-    if (best < 0 || cost < best) {
-      best = cost;
-      bn = c;
+    // pair: copies of a CTA that the other's barriers never counted get far longer than a copy takes
+    if constexpr (PAIR) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 100000ull) __nanosleep(1000);
     }
   }
+  if constexpr (PAIR) cluster_sync();  // every MMA into either CTA's TMEM and every remote arrival is done
+  else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem_base, 512);
+    else tmem_dealloc(tmem_base, 512);
+  }
+  if constexpr (PAIR) cluster_sync();  // neither CTA leaves while the other may still address it
+}
+
+template <int FMT, bool PAIR>
+int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, Fp4Params p, int64_t M, int bn,
+               int sms, cudaStream_t s) {
+  using C = F4Cfg<FMT, PAIR>;
+  const int E = p.E, K = p.K, N = p.N;
   p.bn = bn;
   p.n_tiles = (N + bn - 1) / bn;
   p.a_rows = M < 128 ? (int)((M + 7) / 8 * 8) : 128;
@@ -451,7 +533,7 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
   {
     const uint64_t d[3] = {(uint64_t)K / 2, (uint64_t)N, (uint64_t)E};
     const uint64_t str[2] = {(uint64_t)K / 2, (uint64_t)N * (K / 2)};
-    const uint32_t box[3] = {128, (uint32_t)bn, 1};
+    const uint32_t box[3] = {128, (uint32_t)(PAIR ? bn / 2 : bn), 1};
     if (!make_tensor_map(&tb, true, 3, w, d, str, box)) return MGEMM_ECUDA;
   }
   // scales: 512-byte word tiles as 256 two-byte elements, {256, words, row tiles}
@@ -469,15 +551,40 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
   if (rc) return rc;
   if (dev < 0 || dev >= 64) return MGEMM_EINVAL;
   if (!attr_done[dev]) {
-    rc = cuda_rc(cudaFuncSetAttribute(fp4_gemm_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kF4Limit),
+    rc = cuda_rc(cudaFuncSetAttribute(fp4_gemm_kernel<FMT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)kF4Limit),
                  "cudaFuncSetAttribute");
     if (rc) return rc;
     attr_done[dev] = true;
   }
-  const int64_t upper = ((M + 127) / 128 + groups) * p.n_tiles;
-  const unsigned grid = (unsigned)(upper < sms ? upper : sms);
-  return launch_pdl(fp4_gemm_kernel<FMT>, dim3(grid), dim3(kF4Threads), smem, s, 1, "mgemm_fwd_fp4 launch", ta, tb, tsa,
-                    tsb, p);
+  const int64_t groups = M < E ? M : E;
+  const int64_t upper = PAIR ? 2 * ((M + 255) / 256 + groups) * p.n_tiles : ((M + 127) / 128 + groups) * p.n_tiles;
+  const int64_t cap = PAIR ? sms / 2 * 2 : sms;
+  const unsigned grid = (unsigned)(upper < cap ? upper : cap);
+  return launch_pdl(fp4_gemm_kernel<FMT, PAIR>, dim3(grid), dim3(kF4Threads), smem, s, PAIR ? 2u : 1u,
+                    PAIR ? "mgemm_fwd_fp4 launch (CTA pairs)" : "mgemm_fwd_fp4 launch", ta, tb, tsa, tsb, p);
+}
+
+template <int FMT>
+int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, const Fp4Params &p, int64_t M,
+               int sms, cudaStream_t s) {
+  const int64_t groups = M < p.E ? M : p.E;
+  // pairs where the groups hold 256 rows on average
+  if (M >= 256 * groups) return launch_fp4<FMT, true>(x, sx, w, sw, p, M, p.N > 128 ? 256 : 128, sms, s);
+  // columns per tile: the fewest rounds of tiles over the SMs, weighted by the bytes of a stage
+  // (A's rows, the columns and their scales) ; wider at equal cost (fewer reads of A)
+  const int64_t m_est = (M + 127) / 128 > groups ? (M + 127) / 128 : groups;
+  const int a_rows = M < 128 ? (int)M : 128;
+  int bn = 256;
+  int64_t best = -1;
+  for (int c : {256, 192, 128, 64}) {
+    const int64_t cost = (m_est * ((p.N + c - 1) / c) + sms - 1) / sms * (F4Cfg<FMT, false>::stage_bytes(a_rows, c) + 2048);
+    if (best < 0 || cost < best) {
+      best = cost;
+      bn = c;
+    }
+  }
+  return launch_fp4<FMT, false>(x, sx, w, sw, p, M, bn, sms, s);
 }
 
 bool a16(const void *p) { return ((uintptr_t)p & 15) == 0; }

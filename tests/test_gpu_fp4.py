@@ -181,6 +181,23 @@ def test_product(fmt, sizes, K, N):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("sizes,K,N", [
+    ([256], 256, 64), ([257], 320, 72), ([700], 1056, 1408), ([512, 300, 256], 512, 648), ([1, 1200, 0, 100], 768, 264),
+    ([5000, 3, 4000], 288, 392), ([300] * 9, 2080, 1000),
+])
+def test_product_on_cta_pairs(fmt, sizes, K, N):
+    check_product(sizes, K, N, fmt, seed=len(sizes) + K + N)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("sizes,K,N", [
+    ([100], 512, 24 * 192 + 8), ([130, 0, 20, 90], 288, 1544), ([128] * 8, 640, 6400), ([9] * 40, 256, 1344),
+])
+def test_product_tile_widths(fmt, sizes, K, N):
+    check_product(sizes, K, N, fmt, seed=len(sizes) + K + N)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_product_strided_rows_and_many_experts(fmt):
     check_product([2, 0, 40], 192, 128, fmt, 1, ld=208)
     sizes = [0] * 1024
