@@ -22,10 +22,9 @@
 //   warps 2-9  epilogue, two per TMEM lane quarter, each half of the columns:
 //              the accumulator is read, scaled and rounded into registers,
 //              handed back, and then stored (32 bytes per lane and store)
-// TMEM: one accumulator of 256 columns or two narrower ones, then slots of
-// scales (four, or two beside two accumulators of 192 columns).  A slot is
-// rewritten once the MMAs that read it have completed: the stage's empty barrier
-// says so.
+// TMEM: one accumulator of 256 columns or two narrower ones, then as many slots
+// of scales as fit (two to ten).  A slot is rewritten once the MMAs that read it
+// have completed: the stage's empty barrier says so.
 // PAIR (groups of 256 rows and more): a cluster of two CTAs computes 256 rows by
 // bn columns with cta_group::2 MMAs of the even CTA.  Each CTA copies its 128
 // rows of A, half of B's columns and the scales of its rows and of all columns;
@@ -135,7 +134,17 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
   return p != 0;
 }
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+// v, which every lane holds alike, as a result the compiler knows to be uniform
+// (a warp reduction is written to a uniform register).
+__device__ __forceinline__ int uniform(int v) { return (int)__reduce_or_sync(0xffffffffu, (unsigned)v); }
+
+// Arrive on an mbarrier of the pair's other CTA.  The order that matters, of the
+// accumulator's reads before it is written again, is the tcgen05 fence's; a
+// release at cluster scope would also wait for the SM's output stores (3000
+// clocks a tile).
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
 
 template <int FMT, bool PAIR>
 __device__ __forceinline__ void mma_f4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb,
@@ -182,7 +191,8 @@ __device__ __forceinline__ void store_32b(void *dst, const uint32_t *v) {
                : "memory");
 }
 
-template <int FMT, bool PAIR>
+// NT: scale tiles (128 columns) of a column tile
+template <int FMT, bool PAIR, int NT>
 __global__ void __launch_bounds__(kF4Threads, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
@@ -191,15 +201,16 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   // [stages x (A codes | B codes)], then the stages' scales [A tile: WPS words][B tiles: WPS words each]
-  const int nst = p.stages, bn = p.bn, nt = (bn + 127) / 128;
+  const int nst = p.stages, bn = p.bn;
   const int b_rows = PAIR ? bn / 2 : bn;
-  const int op_bytes = (p.a_rows + b_rows) * 128, sf_bytes = (1 + nt) * C::WPS * 512;
+  const int op_bytes = (p.a_rows + b_rows) * 128, sf_bytes = (1 + NT) * C::WPS * 512;
   uint8_t *sSF = smem + (size_t)nst * op_bytes;
   F4Shared &S = *reinterpret_cast<F4Shared *>(sSF + (size_t)nst * sf_bytes);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   // accumulators, the columns from one to the next, and the slots of scales behind them
   const int nacc = bn == 256 ? 1 : 2, acc_cols = bn == 192 ? 192 : 128, sf_col0 = bn == 192 ? 384 : 256;
-  const int slots = bn == 192 ? 2 : 4;
+  constexpr int kSlotCols = C::WPS * (4 + 4 * NT);
+  const int slots = (512 - sf_col0) / kSlotCols;
   const int rank = PAIR ? uniform((int)cluster_ctarank()) : 0;
   const int t_first = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
   const int t_step = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
@@ -313,7 +324,6 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     uint32_t old_phase = 0;
     int it = 0;
     bool ok = true;
-    const uint32_t sfc = (uint32_t)(C::WPS * (4 + 4 * nt));  // TMEM columns of a slot
     // (a pair: the even CTA issues for both)
     for (int t = t_first; t < total && ok && rank == 0; t += t_step) {
       const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
@@ -323,10 +333,10 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t d_tmem = tmem_base + acc * acc_cols;
-      const uint32_t idesc = f4_idesc(PAIR ? 256 : 128, tile_cols(n0), C::NV ? 0u : 1u);
+      const uint32_t d_tmem = (uint32_t)uniform((int)tmem_base + acc * acc_cols);
+      const uint32_t idesc = (uint32_t)uniform((int)f4_idesc(PAIR ? 256 : 128, tile_cols(n0), C::NV ? 0u : 1u));
       // a tile of 64 or 192 columns may start in the middle of a 128-column scale tile
-      const uint32_t sfb_off = (n0 & 64) ? 2u : 0u;
+      const uint32_t sfb_off = (uint32_t)uniform((n0 & 64) ? 2 : 0);
       for (int kb = 0; kb < kb_count; ++kb) {
         if (!mbar_wait_warp(&S.full[stage], phase, vabort)) {
           ok = false;
@@ -345,21 +355,22 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         }
         it += it < slots;
         tc_fence_after();
+        const uint32_t a = (uint32_t)uniform((int)op0 + stage * op_bytes);
+        const uint32_t sf = (uint32_t)uniform((int)sf0 + stage * sf_bytes);
+        const uint32_t sfa_t = (uint32_t)uniform((int)tmem_base + sf_col0 + slot * kSlotCols), sfb_t = sfa_t + 4 * C::WPS;
         if (elect_one()) {
-          const uint32_t a = op0 + (uint32_t)(stage * op_bytes), sf = sf0 + (uint32_t)(stage * sf_bytes);
-          const uint32_t sfa_t = tmem_base + sf_col0 + slot * sfc, sfb_t = sfa_t + 4 * C::WPS;
           const uint64_t ad = smem_desc_sw128(a, 16, 1024), bd = smem_desc_sw128(a + p.a_rows * 128, 16, 1024);
           const uint64_t sd = smem_desc_rows16(sf);  // (descriptors advance by bytes >> 4)
           auto copy_scales = [&](int j) {
             copy_scale_tile<PAIR>(sfa_t + 4 * j, sd + 32 * j);
-            copy_scale_tile<PAIR>(sfb_t + 4 * j * nt, sd + 32 * (C::WPS + j));
-            if (nt == 2) copy_scale_tile<PAIR>(sfb_t + 4 * j * nt + 4, sd + 32 * (2 * C::WPS + j));
+            copy_scale_tile<PAIR>(sfb_t + 4 * j * NT, sd + 32 * (C::WPS + j));
+            if (NT == 2) copy_scale_tile<PAIR>(sfb_t + 4 * j * NT + 4, sd + 32 * (2 * C::WPS + j));
           };
           auto step = [&](int k) {
             const int j = C::NV ? k : k / 2;
             const uint32_t id = C::NV ? 0u : (uint32_t)(k & 1) * 2u;
             mma_f4<FMT, PAIR>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), sfa_t + 4 * j,
-                        sfb_t + 4 * j * nt + sfb_off, (kb | k) != 0);
+                        sfb_t + 4 * j * NT + sfb_off, (kb | k) != 0);
           };
           if (kb * 256 + 256 <= p.K) {
 #pragma unroll
@@ -455,7 +466,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       __syncwarp();
       if (lane == 0) {
         if (rank == 0) mbar_arrive(&S.tempty[acc]);
-        else mbar_arrive_cluster(cluster_addr(&S.tempty[acc], 0));
+        else mbar_arrive_remote(cluster_addr(&S.tempty[acc], 0));
       }
       if (++acc == nacc) {
         acc = 0;
@@ -507,7 +518,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   if constexpr (PAIR) cluster_sync();  // neither CTA leaves while the other may still address it
 }
 
-template <int FMT, bool PAIR>
+template <int FMT, bool PAIR, int NT>
 int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, Fp4Params p, int64_t M, int bn,
                int sms, cudaStream_t s) {
   using C = F4Cfg<FMT, PAIR>;
@@ -523,7 +534,7 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
   if (st > kF4MaxStages) st = kF4MaxStages;
   p.stages = st;
   const size_t smem = fixed + (size_t)st * p.stage_bytes;
-  const int W = fp4_words(FMT, K), nt = (bn + 127) / 128;
+  const int W = fp4_words(FMT, K);
   CUtensorMap ta, tb, tsa, tsb;
   {
     const uint64_t d[2] = {(uint64_t)K / 2, (uint64_t)M}, str[1] = {(uint64_t)K / 2};
@@ -544,14 +555,14 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
     return make_tensor_map(m, false, 3, base, d, str, box, false);
   };
   if (!sf_map(&tsa, sx, mgemm_colwise_ld(M, E) / 128, 1)) return MGEMM_ECUDA;
-  if (!sf_map(&tsb, sw, (int64_t)E * ((N + 127) / 128), nt)) return MGEMM_ECUDA;
+  if (!sf_map(&tsb, sw, (int64_t)E * ((N + 127) / 128), NT)) return MGEMM_ECUDA;
   static bool attr_done[64] = {};
   int dev = 0;
   int rc = cuda_rc(cudaGetDevice(&dev), "cudaGetDevice");
   if (rc) return rc;
   if (dev < 0 || dev >= 64) return MGEMM_EINVAL;
   if (!attr_done[dev]) {
-    rc = cuda_rc(cudaFuncSetAttribute(fp4_gemm_kernel<FMT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    rc = cuda_rc(cudaFuncSetAttribute(fp4_gemm_kernel<FMT, PAIR, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       (int)kF4Limit),
                  "cudaFuncSetAttribute");
     if (rc) return rc;
@@ -561,7 +572,7 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
   const int64_t upper = PAIR ? 2 * ((M + 255) / 256 + groups) * p.n_tiles : ((M + 127) / 128 + groups) * p.n_tiles;
   const int64_t cap = PAIR ? sms / 2 * 2 : sms;
   const unsigned grid = (unsigned)(upper < cap ? upper : cap);
-  return launch_pdl(fp4_gemm_kernel<FMT, PAIR>, dim3(grid), dim3(kF4Threads), smem, s, PAIR ? 2u : 1u,
+  return launch_pdl(fp4_gemm_kernel<FMT, PAIR, NT>, dim3(grid), dim3(kF4Threads), smem, s, PAIR ? 2u : 1u,
                     PAIR ? "mgemm_fwd_fp4 launch (CTA pairs)" : "mgemm_fwd_fp4 launch", ta, tb, tsa, tsb, p);
 }
 
@@ -570,7 +581,9 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
                int sms, cudaStream_t s) {
   const int64_t groups = M < p.E ? M : p.E;
   // pairs where the groups hold 256 rows on average
-  if (M >= 256 * groups) return launch_fp4<FMT, true>(x, sx, w, sw, p, M, p.N > 128 ? 256 : 128, sms, s);
+  if (M >= 256 * groups)
+    return p.N > 128 ? launch_fp4<FMT, true, 2>(x, sx, w, sw, p, M, 256, sms, s)
+                     : launch_fp4<FMT, true, 1>(x, sx, w, sw, p, M, 128, sms, s);
   // columns per tile: the fewest rounds of tiles over the SMs, weighted by the bytes of a stage
   // (A's rows, the columns and their scales) ; wider at equal cost (fewer reads of A)
   const int64_t m_est = (M + 127) / 128 > groups ? (M + 127) / 128 : groups;
@@ -584,7 +597,8 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
       bn = c;
     }
   }
-  return launch_fp4<FMT, false>(x, sx, w, sw, p, M, bn, sms, s);
+  return bn > 128 ? launch_fp4<FMT, false, 2>(x, sx, w, sw, p, M, bn, sms, s)
+                  : launch_fp4<FMT, false, 1>(x, sx, w, sw, p, M, bn, sms, s);
 }
 
 bool a16(const void *p) { return ((uintptr_t)p & 15) == 0; }
