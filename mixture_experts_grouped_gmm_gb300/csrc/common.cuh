@@ -22,10 +22,10 @@ inline int cuda_rc(cudaError_t e, const char *where) {
   return MGEMM_ECUDA;
 }
 
-// Tiled tensor map with 128-byte swizzle (or none) and zero fill outside the
-// tensor (dims[0] contiguous; strides in bytes for dims 1..rank-1).
+// Tiled tensor map with 128-byte swizzle (or none, or 64-byte) and zero fill outside
+// the tensor (dims[0] contiguous; strides in bytes for dims 1..rank-1).
 bool make_tensor_map(CUtensorMap *m, bool byte_elems, int rank, const void *base, const uint64_t *dims,
-                     const uint64_t *strides, const uint32_t *box, bool swizzle128 = true);
+                     const uint64_t *strides, const uint32_t *box, bool swizzle128 = true, bool swizzle64 = false);
 // cuTensorMapEncodeTiled needs a current context; a thread that has made no
 // CUDA call yet (an autograd worker, say) has none.  Makes the current
 // device's primary context current, once per thread.

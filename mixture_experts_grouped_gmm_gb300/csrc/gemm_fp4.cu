@@ -16,12 +16,19 @@
 // them there (tcgen05.cp, 512 bytes per 128 rows and word) ahead of the
 // stage's four MMAs.
 //
-// CTA (persistent, one per SM, 320 threads):
+// CTA (persistent, one per SM, 352 threads):
 //   warp 0     TMA producer: a ring of stages, as many as fit
-//   warp 1     TMEM owner; one thread copies scales and issues MMAs
+//   warp 1     TMEM owner; issues the MMAs
+//   warp 10    copies a stage's scales to tensor memory ahead of its MMAs (12
+//              copies of a 256-column stage cost the issuing warp as long as the
+//              MMAs take)
 //   warps 2-9  epilogue, two per TMEM lane quarter, each half of the columns:
 //              the accumulator is read, scaled and rounded into registers,
-//              handed back, and then stored (32 bytes per lane and store)
+//              handed back, and then stored, 32 columns at a time, through a
+//              swizzled 2 KB buffer and TMA (stores of 32 rows from registers
+//              hold up the load-store unit for some 3000 clocks a tile, and
+//              with it every barrier of the pipeline); rows of a group's edge
+//              and scattered rows are stored directly
 // TMEM: one accumulator of 256 columns or two narrower ones, then as many slots
 // of scales as fit (two to ten).  A slot is rewritten once the MMAs that read it
 // have completed: the stage's empty barrier says so.
@@ -53,10 +60,12 @@ struct Fp4Params {
   int vec32;          // output rows and tiles start on 32-byte boundaries
 };
 
-constexpr int kF4Threads = 320;
+constexpr int kF4Threads = 352;
 constexpr int kF4EpiWarps = 8;
 constexpr int kF4MaxStages = 20;
-constexpr int kF4Groups = 256;  // active groups whose places are kept in shared memory
+constexpr int kF4MaxSlots = 16;  // slots of scales in tensor memory
+constexpr int kF4Groups = 128;  // active groups whose places are kept in shared memory
+constexpr int kF4Stage = 32 * 64;  // bytes of an epilogue warp's staging buffer: 32 rows of 32 columns
 constexpr size_t kF4Limit = (size_t)227 * 1024;
 
 template <int FMT, bool kPair>
@@ -71,7 +80,7 @@ struct F4Cfg {
 };
 
 struct F4Shared {
-  uint64_t full[kF4MaxStages], empty[kF4MaxStages], tfull[2], tempty[2], drain;
+  uint64_t full[kF4MaxStages], empty[kF4MaxStages], tfull[2], tempty[2], drain, sf_ready[kF4MaxSlots], sf_drain;
   uint32_t tmem_slot;
   int abort_flag;
   float cinv[kF4EpiWarps][128];  // the warps' column factors
@@ -182,6 +191,17 @@ __device__ __forceinline__ uint32_t f4_idesc(int m, int n, uint32_t ue8m0) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (ue8m0 << 23) | ((uint32_t)(m >> 4) << 24);
 }
 
+__device__ __forceinline__ uint64_t f32x2(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) { return f32x2(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16x2_u64(uint64_t v) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
 // 1 / s of a power of two s
 __device__ __forceinline__ float f4_recip(float s) { return __uint_as_float(0x7F000000u - __float_as_uint(s)); }
 
@@ -196,7 +216,7 @@ template <int FMT, bool PAIR, int NT>
 __global__ void __launch_bounds__(kF4Threads, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
-                    const __grid_constant__ Fp4Params p) {
+                    const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ Fp4Params p) {
   using C = F4Cfg<FMT, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -205,7 +225,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   const int b_rows = PAIR ? bn / 2 : bn;
   const int op_bytes = (p.a_rows + b_rows) * 128, sf_bytes = (1 + NT) * C::WPS * 512;
   uint8_t *sSF = smem + (size_t)nst * op_bytes;
-  F4Shared &S = *reinterpret_cast<F4Shared *>(sSF + (size_t)nst * sf_bytes);
+  uint8_t *sOut = sSF + (size_t)nst * sf_bytes;  // the epilogue's staging buffers (512-byte aligned)
+  F4Shared &S = *reinterpret_cast<F4Shared *>(sOut + kF4EpiWarps * kF4Stage);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
   // accumulators, the columns from one to the next, and the slots of scales behind them
   const int nacc = bn == 256 ? 1 : 2, acc_cols = bn == 192 ? 192 : 128, sf_col0 = bn == 192 ? 384 : 256;
@@ -225,13 +246,16 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       mbar_init(&S.tfull[a], 1);
       mbar_init(&S.tempty[a], PAIR ? 2 * kF4EpiWarps : kF4EpiWarps);
     }
+    for (int i = 0; i < kF4MaxSlots; ++i) mbar_init(&S.sf_ready[i], 1);
     mbar_init(&S.drain, 1);
+    mbar_init(&S.sf_drain, 1);
     S.abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmSA);
     tma_prefetch_desc(&tmSB);
+    tma_prefetch_desc(&tmOut);
   }
   if (warp == 1) {
     if constexpr (PAIR) {
@@ -319,74 +343,53 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     if (!ok && lane == 0) timeout();
   } else if (warp == 1) {
     int stage = 0, acc = 0, slot = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    int old = 0;  // the stage of `slots` iterations ago, and its phase
-    uint32_t old_phase = 0;
-    int it = 0;
+    uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
     bool ok = true;
     // (a pair: the even CTA issues for both)
     for (int t = t_first; t < total && ok && rank == 0; t += t_step) {
       const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
       const int n0 = uniform(ti.n0);
+      const uint32_t idesc = (uint32_t)uniform((int)f4_idesc(PAIR ? 256 : 128, tile_cols(n0), C::NV ? 0u : 1u));
+      // a tile of 64 or 192 columns may start in the middle of a 128-column scale tile
+      const uint32_t sfb_off = (uint32_t)uniform((n0 & 64) ? 2 : 0);
+      const uint32_t d_tmem = (uint32_t)uniform((int)tmem_base + acc * acc_cols);
       if (!mbar_wait_warp(&S.tempty[acc], acc_phase ^ 1, vabort)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const uint32_t d_tmem = (uint32_t)uniform((int)tmem_base + acc * acc_cols);
-      const uint32_t idesc = (uint32_t)uniform((int)f4_idesc(PAIR ? 256 : 128, tile_cols(n0), C::NV ? 0u : 1u));
-      // a tile of 64 or 192 columns may start in the middle of a 128-column scale tile
-      const uint32_t sfb_off = (uint32_t)uniform((n0 & 64) ? 2 : 0);
       for (int kb = 0; kb < kb_count; ++kb) {
-        if (!mbar_wait_warp(&S.full[stage], phase, vabort)) {
+        const uint32_t a = (uint32_t)uniform((int)op0 + stage * op_bytes);
+        const uint32_t sfa_t = (uint32_t)uniform((int)tmem_base + sf_col0 + slot * kSlotCols), sfb_t = sfa_t + 4 * C::WPS;
+        const bool here = mbar_wait(&S.full[stage], phase, vabort) && mbar_wait(&S.sf_ready[slot], slot_phase, vabort);
+        if (!__all_sync(0xffffffffu, here)) {
           ok = false;
           break;
         }
-        // the slot's last readers have completed (a ring of no more stages than slots says so by itself)
-        if (it >= slots && nst > slots) {
-          if (!mbar_wait_warp(&S.empty[old], old_phase, vabort)) {
-            ok = false;
-            break;
-          }
-          if (++old == nst) {
-            old = 0;
-            old_phase ^= 1;
-          }
-        }
-        it += it < slots;
         tc_fence_after();
-        const uint32_t a = (uint32_t)uniform((int)op0 + stage * op_bytes);
-        const uint32_t sf = (uint32_t)uniform((int)sf0 + stage * sf_bytes);
-        const uint32_t sfa_t = (uint32_t)uniform((int)tmem_base + sf_col0 + slot * kSlotCols), sfb_t = sfa_t + 4 * C::WPS;
         if (elect_one()) {
           const uint64_t ad = smem_desc_sw128(a, 16, 1024), bd = smem_desc_sw128(a + p.a_rows * 128, 16, 1024);
-          const uint64_t sd = smem_desc_rows16(sf);  // (descriptors advance by bytes >> 4)
-          auto copy_scales = [&](int j) {
-            copy_scale_tile<PAIR>(sfa_t + 4 * j, sd + 32 * j);
-            copy_scale_tile<PAIR>(sfb_t + 4 * j * NT, sd + 32 * (C::WPS + j));
-            if (NT == 2) copy_scale_tile<PAIR>(sfb_t + 4 * j * NT + 4, sd + 32 * (2 * C::WPS + j));
-          };
-          auto step = [&](int k) {
+          auto step = [&](int k) {  // (descriptors advance by bytes >> 4)
             const int j = C::NV ? k : k / 2;
             const uint32_t id = C::NV ? 0u : (uint32_t)(k & 1) * 2u;
             mma_f4<FMT, PAIR>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), sfa_t + 4 * j,
-                        sfb_t + 4 * j * NT + sfb_off, (kb | k) != 0);
+                              sfb_t + 4 * j * NT + sfb_off, (kb | k) != 0);
           };
           if (kb * 256 + 256 <= p.K) {
 #pragma unroll
-            for (int j = 0; j < C::WPS; ++j) copy_scales(j);
-#pragma unroll
             for (int k = 0; k < 4; ++k) step(k);
           } else {  // the contraction ends inside this stage
-            const int steps = (p.K - kb * 256 + 63) / 64, words = C::NV ? steps : (steps + 1) / 2;
-            for (int j = 0; j < words; ++j) copy_scales(j);
+            const int steps = (p.K - kb * 256 + 63) / 64;
             for (int k = 0; k < steps; ++k) step(k);
           }
           if constexpr (PAIR) mma_commit_pair(&S.empty[stage], 0x3);
           else mma_commit(&S.empty[stage]);
         }
         __syncwarp();
-        if (++slot == slots) slot = 0;
+        if (++slot == slots) {
+          slot = 0;
+          slot_phase ^= 1;
+        }
         if (++stage == nst) {
           stage = 0;
           phase ^= 1;
@@ -408,6 +411,60 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       if constexpr (PAIR) mma_commit_pair(&S.drain, 0x1);
       else mma_commit(&S.drain);
       mbar_wait_drain(&S.drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == 2 + kF4EpiWarps) {
+    int stage = 0, slot = 0, old = 0, it = 0;  // old: the stage of `slots` iterations ago
+    uint32_t phase = 0, old_phase = 0;
+    bool ok = true;
+    for (int t = t_first; t < total && ok && rank == 0; t += t_step) {
+      for (int kb = 0; kb < kb_count; ++kb) {
+        const uint32_t sf = (uint32_t)uniform((int)sf0 + stage * sf_bytes);
+        const uint32_t sfa_t = (uint32_t)uniform((int)tmem_base + sf_col0 + slot * kSlotCols), sfb_t = sfa_t + 4 * C::WPS;
+        bool here = mbar_wait(&S.full[stage], phase, vabort);
+        // the slot's last readers have completed (a ring of no more stages than slots says so by itself)
+        const bool reuse = it >= slots && nst > slots;
+        if (reuse) here = here && mbar_wait(&S.empty[old], old_phase, vabort);
+        if (!__all_sync(0xffffffffu, here)) {
+          ok = false;
+          break;
+        }
+        if (reuse && ++old == nst) {
+          old = 0;
+          old_phase ^= 1;
+        }
+        it += it < slots;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t sd = smem_desc_rows16(sf);
+          auto copy = [&](int j) {
+            copy_scale_tile<PAIR>(sfa_t + 4 * j, sd + 32 * j);
+            copy_scale_tile<PAIR>(sfb_t + 4 * j * NT, sd + 32 * (C::WPS + j));
+            if (NT == 2) copy_scale_tile<PAIR>(sfb_t + 4 * j * NT + 4, sd + 32 * (2 * C::WPS + j));
+          };
+          if (kb * 256 + 256 <= p.K) {
+#pragma unroll
+            for (int j = 0; j < C::WPS; ++j) copy(j);
+          } else {  // the words of the last steps
+            const int steps = (p.K - kb * 256 + 63) / 64, words = C::NV ? steps : (steps + 1) / 2;
+            for (int j = 0; j < words; ++j) copy(j);
+          }
+          if constexpr (PAIR) mma_commit_pair(&S.sf_ready[slot], 0x1);
+          else mma_commit(&S.sf_ready[slot]);
+        }
+        __syncwarp();
+        if (++slot == slots) slot = 0;
+        if (++stage == nst) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) timeout();
+    if (rank == 0 && elect_one()) {  // every copy has landed before tensor memory is freed
+      if constexpr (PAIR) mma_commit_pair(&S.sf_drain, 0x1);
+      else mma_commit(&S.sf_drain);
+      mbar_wait_drain(&S.sf_drain, 0);
     }
     __syncwarp();
   } else {
@@ -443,25 +500,12 @@ __global__ void __launch_bounds__(kF4Threads, 1)
       }
       tc_fence_after();
       const uint32_t taddr = tmem_base + ((uint32_t)(q * 32) << 16) + acc * acc_cols + h * half;
-      uint32_t pk[4][16];
+      // the accumulator first, so that it is handed back at once
+      uint32_t v[4][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (c * 32 >= half) break;
-        uint32_t v[32];
-        tmem_ld_32x32b_x32(taddr + c * 32, v);
-        tmem_ld_wait();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          float v0 = __uint_as_float(v[2 * j]) * f, v1 = __uint_as_float(v[2 * j + 1]) * f;
-          if (C::NV) {
-            const float2 ci = *reinterpret_cast<const float2 *>(cinv + c * 32 + 2 * j);
-            v0 *= ci.x;
-            v1 *= ci.y;
-          }
-          __nv_bfloat162 b2 = __floats2bfloat162_rn(v0, v1);
-          pk[c][j] = *reinterpret_cast<uint32_t *>(&b2);
-        }
-      }
+      for (int c = 0; c < 4; ++c)
+        if (c * 32 < half) tmem_ld_32x32b_x32(taddr + c * 32, v[c]);
+      tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -472,26 +516,62 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         acc = 0;
         acc_phase ^= 1;
       }
-      if (row_ok) {
-        __nv_bfloat16 *o = p.out + dst * p.N + col0;
+      const uint64_t f2 = f32x2(f, f);
+      const bool whole = !p.row_map && q * 32 + 32 <= ti.rows;  // the warp's 32 rows are all the group's
+      uint8_t *buf = sOut + ew * kF4Stage;
+      __nv_bfloat16 *o = p.out + dst * p.N + col0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c * 32 >= half) break;
+      for (int c = 0; c < 4; ++c) {
+        if (c * 32 >= half || col0 + c * 32 >= p.N) break;
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const uint32_t *w = &v[c][2 * j];
+          uint64_t a = f32x2(w[0], w[1]), b = f32x2(w[2], w[3]);
+          if (C::NV || p.row_weight) {
+            a = mul_f32x2(a, f2);
+            b = mul_f32x2(b, f2);
+          }
+          if (C::NV) {
+            const float4 ci = *reinterpret_cast<const float4 *>(cinv + c * 32 + 2 * j);
+            a = mul_f32x2(a, f32x2(ci.x, ci.y));
+            b = mul_f32x2(b, f32x2(ci.z, ci.w));
+          }
+          pk[j] = pack_bf16x2_u64(a);
+          pk[j + 1] = pack_bf16x2_u64(b);
+        }
+        if (whole) {
+          if (lane == 0) bulk_wait_read<0>();  // the buffer's last store has read it
+          __syncwarp();
+          // 64-byte rows, 16-byte unit j of row r at unit j ^ (r / 2 % 4) (the 64-byte swizzle)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmOut, buf, col0 + c * 32, ti.row0 + q * 32);
+            bulk_commit();
+          }
+        } else if (row_ok) {
           if (p.vec32) {  // whole 32-byte sectors (N % 16 == 0)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              if (col0 + c * 32 + j * 16 < p.N) store_32b(o + c * 32 + j * 16, &pk[c][8 * j]);
+              if (col0 + c * 32 + j * 16 < p.N) store_32b(o + c * 32 + j * 16, &pk[8 * j]);
           } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (col0 + c * 32 + j * 8 < p.N)
                 *reinterpret_cast<uint4 *>(o + c * 32 + j * 8) =
-                    make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2], pk[c][4 * j + 3]);
+                    make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
           }
         }
       }
       __syncwarp();  // the column factors are read
     }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -529,13 +609,13 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
   p.vec32 = N % 16 == 0 && ((uintptr_t)p.out & 31) == 0;
   p.stage_bytes = C::stage_bytes(p.a_rows, bn);
   // the MMA reads 128 A rows from a stage's start whatever the box holds: room behind the last stage
-  const size_t fixed = 1024 + sizeof(F4Shared) + (size_t)(128 - p.a_rows) * 128;
+  const size_t fixed = 1024 + kF4EpiWarps * kF4Stage + sizeof(F4Shared) + (size_t)(128 - p.a_rows) * 128;
   int st = (int)((kF4Limit - fixed) / p.stage_bytes);
   if (st > kF4MaxStages) st = kF4MaxStages;
   p.stages = st;
   const size_t smem = fixed + (size_t)st * p.stage_bytes;
   const int W = fp4_words(FMT, K);
-  CUtensorMap ta, tb, tsa, tsb;
+  CUtensorMap ta, tb, tsa, tsb, to;
   {
     const uint64_t d[2] = {(uint64_t)K / 2, (uint64_t)M}, str[1] = {(uint64_t)K / 2};
     const uint32_t box[2] = {128, (uint32_t)p.a_rows};
@@ -556,6 +636,12 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
   };
   if (!sf_map(&tsa, sx, mgemm_colwise_ld(M, E) / 128, 1)) return MGEMM_ECUDA;
   if (!sf_map(&tsb, sw, (int64_t)E * ((N + 127) / 128), NT)) return MGEMM_ECUDA;
+  {  // the output rows (a scattered output is stored directly: the map is then not used)
+    const uint64_t d[2] = {(uint64_t)N, (uint64_t)(p.row_map ? p.map_limit > 0 ? p.map_limit : 1 : M)};
+    const uint64_t str[1] = {(uint64_t)N * 2};
+    const uint32_t box[2] = {32, 32};
+    if (!make_tensor_map(&to, false, 2, p.out, d, str, box, true, true)) return MGEMM_ECUDA;
+  }
   static bool attr_done[64] = {};
   int dev = 0;
   int rc = cuda_rc(cudaGetDevice(&dev), "cudaGetDevice");
@@ -573,7 +659,7 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
   const int64_t cap = PAIR ? sms / 2 * 2 : sms;
   const unsigned grid = (unsigned)(upper < cap ? upper : cap);
   return launch_pdl(fp4_gemm_kernel<FMT, PAIR, NT>, dim3(grid), dim3(kF4Threads), smem, s, PAIR ? 2u : 1u,
-                    PAIR ? "mgemm_fwd_fp4 launch (CTA pairs)" : "mgemm_fwd_fp4 launch", ta, tb, tsa, tsb, p);
+                    PAIR ? "mgemm_fwd_fp4 launch (CTA pairs)" : "mgemm_fwd_fp4 launch", ta, tb, tsa, tsb, to, p);
 }
 
 template <int FMT>
