@@ -5,19 +5,21 @@
 //   s = sigmoid(l) or softmax(l),  c = s + bias,  ids = the top_k of c inside the
 //   best groups,  w = scale s[ids] / (renormalize ? sum s[ids] : 1)
 //
-// One warp per token; lane l holds experts l NV .. l NV + NV - 1 in registers, so
-// among equal values the lowest lane holds the lowest id.  Values are compared
-// as 32-bit order keys (order_key below): a warp maximum is then one integer
-// redux instruction, and a NaN, an expert that is off and one outside the groups
-// kept have keys of their own.
+// A token takes a warp; lane l holds experts l NV .. l NV + NV - 1 in registers,
+// so among equal values the lowest lane holds the lowest id.  Values are compared
+// as 32-bit order keys (order_key below): a NaN, an expert that is off and one
+// outside the groups kept have keys of their own, and a warp maximum is one
+// integer instruction.
 //
-// Bound by instruction issue, not by memory: a score costs about 15
-// instructions an expert and lane, against 4 bytes read.  So a lane keeps its
-// two best experts: a choice takes a maximum over the lanes' best and promotes
-// the second, and only a lane chosen from a third time scans its experts again.
-// Where groups are whole lanes (NV divides the group, a power of two of lanes)
-// their two best come from the same pairs by shuffles; otherwise the groups are
-// scanned in turn.
+// Bound by instruction issue, not by memory: an expert costs 4 bytes and some 35
+// instructions of a lane (score, key, the lane's best), a choice some 25 of the
+// warp.  So a lane keeps its three best experts in order: a choice takes the
+// maximum over the lanes' best and moves that lane's list up, and only a lane
+// chosen from a fourth time looks its experts over again.  Where groups are whole
+// lanes (NV divides the group, a power of two of lanes) their two best come from
+// the same lists by shuffles; otherwise the groups are scanned in turn.  (Half a
+// warp per token measured slower: the lanes' longer lists cost what the shared
+// choices save.)
 #include "common.cuh"
 
 namespace mgemm {
@@ -28,11 +30,11 @@ constexpr uint32_t kFull = 0xffffffffu;
 // already chosen), and one that is switched off
 constexpr uint32_t kKeyOut = 0u, kKeyOff = 1u;
 
-// Unsigned integers in the order of the floats: -0 equals +0, a NaN is the largest.
+// Unsigned integers in the order of the floats: -0 equals +0, a NaN is the
+// largest (the sum's NaN is the positive one).
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.f);
-  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-  return v != v ? kFull : k;
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 template <typename T>
@@ -49,9 +51,11 @@ __device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16 *
 // (a correctly rounded reciprocal is the correctly rounded quotient 1 / x)
 __device__ __forceinline__ float sigmoidf(float l) { return __frcp_rn(1.f + expf(-l)); }
 
-__device__ __forceinline__ float warp_sum(float a) {
+// Sum over SW lanes (a warp, or an aligned part of one).
+template <int SW = 32>
+__device__ __forceinline__ float lanes_sum(float a) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
+  for (int o = SW / 2; o > 0; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
   return a;
 }
 
@@ -128,21 +132,24 @@ __device__ __forceinline__ void load_lane(const L *row, int e0, int E, bool vec,
   }
 }
 
-// A lane's two largest keys and the places of both; equal keys: the lower place first.
+// A lane's three largest keys and their places; equal keys: the lower place first.
 struct Best {
-  uint32_t k1, k2;
-  int j1, j2;
+  uint32_t k1, k2, k3;
+  int j1, j2, j3;
 };
 template <int N>
-__device__ __forceinline__ Best two_best(const uint32_t (&key)[N]) {
-  Best b{key[0], kKeyOut, 0, 0};
+__device__ __forceinline__ Best three_best(const uint32_t (&key)[N]) {
+  Best b{key[0], kKeyOut, kKeyOut, 0, 0, 0};
 #pragma unroll
   for (int j = 1; j < N; ++j) {
-    const bool first = key[j] > b.k1, second = key[j] > b.k2;
-    b.j2 = first ? b.j1 : second ? j : b.j2;
-    b.j1 = first ? j : b.j1;
-    b.k2 = max(b.k2, min(b.k1, key[j]));
-    b.k1 = max(b.k1, key[j]);
+    const uint32_t k = key[j];
+    const bool g1 = k > b.k1, g2 = k > b.k2, g3 = k > b.k3;
+    b.j3 = g2 ? b.j2 : g3 ? j : b.j3;
+    b.j2 = g1 ? b.j1 : g2 ? j : b.j2;
+    b.j1 = g1 ? j : b.j1;
+    b.k3 = max(b.k3, min(b.k2, k));
+    b.k2 = max(b.k2, min(b.k1, k));
+    b.k1 = max(b.k1, k);
   }
   return b;
 }
@@ -155,7 +162,7 @@ __global__ void __launch_bounds__(kRouteThreads)
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
   if (t >= p.T) return;  // whole warps leave together
   const int e0 = lane * NV;
   const L *row = logits + t * p.ld;
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(kRouteThreads)
         s[j] = key[j] == kKeyOff ? 0.f : expf(s[j] - m);
         sum += s[j];
       }
-      sum = warp_sum(sum);
+      sum = lanes_sum(sum);
       if (sum == 0.f) sum = 1.f;  // every expert is off
     }
     if (bias) {
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(kRouteThreads)
   };
   Best best;
   if constexpr (GROUPS == 1) {
-    best = two_best(key);
+    best = three_best(key);
     uint32_t k1 = best.k1, k2 = best.k2;
     for (int o = 1; o < p.lanes_per_group; o <<= 1) {
       const uint32_t a = __shfl_xor_sync(kFull, k1, o), b = __shfl_xor_sync(kFull, k2, o);
@@ -224,15 +231,13 @@ __global__ void __launch_bounds__(kRouteThreads)
       k1 = max(k1, a);
     }
     const uint32_t mine = group_score(k1, k2);
-    const int g = lane / p.lanes_per_group;
+    const int own = lane & -p.lanes_per_group;  // the group's first lane
     int rank = 0;
-    for (int o = 0; o < p.n_group; ++o) {
-      const uint32_t other = __shfl_sync(kFull, mine, o * p.lanes_per_group);
-      rank += other > mine || (other == mine && o < g);
+    for (int o = 0; o < p.n_group * p.lanes_per_group; o += p.lanes_per_group) {
+      const uint32_t other = __shfl_sync(kFull, mine, o);
+      rank += other > mine - (o < own ? 1u : 0u);  // equal scores: the lower group first (a score is 1 at least)
     }
-    if (rank >= p.topk_group) {  // (lanes past the groups hold no keys)
-      best.k1 = best.k2 = kKeyOut;  // none of the lane's experts is chosen, so none is looked over again
-    }
+    if (rank >= p.topk_group) best.k1 = best.k2 = best.k3 = kKeyOut;  // none of the lane's experts is chosen (nor looked over again)
   } else if constexpr (GROUPS == 2) {
     // each group's best one or two keys over the warp; lane g % 32 keeps the
     // score of group g (g < 64)
@@ -271,17 +276,15 @@ __global__ void __launch_bounds__(kRouteThreads)
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (e0 + j < p.E && !((kept >> ((e0 + j) / gs)) & 1ull)) key[j] = kKeyOut;
-    best = two_best(key);
+    best = three_best(key);
   } else {
-    best = two_best(key);
+    best = three_best(key);
   }
 
   // the top_k keys, largest first; lane r keeps the id of pick r (top_k <= 32).
-  // A lane's own picks are bits of `taken`; its second best steps in for the
-  // first, and then its other experts are looked over again.
-  int my_id = 0;
+  // A lane's own picks are bits of `taken`, `left` what remains of its list.
+  int my_id = 0, left = 3;
   uint32_t taken = 0;
-  bool spare = true;  // best.k2 is the lane's second best
   for (int r = 0; r < p.top_k; ++r) {
     const uint32_t top = __reduce_max_sync(kFull, best.k1);
     const int src = __ffs(__ballot_sync(kFull, best.k1 == top)) - 1;
@@ -289,16 +292,19 @@ __global__ void __launch_bounds__(kRouteThreads)
     if (lane == r) my_id = id;
     if (lane == src) {
       taken |= 1u << best.j1;
-      if (spare) {
-        best.k1 = best.k2;
-        best.j1 = best.j2;
-      } else {
-        uint32_t rest[NV];
+      best.k1 = best.k2;
+      best.j1 = best.j2;
+      best.k2 = best.k3;
+      best.j2 = best.j3;
+      best.k3 = kKeyOut;
+      --left;
+    }
+    if (NV > 3 && left == 0) {
+      uint32_t rest[NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) rest[j] = (taken >> j) & 1u ? kKeyOut : key[j];
-        best = two_best(rest);
-      }
-      spare = !spare;
+      for (int j = 0; j < NV; ++j) rest[j] = (taken >> j) & 1u ? kKeyOut : key[j];
+      best = three_best(rest);
+      left = 3;
     }
   }
   // the picks' scores, one per lane
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(kRouteThreads)
     if (!(l <= MGEMM_ROUTE_MASKED)) s = p.sigmoid ? sigmoidf(l) : expf(l - m) / sum;
   }
   if (p.renormalize) {
-    const float total = warp_sum(s);
+    const float total = lanes_sum(s);
     s = total == 0.f ? 0.f : s / total;
   }
   if (lane < p.top_k) {
@@ -341,78 +347,153 @@ __device__ __forceinline__ void store_unit(__nv_bfloat16 *p, const float (&v)[8]
   *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One warp per token: lane j < top_k takes pick j's coefficient; the row's
-// other values (zeros; softmax without renormalization: -s_e sum g w) are
-// written first, then the picks over them.  Bound by the E gradients written.
+__device__ __forceinline__ float route_score_rest(float l) {  // 1 - sigmoid(l); any where the expert is off (its w is 0)
+  return l <= MGEMM_ROUTE_MASKED ? 0.5f : __frcp_rn(1.f + expf(l));
+}
+
+// Gradients at the picks only (sigmoid, or renormalized weights).  Bound by the
+// zeros written around them: a CTA clears the rows of its kBwdTokens tokens with
+// 16-byte stores, computes a pick per thread meanwhile, and stores the picks after
+// a barrier.  (A warp per token spends 230 instructions on it, 26 us for 65536 x
+// 256; so they are 13.)
+constexpr int kBwdTokens = 32;
+
 template <typename L>
 __global__ void __launch_bounds__(kRouteThreads)
-    route_bwd_kernel(const float *__restrict__ grad_w, const L *__restrict__ logits, const float *__restrict__ weights,
-                     const int32_t *__restrict__ ids, const RouteBwdParams p, L *__restrict__ grad) {
+    route_bwd_picks_kernel(const float *__restrict__ grad_w, const L *__restrict__ logits,
+                           const float *__restrict__ weights, const int32_t *__restrict__ ids, const RouteBwdParams p,
+                           L *__restrict__ grad) {
   constexpr int U = 16 / sizeof(L);  // values per 16-byte unit
+  constexpr int kMost = kBwdTokens * MGEMM_ROUTE_MAX_TOPK / kRouteThreads;  // picks per thread at most
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (t >= p.T) return;
-  const L *row = logits ? logits + t * p.ld : nullptr;
+  __shared__ float part[kBwdTokens * MGEMM_ROUTE_MAX_TOPK];  // a pick's g r
+  const int64_t t0 = (int64_t)blockIdx.x * kBwdTokens;
+  const int tokens = (int)min((int64_t)kBwdTokens, p.T - t0), picks = tokens * p.top_k;
+  float g[kMost], w[kMost], rest[kMost];
+  int id[kMost];
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int k = i * kRouteThreads + threadIdx.x;
+    if (i * kRouteThreads >= picks) break;
+    id[i] = -1;
+    if (k < picks) {
+      const int64_t o = t0 * p.top_k + k;
+      g[i] = __ldg(grad_w + o);
+      w[i] = __ldg(weights + o);
+      id[i] = __ldg(ids + o);
+      if (id[i] < 0 || id[i] >= p.E) id[i] = -1;
+    }
+  }
+  // the rows' zeros: whole units (of all rows at once where they follow each other), then single values
+  const int units = p.vec_grad ? p.E / U : 0;
+  const float z[U] = {};
+  if (units * U == p.E && p.ld_grad == p.E) {
+    L *out = grad + t0 * p.ld_grad;
+    for (int u = threadIdx.x; u < tokens * units; u += kRouteThreads) store_unit(out + u * U, z);
+  } else {
+    for (int r = threadIdx.x >> 5; r < tokens; r += kRouteThreads / 32) {
+      L *out = grad + (t0 + r) * p.ld_grad;
+      for (int u = threadIdx.x & 31; u < units; u += 32) store_unit(out + u * U, z);
+      for (int e = units * U + (threadIdx.x & 31); e < p.E; e += 32) store_grad(out + e, 0.f);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    if (i * kRouteThreads >= picks) break;
+    const int k = i * kRouteThreads + threadIdx.x;
+    rest[i] = 1.f;
+    if (id[i] >= 0 && p.sigmoid) rest[i] = route_score_rest(load_logit(logits + (t0 + k / p.top_k) * p.ld + id[i]));
+    if (k < picks) part[k] = id[i] >= 0 && p.renormalize ? g[i] * (w[i] / p.scale) : 0.f;
+  }
+  __syncthreads();  // the zeros are stored, the parts are there
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    if (i * kRouteThreads >= picks) break;
+    if (id[i] < 0) continue;
+    const int k = i * kRouteThreads + threadIdx.x, r = k / p.top_k;
+    float f = 0.f;
+    if (p.renormalize)
+      for (int j = 0; j < p.top_k; ++j) f += part[r * p.top_k + j];
+    store_grad(grad + (t0 + r) * p.ld_grad + id[i], w[i] * (g[i] - f) * rest[i]);
+  }
+}
+
+// Softmax with raw weights: every expert's probability is needed,
+// - s_e sum g w everywhere and the picks over it.  SW lanes per token.
+template <typename L, int SW>
+__global__ void __launch_bounds__(kRouteThreads)
+    route_bwd_rows_kernel(const float *__restrict__ grad_w, const L *__restrict__ logits,
+                          const float *__restrict__ weights, const int32_t *__restrict__ ids, const RouteBwdParams p,
+                          L *__restrict__ grad) {
+  constexpr int U = 16 / sizeof(L);
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & (SW - 1);
+  const int64_t t0 = (int64_t)blockIdx.x * (kRouteThreads / SW) + threadIdx.x / SW;
+  if (t0 - (threadIdx.x & 31) / SW >= p.T) return;  // whole warps leave together
+  const bool live = t0 < p.T;
+  const int64_t t = live ? t0 : p.T - 1;
+  const L *row = logits + t * p.ld;
   L *out = grad + t * p.ld_grad;
-  const bool plain = p.sigmoid || p.renormalize;  // gradients at the picks only
-  float g = 0.f, w = 0.f;
-  int id = -1;
-  if (lane < p.top_k) {
-    g = __ldg(grad_w + t * p.top_k + lane);
-    w = __ldg(weights + t * p.top_k + lane);
-    id = __ldg(ids + t * p.top_k + lane);
-    if (id < 0 || id >= p.E) id = -1;
+  const int n = p.vec && p.vec_grad ? p.E / U : 0;  // whole 16-byte units, then single values
+  float m = -INFINITY, sum = 0.f, f = 0.f;
+  for (int r = lane; r < p.top_k; r += SW) {
+    const int id = __ldg(ids + t * p.top_k + r);
+    if (id >= 0 && id < p.E) f += __ldg(grad_w + t * p.top_k + r) * __ldg(weights + t * p.top_k + r);
   }
-  const int units = p.vec_grad ? p.E / U : 0;  // whole units, then single values
-  if (plain) {
-    float z[U] = {};
-    for (int u = lane; u < units; u += 32) store_unit(out + u * U, z);
-    for (int e = units * U + lane; e < p.E; e += 32) store_grad(out + e, 0.f);
-  }
-  const float r = p.renormalize ? w / p.scale : w;
-  const float f = warp_sum(id >= 0 ? g * r : 0.f);
-  float d = p.renormalize ? w * (g - f) : w * g;
-  if (p.sigmoid && id >= 0) {
-    const float l = load_logit(row + id);
-    d *= l <= MGEMM_ROUTE_MASKED ? 0.5f : 1.f / (1.f + expf(l));  // 1 - s; w is 0 where the expert is off
-  }
-  if (!plain) {  // every expert's probability is needed
-    float m = -INFINITY, sum = 0.f;
-    const bool vec = p.vec && p.vec_grad;
-    const int n = vec ? units : 0;
-    for (int u = lane; u < n; u += 32) {
-      float v[U];
-      load_values<U>(row + u * U, true, v);
+  for (int u = lane; u < n; u += SW) {
+    float v[U];
+    load_values<U>(row + u * U, true, v);
 #pragma unroll
-      for (int i = 0; i < U; ++i) m = fmaxf(m, v[i]);
-    }
-    for (int e = n * U + lane; e < p.E; e += 32) m = fmaxf(m, load_logit(row + e));
-    m = warp_max(m);
-    if (m <= MGEMM_ROUTE_MASKED) m = 0.f;
-    auto term = [&](float l) { return l <= MGEMM_ROUTE_MASKED ? 0.f : expf(l - m); };
-    for (int u = lane; u < n; u += 32) {
-      float v[U];
-      load_values<U>(row + u * U, true, v);
+    for (int i = 0; i < U; ++i) m = fmaxf(m, v[i]);
+  }
+  for (int e = n * U + lane; e < p.E; e += SW) m = fmaxf(m, load_logit(row + e));
 #pragma unroll
-      for (int i = 0; i < U; ++i) sum += term(v[i]);
-    }
-    for (int e = n * U + lane; e < p.E; e += 32) sum += term(load_logit(row + e));
-    sum = warp_sum(sum);
-    const float c = sum == 0.f ? 0.f : -f / sum;
-    for (int u = lane; u < n; u += 32) {
+  for (int o = SW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  if (m <= MGEMM_ROUTE_MASKED) m = 0.f;
+  auto term = [&](float l) { return l <= MGEMM_ROUTE_MASKED ? 0.f : expf(l - m); };
+  for (int u = lane; u < n; u += SW) {
+    float v[U];
+    load_values<U>(row + u * U, true, v);
+#pragma unroll
+    for (int i = 0; i < U; ++i) sum += term(v[i]);
+  }
+  for (int e = n * U + lane; e < p.E; e += SW) sum += term(load_logit(row + e));
+  sum = lanes_sum<SW>(sum);
+  f = lanes_sum<SW>(f);
+  const float c = sum == 0.f ? 0.f : -f / sum;
+  if (live) {
+    for (int u = lane; u < n; u += SW) {
       float v[U];
       load_values<U>(row + u * U, true, v);
 #pragma unroll
       for (int i = 0; i < U; ++i) v[i] = term(v[i]) * c;
       store_unit(out + u * U, v);
     }
-    for (int e = n * U + lane; e < p.E; e += 32) store_grad(out + e, term(load_logit(row + e)) * c);
-    if (id >= 0) d += term(load_logit(row + id)) * c;
+    for (int e = n * U + lane; e < p.E; e += SW) store_grad(out + e, term(load_logit(row + e)) * c);
   }
   __syncwarp();
-  if (id >= 0) store_grad(out + id, d);
+  for (int r = lane; live && r < p.top_k; r += SW) {
+    const int64_t o = t * p.top_k + r;
+    const int id = __ldg(ids + o);
+    if (id >= 0 && id < p.E) store_grad(out + id, __ldg(weights + o) * __ldg(grad_w + o) + term(load_logit(row + id)) * c);
+  }
+}
+
+template <typename L>
+int launch_route_bwd(const float *grad_w, const void *logits, const float *weights, const int32_t *ids,
+                     const RouteBwdParams &p, void *grad, cudaStream_t s) {
+  auto go = [&](auto kernel, int per_cta) {
+    return launch_pdl(kernel, dim3((unsigned)((p.T + per_cta - 1) / per_cta)), dim3(kRouteThreads), 0, s, 1,
+                      "mgemm_route_bwd launch", grad_w, (const L *)logits, weights, ids, p, (L *)grad);
+  };
+  if (p.sigmoid || p.renormalize) return go(route_bwd_picks_kernel<L>, kBwdTokens);
+  // as many lanes as a row has 16-byte units, up to a warp
+  const int units = p.E * (int)sizeof(L) / 16;
+  if (units <= 8) return go(route_bwd_rows_kernel<L, 8>, kRouteThreads / 8);
+  if (units <= 16) return go(route_bwd_rows_kernel<L, 16>, kRouteThreads / 16);
+  return go(route_bwd_rows_kernel<L, 32>, kRouteThreads / 32);
 }
 
 bool route_sizes_ok(int64_t T, int E, int top_k, int64_t ld) {
@@ -420,48 +501,55 @@ bool route_sizes_ok(int64_t T, int E, int top_k, int64_t ld) {
          ld >= E && (T + 7) / 8 < (int64_t(1) << 31);
 }
 
+template <typename L, int GROUPS>
+int launch_route_nv(int nv, const void *logits, const float *bias, const RouteParams &p, float *weights, int32_t *ids,
+                    cudaStream_t s) {
+  const int per_cta = kRouteThreads / 32;
+  const unsigned blocks = (unsigned)((p.T + per_cta - 1) / per_cta);
+  auto go = [&](auto kernel) {
+    return launch_pdl(kernel, dim3(blocks), dim3(kRouteThreads), 0, s, 1, "mgemm_route launch", (const L *)logits, bias,
+                      p, weights, ids);
+  };
+  switch (nv) {  // (the sizes route_lanes chooses from)
+    case 1: return go(route_kernel<1, GROUPS, L>);
+    case 2: return go(route_kernel<2, GROUPS, L>);
+    case 4: return go(route_kernel<4, GROUPS, L>);
+    case 8: return go(route_kernel<8, GROUPS, L>);
+    case 16: return go(route_kernel<16, GROUPS, L>);
+    case 32: return go(route_kernel<32, GROUPS, L>);
+  }
+  if constexpr (GROUPS == 1) {
+    if (nv == 3) return go(route_kernel<3, GROUPS, L>);
+    if (nv == 5) return go(route_kernel<5, GROUPS, L>);
+    if (nv == 10) return go(route_kernel<10, GROUPS, L>);
+    if (nv == 12) return go(route_kernel<12, GROUPS, L>);
+  }
+  return MGEMM_EINVAL;
+}
+
 template <typename L>
 int launch_route(const void *logits, const float *bias, RouteParams p, float *weights, int32_t *ids, cudaStream_t s) {
-  const int warps = kRouteThreads / 32;
-  const unsigned blocks = (unsigned)((p.T + warps - 1) / warps);
   p.vec = ((uintptr_t)logits & 15) == 0 && p.ld * (int64_t)sizeof(L) % 16 == 0;
   p.vec_bias = ((uintptr_t)bias & 15) == 0;
-  const int nv = (p.E + 31) / 32, gs = p.E / p.n_group;
-  // experts per lane: the fewest that are compiled, and for groups of whole lanes the fewest of
-  // those that divide a group into a power of two of lanes
-  static constexpr int kNv[] = {1, 2, 3, 4, 5, 6, 8, 12, 16, 32};
-  int pick = 0, groups = 0;
-  for (int c : kNv) {
-    if (c < nv) continue;
-    if (!pick) pick = c;
-    const int lanes = gs / c;
-    if (p.n_group > 1 && gs % c == 0 && (lanes & (lanes - 1)) == 0) {
-      pick = c;
-      groups = 1;
+  // experts per lane: the fewest that are compiled; for groups of whole lanes the fewest of those
+  // that divide a group into a power of two of lanes
+  static constexpr int kPlain[] = {1, 2, 4, 8, 16, 32}, kWhole[] = {1, 2, 3, 4, 5, 8, 10, 12, 16, 32};
+  const int gs = p.E / p.n_group;
+  if (p.n_group > 1)
+    for (int c : kWhole) {
+      const int lanes = gs / c;
+      if (c * 32 < p.E || gs % c || (lanes & (lanes - 1))) continue;
       p.lanes_per_group = lanes;
+      return launch_route_nv<L, 1>(c, logits, bias, p, weights, ids, s);
+    }
+  int nv = 32;
+  for (int c : kPlain)
+    if (c * 32 >= p.E) {
+      nv = c;
       break;
     }
-  }
-  if (p.n_group > 1 && !groups) groups = 2;
-#define MGEMM_ROUTE_LAUNCH(NV)                                                                                       \
-  if (pick == NV)                                                                                                    \
-  return launch_pdl(groups == 0   ? route_kernel<NV, 0, L>                                                           \
-                    : groups == 1 ? route_kernel<NV, 1, L>                                                           \
-                                  : route_kernel<NV, 2, L>,                                                          \
-                    dim3(blocks), dim3(kRouteThreads), 0, s, 1, "mgemm_route launch", (const L *)logits, bias, p,     \
-                    weights, ids)
-  MGEMM_ROUTE_LAUNCH(1);
-  MGEMM_ROUTE_LAUNCH(2);
-  MGEMM_ROUTE_LAUNCH(3);
-  MGEMM_ROUTE_LAUNCH(4);
-  MGEMM_ROUTE_LAUNCH(5);
-  MGEMM_ROUTE_LAUNCH(6);
-  MGEMM_ROUTE_LAUNCH(8);
-  MGEMM_ROUTE_LAUNCH(12);
-  MGEMM_ROUTE_LAUNCH(16);
-  MGEMM_ROUTE_LAUNCH(32);
-#undef MGEMM_ROUTE_LAUNCH
-  return MGEMM_EINVAL;
+  return p.n_group > 1 ? launch_route_nv<L, 2>(nv, logits, bias, p, weights, ids, s)
+                       : launch_route_nv<L, 0>(nv, logits, bias, p, weights, ids, s);
 }
 
 }  // namespace
@@ -505,12 +593,7 @@ extern "C" int mgemm_route_bwd(const float *grad_weights, const void *logits, in
   const RouteBwdParams p{T, ld, ld_grad, E, top_k, scoring == MGEMM_SCORE_SIGMOID, renormalize, scale,
                          ((uintptr_t)logits & 15) == 0 && ld * es % 16 == 0,
                          ((uintptr_t)grad_logits & 15) == 0 && ld_grad * es % 16 == 0};
-  const unsigned blocks = (unsigned)((T + 7) / 8);
   cudaStream_t s = (cudaStream_t)stream;
-  if (logits_bf16)
-    return launch_pdl(route_bwd_kernel<__nv_bfloat16>, dim3(blocks), dim3(256), 0, s, 1, "mgemm_route_bwd launch",
-                      grad_weights, (const __nv_bfloat16 *)logits, topk_weights, topk_ids, p,
-                      (__nv_bfloat16 *)grad_logits);
-  return launch_pdl(route_bwd_kernel<float>, dim3(blocks), dim3(256), 0, s, 1, "mgemm_route_bwd launch", grad_weights,
-                    (const float *)logits, topk_weights, topk_ids, p, (float *)grad_logits);
+  return logits_bf16 ? launch_route_bwd<__nv_bfloat16>(grad_weights, logits, topk_weights, topk_ids, p, grad_logits, s)
+                     : launch_route_bwd<float>(grad_weights, logits, topk_weights, topk_ids, p, grad_logits, s);
 }

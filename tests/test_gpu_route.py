@@ -88,6 +88,20 @@ def test_groups(scoring, E, G, keep, top, k):
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_picks_that_crowd_into_a_lane(scoring):
+    # the best experts are neighbours: lanes of 2 to 32 experts give up many, or all, of theirs
+    for E, k in ((64, 16), (96, 32), (256, 32), (512, 32), (1024, 32)):
+        l = spread_logits(4, E, E)
+        top = np.sort(l, 1)[:, ::-1]
+        for t, at in enumerate((0, 5, E - k, E // 2 - 3)):
+            rest = top[t, k:].copy()
+            l[t, :at], l[t, at:at + k], l[t, at + k:] = rest[:at], top[t, :k], rest[at:]
+        check(l, k, scoring)
+        check(l, k, scoring, n_group=2, topk_group=2, group_top=2)
+    check(np.tile(np.arange(96, dtype=np.float32) * 0.01, (2, 1)), 24, scoring, n_group=4, topk_group=1, group_top=1)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_ties_and_bf16(scoring, dtype):
     rng = np.random.default_rng(5)
