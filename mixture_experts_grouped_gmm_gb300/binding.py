@@ -30,6 +30,7 @@ MGEMM_COL_PAD = 128
 STATUS = {0: "ok", 1: "negative group size", 2: "group sizes do not sum to M", 4: "pipeline wait timed out"}
 
 _lib = None
+_calls = None
 
 
 class MgemmError(RuntimeError):
@@ -168,6 +169,26 @@ def lib():
             fn.argtypes = args
         _lib = L
     return _lib
+
+
+# The entries that _calls reaches, in the order its bind() takes them.
+_CALLS = ("mgemm_route", "mgemm_route_bwd", "mgemm_quant_fp4", "mgemm_dequant_fp4", "mgemm_fp4_scale_bytes",
+          "mgemm_gmm_fp4_workspace_bytes", "mgemm_gmm_fp4")
+
+
+def calls():
+    """The extension module _calls (built with the library), bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        try:
+            from . import _calls as m
+        except ImportError as e:
+            raise MgemmError(f"_calls.so is missing ({e}); build it with "
+                             "mixture_experts_grouped_gmm_gb300.build.build()") from e
+        m.bind(tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _CALLS))
+        _calls = m
+    return _calls
 
 
 def _p(t):

@@ -1,4 +1,6 @@
-"""Builds libmgemm.so in-tree from csrc/ with nvcc for sm_103a.
+"""Builds libmgemm.so in-tree from csrc/ with nvcc for sm_103a, and _calls.so,
+the host side of the decode-size operators (csrc/torch_calls.cpp, against the
+installed torch's headers).
 
 The translation units compile in parallel (one ``-gencode``), then link into
 one shared library beside this file.  The CUDA runtime is linked statically
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmgemm.so")
+CALLS_PATH = os.path.join(PKG, "_calls.so")
 
 SOURCES = ["args.cu", "quant.cu", "gemm_bf16.cu", "gemm_fp8.cu", "gemm_api.cu", "gemm_f8i4.cu", "gemm_sparse.cu",
            "noalloc.cu",
@@ -40,7 +43,7 @@ def _inputs():
     files = []
     for d in (CSRC, INCLUDE):
         for f in os.listdir(d):
-            if f.endswith((".cu", ".cuh", ".h", ".map")):
+            if f.endswith((".cu", ".cuh", ".h", ".map", ".cpp")):
                 files.append(os.path.join(d, f))
     files.append(os.path.abspath(__file__))
     return files
@@ -79,9 +82,9 @@ def gemm_source_hash():
 
 
 def up_to_date():
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(CALLS_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(CALLS_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -89,7 +92,33 @@ def build(force=False, verbose=False, extra_flags=()):
     """Compile and link; returns the library path.  Raises on a compiler error."""
     if not force and up_to_date():
         return LIB_PATH
-    return _build_into(LIB_PATH, BUILD_DIR, verbose, extra_flags)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(_build_calls)
+        path = _build_into(LIB_PATH, BUILD_DIR, verbose, extra_flags)
+        calls.result()
+    return path
+
+
+def _build_calls():
+    """csrc/torch_calls.cpp -> _calls.so, a Python extension module (it is given the library's
+    addresses at run time, so it does not link against it)."""
+    import sysconfig
+
+    import torch
+
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [sysconfig.get_paths()["include"], os.path.join(t, "include"),
+           os.path.join(t, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include"), INCLUDE]
+    tmp = CALLS_PATH + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *["-I" + i for i in inc],
+           os.path.join(CSRC, "torch_calls.cpp"), "-o", tmp, "-L" + os.path.join(t, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
 
 
 def build_variant(name, defines, force=False):

@@ -8,14 +8,13 @@ product runs on the block-scaled tensor-core path.  It is a serving operator:
 the weights are laid out once, and no gradient flows through it.
 
 This module only allocates outputs with torch and calls the binding; every
-step runs in the CUDA library.  At decode sizes a call's time is the host's: an
-allocation costs it about 4 us next to 3 us for a launch.  So a cast makes one
-allocation for its three parts (their tensors are made when asked for), and
-gmm_fp4 keeps a small workspace per stream.
+step runs in the CUDA library.  At decode sizes a call's time is the host's, so
+the plain case of each goes through the extension module (csrc/torch_calls.cpp),
+and a cast makes one allocation for its three parts (their tensors are made when
+asked for).
 """
 
 import functools
-import threading
 
 import torch
 
@@ -58,26 +57,20 @@ class Fp4Tensor:
             rows = row_scale.data_ptr()
         elif row_scale is not None:
             raise B.MgemmError("mxfp4 has no row scales")
-        for t in (codes, scales, row_scale):
-            if t is not None and (not t.is_cuda or t.device != codes.device):
-                raise B.MgemmError("mgemm kernels take device tensors only, of one device")
+        dev = codes.get_device()  # -1 on the CPU
+        if dev < 0 or scales.get_device() != dev or (rows is not None and row_scale.get_device() != dev):
+            raise B.MgemmError("mgemm kernels take device tensors only, of one device")
         self.fmt, self.device = fmt, codes.device
         self._parts = (codes, scales, row_scale)
         self._storage = None
         self._ptrs = (codes.data_ptr(), scales.data_ptr(), rows)
 
     @classmethod
-    def _empty(cls, fmt, code, E, N, K, device):
-        """Unwritten parts, one after another in one allocation."""
+    def _of(cls, fmt, code, storage, ptrs, shape):
+        """Of parts that lie one after another in one allocation, each from a multiple of 256 bytes."""
         q = cls.__new__(cls)
-        q.fmt, q.code, q.shape, q.device = fmt, code, (E, N, K), device
-        n_codes = (E * N * (K // 2) + 255) & ~255
-        n_scales = E * _scale_bytes(code, N, K)  # a multiple of 512
-        q._storage = torch.empty(n_codes + n_scales + (4 * E * N if fmt == "nvfp4" else 0), dtype=torch.uint8,
-                                 device=device)
-        q._parts = None
-        p = q._storage.data_ptr()
-        q._ptrs = (p, p + n_codes, p + n_codes + n_scales if fmt == "nvfp4" else None)
+        q.fmt, q.code, q.shape, q.device = fmt, code, shape, storage.device
+        q._storage, q._ptrs, q._parts = storage, ptrs, None
         return q
 
     def _part(self, i):
@@ -97,47 +90,26 @@ class Fp4Tensor:
 def quantize_fp4(x, fmt):
     """bf16 [E, N, K] or [N, K] on the GPU (rows at a common stride, else copied) -> Fp4Tensor; K % 32 == 0."""
     code = _format(fmt)
-    dim = x.dim()
-    if x.dtype != BF16 or (dim != 2 and dim != 3):
-        raise B.MgemmError("quantize_fp4 takes a bf16 [E, N, K] or [N, K]")
-    B._cuda(x)
-    E, N, K = x.shape if dim == 3 else (1, *x.shape)
-    st = x.stride()
-    ld = st[-2]
-    if st[-1] != 1 or ld % 8 or ld < K or x.data_ptr() % 16 or (E > 1 and st[0] != N * ld):
-        x = x.contiguous()
-        ld = K
-    q = Fp4Tensor._empty(fmt, code, E, N, K, x.device)
-    B._check(B.lib().mgemm_quant_fp4(x.data_ptr(), E, N, K, ld, code, *q._ptrs, B._stream(x)), "mgemm_quant_fp4")
-    return q
+    r = B.calls().quantize(x, code)
+    if r is None:  # not the plain case: looked at, mended or refused here
+        if x.dtype != BF16 or x.dim() not in (2, 3):
+            raise B.MgemmError("quantize_fp4 takes a bf16 [E, N, K] or [N, K]")
+        B._cuda(x)
+        r = B.calls().quantize(x.clone(memory_format=torch.contiguous_format), code)
+        if r is None:
+            raise B.MgemmError(f"quantize_fp4: sizes {tuple(x.shape)} are out of range")
+    if type(r) is int:
+        B._check(r, "mgemm_quant_fp4")
+    storage, ptrs, shape = r
+    return Fp4Tensor._of(fmt, code, storage, ptrs, shape)
 
 
 def dequantize_fp4(q):
     """The values an Fp4Tensor stands for, bf16 [E, N, K]."""
-    out = torch.empty(q.shape, dtype=BF16, device=q.device)
-    E, N, K = q.shape
-    B._check(B.lib().mgemm_dequant_fp4(*q._ptrs, E, N, K, q.code, out.data_ptr(), K, B._stream(out)),
-             "mgemm_dequant_fp4")
-    return out
-
-
-# Workspaces of at most this many bytes are kept, one per thread, device and
-# stream (work of one stream runs in order, so its calls can share one).  Larger
-# ones are allocated per call, and so are those of a call that is being captured
-# into a graph, which goes on using the memory.
-KEPT_WORKSPACE = 16 << 20
-_kept = threading.local()
-
-
-def _workspace(nbytes, x, stream):
-    if nbytes > KEPT_WORKSPACE or torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    kept = _kept.__dict__
-    key = (x.get_device(), stream)
-    ws = kept.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = kept[key] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=x.device)
-    return ws
+    if type(q) is not Fp4Tensor:
+        raise B.MgemmError("dequantize_fp4 takes an Fp4Tensor (see quantize_fp4)")
+    r = B.calls().dequantize(q._ptrs, q.shape, q.code, q.device.index)
+    return B._check(r, "mgemm_dequant_fp4") if type(r) is int else r
 
 
 def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
@@ -146,10 +118,15 @@ def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
     x: bf16 [M, K] on the GPU, rows contiguous by expert; w: Fp4Tensor [E, N, K];
     group_sizes: int64 [E] on the GPU, summing to M.  ``out`` (bf16 [M, N]) is
     allocated when not given.  ``workspace`` (uint8, see
-    mgemm_gmm_fp4_workspace_bytes): scratch that starts with the args block, for
-    ``binding.args_status``; by default the stream's own.  Returns bf16 [M, N]."""
+    mgemm_gmm_fp4_workspace_bytes; scratch that starts with the args block, for
+    ``binding.args_status``) is too.  Returns bf16 [M, N]."""
     if type(w) is not Fp4Tensor:
         raise B.MgemmError("gmm_fp4 takes an Fp4Tensor (see quantize_fp4)")
+    if out is None and workspace is None:
+        r = B.calls().gmm(x, w._ptrs, w.shape, w.code, group_sizes, torch.is_grad_enabled())
+        if r is not None:
+            return B._check(r, "mgemm_gmm_fp4") if type(r) is int else r
+    # the caller's buffers, or not the plain case: looked at, mended or refused here
     E, N, K = w.shape
     if x.dtype != BF16 or x.dim() != 2 or x.shape[1] != K:
         raise B.MgemmError(f"gmm_fp4 takes bf16 x [M, {K}]")
@@ -159,19 +136,16 @@ def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
         raise B.MgemmError("group_sizes must be contiguous int64 [E]")
     B._cuda(x, group_sizes, out, workspace)
     M = x.shape[0]
-    ld, unit = x.stride()
-    if unit != 1 or ld % 8 or ld < K or x.data_ptr() % 16:
-        x = x.contiguous()
-        ld = K
+    if x.stride(1) != 1 or x.stride(0) % 8 or x.stride(0) < K or x.data_ptr() % 16:
+        x = x.clone(memory_format=torch.contiguous_format)
     if out is None:
         out = torch.empty((M, N), dtype=BF16, device=x.device)
     elif out.dtype != BF16 or out.shape != (M, N) or not out.is_contiguous():
         raise B.MgemmError("gmm_fp4: out must be contiguous bf16 [M, N]")
-    stream = B._stream(x)
     if workspace is None:
-        workspace = _workspace(_workspace_bytes(w.code, M, K, E), x, stream)
+        workspace = torch.empty(_workspace_bytes(w.code, M, K, E), dtype=torch.uint8, device=x.device)
     codes, scales, rows = w._ptrs
-    B._check(B.lib().mgemm_gmm_fp4(group_sizes.data_ptr(), E, w.code, x.data_ptr(), ld, codes, scales, rows,
-                                   out.data_ptr(), M, K, N, workspace.data_ptr(), workspace.numel(), stream),
+    B._check(B.lib().mgemm_gmm_fp4(group_sizes.data_ptr(), E, w.code, x.data_ptr(), x.stride(0), codes, scales, rows,
+                                   out.data_ptr(), M, K, N, workspace.data_ptr(), workspace.numel(), B._stream(x)),
              "mgemm_gmm_fp4")
     return out

@@ -30,8 +30,15 @@ the caller already has.  For decode-size batches the routing, the alignment and
 the args block come from one launch (``mgemm_moe_route_align``, the same
 results bit for bit), and for at most 32 entries (a hidden size that is a
 multiple of 64) the first GEMM reads the token rows through the sorted ids
-itself (``mgemm_fwd_gated_gather``), so the layer takes four launches.  This
-module only
+itself (``mgemm_fwd_gated_gather``), so the layer takes four launches.
+
+``fused_moe_fp4`` and ``fused_experts_fp4`` are the same layer over 4-bit experts
+(``fp4.Fp4Tensor``): the routed tokens are gathered and cast, the gated rows cast
+again between the two products, and no group is padded.  ``route_experts`` (with
+its gradient: ``Router``) is the router of layers with many experts, with sigmoid
+or softmax scores, a balance bias and expert groups.
+
+This module only
 allocates buffers with torch and calls the binding; every step runs in the
 CUDA library, and nothing waits on the host.
 """
@@ -39,6 +46,7 @@ CUDA library, and nothing waits on the host.
 import torch
 
 from . import binding as B
+from .fp4 import Fp4Tensor
 
 BLOCK = B.MGEMM_TILE_M  # rows per block: the GEMM's row tile
 # fused_moe routes batches of at most this many tokens in the one-CTA launch
@@ -94,6 +102,10 @@ def route_experts(logits, topk, scoring="softmax", bias=None, n_group=1, topk_gr
     when asked and times ``scale``.  A logit of -inf (or its type's lowest value)
     switches the expert off.  Returns (topk_weights float32 [T, topk], topk_ids
     int32 [T, topk]); ``Router`` is the same with a gradient."""
+    r = B.calls().route(logits, topk, SCORES.get(scoring), bias, n_group, topk_group, group_top, renormalize, scale)
+    if r is not None:
+        return r if type(r) is tuple else B._check(r, "mgemm_route")
+    # not the plain case: looked at, mended or refused here
     logits = _route_logits(logits, scoring)
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != logits.shape[1] or
                              not bias.is_contiguous()):
@@ -108,6 +120,9 @@ def route_experts(logits, topk, scoring="softmax", bias=None, n_group=1, topk_gr
 def route_experts_backward(grad_weights, logits, topk_weights, topk_ids, scoring="softmax", renormalize=True,
                            scale=1.0):
     """The logits' gradient [T, E] (in their type) of route_experts' weights (mgemm_route_bwd)."""
+    r = B.calls().route_bwd(grad_weights, logits, topk_weights, topk_ids, SCORES.get(scoring), renormalize, scale)
+    if r is not None:
+        return B._check(r, "mgemm_route_bwd") if type(r) is int else r
     logits = _route_logits(logits, scoring)
     if topk_weights.shape != topk_ids.shape or grad_weights.shape != topk_ids.shape or \
             topk_ids.dtype != torch.int32 or topk_weights.dtype != torch.float32 or \
@@ -236,5 +251,64 @@ def _experts(hidden_states, w1, w2, topk_weights, sorted_ids, npp, args, T, top_
     wts = topk_weights.to(torch.float32).contiguous().view(-1)
     B.mgemm_fwd_scatter(args, B.MGEMM_BF16, 1, a2, w2, c3, sorted_ids, n, wts, rows, F, H, E)
     out = torch.empty(T, H, dtype=bf, device=dev)
+    B.mgemm_topk_sum(c3, T, top_k, out)
+    return out
+
+
+# --------------------------------------------------------------------- 4 bits
+def fused_moe_fp4(hidden_states, w1, w2, gating_output, topk, **routing):
+    """The routed layer over 4-bit experts: route_experts(gating_output, topk,
+    **routing), then fused_experts_fp4."""
+    topk_weights, topk_ids = route_experts(gating_output, topk, **routing)
+    return fused_experts_fp4(hidden_states, w1, w2, topk_weights, topk_ids)
+
+
+def fused_experts_fp4(hidden_states, w1, w2, topk_weights, topk_ids):
+    """hidden_states bf16 [T, H]; w1 Fp4Tensor [E, 2F, H] (gate, then up rows) and w2
+    Fp4Tensor [E, H, F] of one format; topk_weights float32 [T, top_k]; topk_ids int
+    [T, top_k], every id in [0, E).  Returns bf16 [T, H].
+
+    Steps: the entries sorted by expert (blocks of one row: ragged groups need no
+    padding), the token rows gathered and cast to 4 bits, the first product, its
+    gate applied and the result cast to 4 bits in one pass, the second product
+    with each row times its routed weight and stored at its entry, the sum over a
+    token's entries."""
+    if type(w1) is not Fp4Tensor or type(w2) is not Fp4Tensor or w1.fmt != w2.fmt:
+        raise B.MgemmError("fused_experts_fp4 takes two Fp4Tensors of one format")
+    E, F2, H = w1.shape
+    F = F2 // 2
+    if F2 % 2 or w2.shape != (E, H, F):
+        raise B.MgemmError(f"fused_experts_fp4: w1 {w1.shape} and w2 {w2.shape} do not belong together")
+    if hidden_states.dtype != torch.bfloat16 or hidden_states.dim() != 2 or hidden_states.shape[1] != H:
+        raise B.MgemmError(f"fused_experts_fp4 takes bf16 hidden states [T, {H}]")
+    T, top_k = topk_ids.shape
+    x = hidden_states.contiguous()
+    dev, n, code = x.device, T * top_k, w1.code
+    bf, u8 = torch.bfloat16, torch.uint8
+    out = torch.empty(T, H, dtype=bf, device=dev)
+    if n == 0:
+        return out
+    if n <= B.MGEMM_ROUTE_ALIGN_MAX_ENTRIES:
+        sorted_ids, _, _, _, args = align_args(topk_ids, E, 1)
+    else:
+        sorted_ids, _, _, gs = align(topk_ids, E, 1)
+        args = torch.empty(B.mgemm_args_bytes(E), dtype=u8, device=dev)
+        B.mgemm_fill_args(gs, E, -1, args)
+    tiles = B.mgemm_colwise_ld(n, E)
+
+    def cast(inp, K, **how):
+        codes = torch.empty(n, K // 2, dtype=u8, device=dev)
+        sf = torch.empty(B.mgemm_fp4_scale_bytes(code, tiles, K), dtype=u8, device=dev)
+        rows = torch.empty(n, dtype=torch.float32, device=dev) if w1.fmt == "nvfp4" else None
+        B.mgemm_quant_fp4_rows(args, E, n, inp, K, code, codes, sf, rows, **how)
+        return codes, sf, rows
+
+    a1 = cast(x, H, sorted_ids=sorted_ids, numel=n, top_k=top_k)
+    h = torch.empty(n, F2, dtype=bf, device=dev)
+    B.mgemm_fwd_fp4(args, code, *a1, w1.codes, w1.scales, w1.row_scale, h, n, H, F2, E)
+    a2 = cast(h, F, gated=True)
+    c3 = torch.empty(n, H, dtype=bf, device=dev)
+    wts = topk_weights.to(torch.float32).contiguous().view(-1)
+    B.mgemm_fwd_fp4(args, code, *a2, w2.codes, w2.scales, w2.row_scale, c3, n, F, H, E, sorted_ids, n, wts)
     B.mgemm_topk_sum(c3, T, top_k, out)
     return out
