@@ -19,9 +19,9 @@
 // CTA (persistent, one per SM, 352 threads):
 //   warp 0     TMA producer: a ring of stages, as many as fit
 //   warp 1     TMEM owner; issues the MMAs
-//   warp 10    copies a stage's scales to tensor memory ahead of its MMAs (12
-//              copies of a 256-column stage cost the issuing warp as long as the
-//              MMAs take)
+//   warp 10    copies a stage's scales to tensor memory ahead of its MMAs (98304
+//              x 1408 x 2048 takes 137 us with one warp for copies and MMAs, 126
+//              with two)
 //   warps 2-9  epilogue, two per TMEM lane quarter, each half of the columns:
 //              the accumulator is read, scaled and rounded into registers,
 //              handed back, and then stored, 32 columns at a time, through a
@@ -30,15 +30,20 @@
 //              with it every barrier of the pipeline); rows of a group's edge
 //              and scattered rows are stored directly
 // TMEM: one accumulator of 256 columns or two narrower ones, then as many slots
-// of scales as fit (two to ten).  A slot is rewritten once the MMAs that read it
+// of scales as fit (two to sixteen).  A slot is rewritten once the MMAs that read it
 // have completed: the stage's empty barrier says so.
 // PAIR (groups of 256 rows and more): a cluster of two CTAs computes 256 rows by
 // bn columns with cta_group::2 MMAs of the even CTA.  Each CTA copies its 128
 // rows of A, half of B's columns and the scales of its rows and of all columns;
 // the odd CTA's copies complete on the even CTA's barriers, and commits free a
 // stage and publish the accumulator in both.  A CTA then fetches 38 KB per
-// stage instead of 54: what bounds large products is the rate at which L2 feeds
-// the SMs (about 48 bytes a clock each), not the MMAs (512 clocks a stage).
+// stage instead of 54.
+// What bounds large products (pairs, 256 columns, at 1.8 GHz): a stage takes 0.35
+// us, 0.28 (the 512 clocks of its MMAs) without its copies, 0.23 without its MMAs:
+// shared memory takes in the 38 KB and gives 38 KB to the MMAs, 600 clocks at 128
+// bytes each.  A tile adds about 1 us, most of it from the last MMA to the next
+// tile's first, while the accumulator is read; two accumulators of 192 columns,
+// which leave scales two slots, hide that and cost more (154 us for the above).
 // Every wait is bounded; on expiry the kernel records MGEMM_STATUS_TIMEOUT,
 // drains the copies and MMAs it issued, frees TMEM and returns.
 #include "fp4.cuh"
@@ -58,6 +63,11 @@ struct Fp4Params {
   int a_rows;         // rows of an A box: 128, or fewer when M is smaller (a multiple of 8)
   int stages, stage_bytes;
   int vec32;          // output rows and tiles start on 32-byte boundaries
+  // Not NULL (mgemm_gmm_fp4): the group sizes, from which the kernel makes its own
+  // schedule, so that it can start on the weights before the cast has ended (a
+  // call of one token 14.6 -> 12.5 us, one of 16 at 16 experts 62.5 -> 59.8).
+  const int64_t *sizes;
+  int64_t M;
 };
 
 constexpr int kF4Threads = 352;
@@ -84,6 +94,9 @@ struct F4Shared {
   uint32_t tmem_slot;
   int abort_flag;
   float cinv[kF4EpiWarps][128];  // the warps' column factors
+  int64_t rows_of[kF4Threads / 32];   // a warp's totals, for the scans over the groups
+  uint64_t tiles_of[kF4Threads / 32];
+  int na;
   // the active groups' first tile, expert, rows and first scale tile
   int start[kF4Groups + 1], expert[kF4Groups], row[kF4Groups], end[kF4Groups], sf[kF4Groups];
 };
@@ -130,6 +143,50 @@ __device__ __forceinline__ F4Tile f4_tile(int t, int &g, const Fp4Params &p, con
   ti.rows = max(0, min(end - ti.row0, p.a_rows));
   ti.sf_tile = sf + mt;
   return ti;
+}
+
+// The schedule of E <= 256 groups (at most kF4Groups of them active) from their
+// sizes: one thread per group, sums over the groups by warp scans.  Sizes that
+// are negative or do not sum to M leave no tile (the call's fill reports them).
+__device__ __forceinline__ void f4_schedule(const Fp4Params &p, F4Shared &S) {
+  const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
+  const int64_t m = i < p.E ? __ldcg(p.sizes + i) : 0;
+  const bool bad = m < 0 || m > p.M;
+  const uint64_t n = bad ? 0 : (uint64_t)m;
+  const uint64_t own = (n + 127) / 128 | (uint64_t)(n > 0) << 32;  // row tiles, which are the scale tiles | active
+  uint64_t rows = n, tiles = own;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const uint64_t r = __shfl_up_sync(0xffffffffu, rows, d), t = __shfl_up_sync(0xffffffffu, tiles, d);
+    if (lane >= d) {
+      rows += r;
+      tiles += t;
+    }
+  }
+  if (lane == 31) {
+    S.rows_of[warp] = (int64_t)rows;
+    S.tiles_of[warp] = tiles;
+  }
+  const bool any_bad = __syncthreads_or(bad);
+  for (int w = 0; w < warp; ++w) {
+    rows += (uint64_t)S.rows_of[w];
+    tiles += S.tiles_of[w];
+  }
+  const uint64_t before = tiles - own;
+  const int a = (int)(before >> 32);
+  if (n > 0 && !any_bad && a < kF4Groups) {
+    S.start[a] = (int)before;
+    S.expert[a] = i;
+    S.row[a] = (int)(rows - n);
+    S.end[a] = (int)rows;
+    S.sf[a] = (int)before;
+  }
+  if (i == kF4Threads - 1) {
+    const bool valid = !any_bad && (int64_t)rows == p.M;  // (then at most kF4Groups are active)
+    S.na = valid ? (int)(tiles >> 32) : 0;
+    S.start[S.na] = valid ? (int)tiles : 0;
+  }
+  __syncthreads();
 }
 
 // One lane of a converged warp.  The instructions that take uniform registers
@@ -271,25 +328,34 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = (uint32_t)uniform((int)S.tmem_slot);
-  pdl_wait();
-  pdl_trigger();
   const ArgsView av(p.args, p.E);
-  const int status0 = *av.status, na = uniform(*av.n_active);
-  const int total = uniform(status0 != 0 ? 0 : __ldg((PAIR ? av.ptile_start : av.mtile_start) + na) * p.n_tiles);
-  const int kb_count = (p.K + 255) / 256;
-  if (total > 0 && na <= kF4Groups) {
+  int na, total;
+  const bool early = !PAIR && p.sizes != nullptr;
+  if (early) {
+    f4_schedule(p, S);
+    na = uniform(S.na);
+    total = uniform(S.start[na] * p.n_tiles);
+  } else {
+    pdl_wait();
+    pdl_trigger();
+    const int status0 = *av.status;
+    na = uniform(*av.n_active);
     const int *start = PAIR ? av.ptile_start : av.mtile_start;
-    for (int i = threadIdx.x; i < na; i += kF4Threads) {
-      const int e = __ldg(av.active + i);
-      S.start[i] = __ldg(start + i);
-      S.expert[i] = e;
-      S.row[i] = (int)__ldg(av.offsets + e);
-      S.end[i] = (int)__ldg(av.offsets + e + 1);
-      S.sf[i] = (int)(__ldg(av.poffsets + e) >> 7);
+    total = uniform(status0 != 0 ? 0 : __ldg(start + na) * p.n_tiles);
+    if (total > 0 && na <= kF4Groups) {
+      for (int i = threadIdx.x; i < na; i += kF4Threads) {
+        const int e = __ldg(av.active + i);
+        S.start[i] = __ldg(start + i);
+        S.expert[i] = e;
+        S.row[i] = (int)__ldg(av.offsets + e);
+        S.end[i] = (int)__ldg(av.offsets + e + 1);
+        S.sf[i] = (int)(__ldg(av.poffsets + e) >> 7);
+      }
+      if (threadIdx.x == 0) S.start[na] = __ldg(start + na);
     }
-    if (threadIdx.x == 0) S.start[na] = __ldg(start + na);
+    __syncthreads();
   }
-  __syncthreads();
+  const int kb_count = (p.K + 255) / 256;
   int g = 0;  // the group of the last tile
   volatile int *vabort = &S.abort_flag;
   uint32_t issued = 0;  // stages armed, for the drain after an abort
@@ -301,45 +367,83 @@ __global__ void __launch_bounds__(kF4Threads, 1)
   // the MMA's columns of the tile at n0 (a pair's halves stay multiples of 32)
   auto tile_cols = [&](int n0) { return PAIR ? min(bn, (p.N - n0 + 63) & ~63) : min(bn, (p.N - n0 + 15) & ~15); };
 
+  // (a schedule of its own: all but the producer wait here for the cast)
+  if (early && warp != 0) {
+    pdl_wait();
+    pdl_trigger();
+  }
+
   if (warp == 0) {
-    int stage = 0;
-    uint32_t phase = 0;
     bool ok = true;
     const uint32_t tx = (PAIR ? 2u : 1u) * (uint32_t)p.stage_bytes;
     const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert's weights
-    for (int t = t_first; t < total && ok; t += t_step) {
-      const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
-      const int e = uniform(ti.e), n0 = uniform(ti.n0), row0 = uniform(ti.row0), sfa_tile = uniform(ti.sf_tile);
-      const int sfb_tile = e * wtiles + n0 / 128, b_row = n0 + rank * (tile_cols(n0) / 2);
-      for (int kb = 0; kb < kb_count; ++kb) {
-        if (!mbar_wait_warp(&S.empty[stage], phase ^ 1, vabort)) {
-          ok = false;
-          break;
+    // body(step, stage, phase, kb, expert, columns, rows and their scale tiles), for every stage until it returns false
+    auto for_stages = [&](auto &&body) {
+      int step = 0, stage = 0;
+      uint32_t phase = 0;
+      g = 0;
+      for (int t = t_first; t < total; t += t_step) {
+        const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
+        const int e = uniform(ti.e), n0 = uniform(ti.n0), row0 = uniform(ti.row0), sfa_tile = uniform(ti.sf_tile);
+        const int sfb_tile = e * wtiles + n0 / 128, b_row = n0 + rank * (tile_cols(n0) / 2);
+        for (int kb = 0; kb < kb_count; ++kb) {
+          if (!body(step, stage, phase, kb, e, b_row, sfb_tile, row0, sfa_tile)) return;
+          ++step;
+          if (++stage == nst) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
-        if (elect_one()) {
-          uint8_t *a = smem + (size_t)stage * op_bytes, *sf = sSF + (size_t)stage * sf_bytes;
-          if (!PAIR || rank == 0) {
+      }
+    };
+    auto put = [&](bool w, bool x, int stage, int kb, int e, int b_row, int sfb_tile, int row0, int sfa_tile) {
+      if (elect_one()) {
+        uint8_t *a = smem + (size_t)stage * op_bytes, *sf = sSF + (size_t)stage * sf_bytes;
+        if (!PAIR || rank == 0) {
+          if (w) {
             mbar_arrive_expect_tx(&S.full[stage], tx);
             tma_load_3d(a + p.a_rows * 128, &tmB, &S.full[stage], kb * 128, b_row, e);
             tma_load_3d(sf + C::WPS * 512, &tmSB, &S.full[stage], 0, kb * C::WPS, sfb_tile);
+          }
+          if (x) {
             tma_load_2d(a, &tmA, &S.full[stage], kb * 128, row0);
             tma_load_3d(sf, &tmSA, &S.full[stage], 0, kb * C::WPS, sfa_tile);
-          } else {  // complete on the even CTA's barrier
-            const uint32_t bar = cluster_addr(&S.full[stage], 0);
-            tma_load_3d_pair(a + p.a_rows * 128, &tmB, bar, kb * 128, b_row, e);
-            tma_load_3d_pair(sf + C::WPS * 512, &tmSB, bar, 0, kb * C::WPS, sfb_tile);
-            tma_load_2d_pair(a, &tmA, bar, kb * 128, row0);
-            tma_load_3d_pair(sf, &tmSA, bar, 0, kb * C::WPS, sfa_tile);
           }
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == nst) {
-          stage = 0;
-          phase ^= 1;
+        } else {  // complete on the even CTA's barrier
+          const uint32_t bar = cluster_addr(&S.full[stage], 0);
+          tma_load_3d_pair(a + p.a_rows * 128, &tmB, bar, kb * 128, b_row, e);
+          tma_load_3d_pair(sf + C::WPS * 512, &tmSB, bar, 0, kb * C::WPS, sfb_tile);
+          tma_load_2d_pair(a, &tmA, bar, kb * 128, row0);
+          tma_load_3d_pair(sf, &tmSA, bar, 0, kb * C::WPS, sfa_tile);
         }
       }
+      __syncwarp();
+      issued += w;
+    };
+    if (early) {
+      // The ring is filled with weights, then, the cast done, with the rows.  The
+      // weights may be read before this grid's wait: it is launched behind the
+      // cast alone, every CTA of which has waited for whatever came before it
+      // when it lets this grid start.
+      for_stages([&](int step, int stage, uint32_t, int kb, auto... at) {
+        if (step >= nst) return false;
+        put(true, false, stage, kb, at...);
+        return true;
+      });
+      pdl_wait();
+      pdl_trigger();
+      for_stages([&](int step, int stage, uint32_t, int kb, auto... at) {
+        if (step >= nst) return false;
+        put(false, true, stage, kb, at...);
+        return true;
+      });
     }
+    for_stages([&](int step, int stage, uint32_t phase, int kb, auto... at) {
+      if (early && step < nst) return true;
+      ok = mbar_wait_warp(&S.empty[stage], phase ^ 1, vabort);
+      if (ok) put(true, true, stage, kb, at...);
+      return ok;
+    });
     if (!ok && lane == 0) timeout();
   } else if (warp == 1) {
     int stage = 0, acc = 0, slot = 0;
@@ -671,8 +775,10 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
     return p.N > 128 ? launch_fp4<FMT, true, 2>(x, sx, w, sw, p, M, 256, sms, s)
                      : launch_fp4<FMT, true, 1>(x, sx, w, sw, p, M, 128, sms, s);
   // columns per tile: the fewest rounds of tiles over the SMs, weighted by the bytes of a stage
-  // (A's rows, the columns and their scales) ; wider at equal cost (fewer reads of A)
-  const int64_t m_est = (M + 127) / 128 > groups ? (M + 127) / 128 : groups;
+  // (A's rows, the columns and their scales); wider at equal cost (fewer reads of A)
+  // (row tiles: half a tile of each group is its ragged end, but no group has less than one.  1024 rows in 8
+  // groups of about 128 are 12 tiles, not 8: 256 columns, 29.7 us; at 8 it would be 192 and 31.8.)
+  const int64_t ragged = (M + 127) / 128 + groups / 2, m_est = ragged > groups ? ragged : groups;
   const int a_rows = M < 128 ? (int)M : 128;
   int bn = 256;
   int64_t best = -1;
@@ -688,6 +794,16 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
 }
 
 bool a16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+int fwd_fp4(int fmt, const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, const Fp4Params &p,
+            int64_t M, cudaStream_t s) {
+  const int rc = ensure_context();
+  if (rc) return rc;
+  const int sms = sm_count_cached();
+  if (sms <= 0) return MGEMM_ECUDA;
+  return fmt == MGEMM_NVFP4 ? launch_fp4<MGEMM_NVFP4>(x, sx, w, sw, p, M, sms, s)
+                            : launch_fp4<MGEMM_MXFP4>(x, sx, w, sw, p, M, sms, s);
+}
 
 // The sizes and pointers both entry points take (out is checked by each).
 int fp4_checks(int fmt, const uint8_t *w, const uint8_t *sw, const float *rw, const void *out, int64_t M, int K, int N,
@@ -729,10 +845,6 @@ extern "C" int mgemm_fwd_fp4(const void *args, int fmt, const uint8_t *x, const 
   if (!a16(args) || !a16(x) || !a16(sx) || ((uintptr_t)rx & 3) || ((uintptr_t)row_map & 3) || ((uintptr_t)row_weight & 3))
     return MGEMM_EALIGN;
   if (M == 0) return MGEMM_OK;
-  rc = ensure_context();
-  if (rc) return rc;
-  const int sms = sm_count_cached();
-  if (sms <= 0) return MGEMM_ECUDA;
   Fp4Params p{};
   p.args = (const uint8_t *)args;
   p.rx = rx;
@@ -744,8 +856,7 @@ extern "C" int mgemm_fwd_fp4(const void *args, int fmt, const uint8_t *x, const 
   p.K = K;
   p.N = N;
   p.E = E;
-  return fmt == MGEMM_NVFP4 ? launch_fp4<MGEMM_NVFP4>(x, sx, w, sw, p, M, sms, (cudaStream_t)stream)
-                            : launch_fp4<MGEMM_MXFP4>(x, sx, w, sw, p, M, sms, (cudaStream_t)stream);
+  return fwd_fp4(fmt, x, sx, w, sw, p, M, (cudaStream_t)stream);
 }
 
 extern "C" int64_t mgemm_gmm_fp4_workspace_bytes(int fmt, int64_t M, int K, int E) {
@@ -774,5 +885,15 @@ extern "C" int mgemm_gmm_fp4(const int64_t *group_sizes, int E, int fmt, const v
       rc = mgemm_quant_fp4_rows(b, E, M, x, M, K, ld_x, nullptr, 0, 1, 0, fmt, b + ws.codes, b + ws.sf, rx, stream);
   }
   if (rc) return rc;
-  return mgemm_fwd_fp4(b, fmt, b + ws.codes, b + ws.sf, rx, w, sw, rw, out, nullptr, 0, nullptr, M, K, N, E, stream);
+  Fp4Params p{};
+  p.args = b;
+  p.rx = rx;
+  p.rw = rw;
+  p.out = (__nv_bfloat16 *)out;
+  p.K = K;
+  p.N = N;
+  p.E = E;
+  p.M = M;
+  if (E <= kFp4FillMaxE && (M < E ? M : E) <= kF4Groups) p.sizes = group_sizes;  // (behind the fused cast alone)
+  return fwd_fp4(fmt, b + ws.codes, b + ws.sf, w, sw, p, M, (cudaStream_t)stream);
 }

@@ -267,6 +267,54 @@ def test_bad_group_sizes_write_nothing_and_tell():
         assert B().args_status(ws) == status and is_sentinel(out)
 
 
+def test_bad_group_sizes_of_many_groups():
+    # 256 rows announced, 5 there: more active groups than a small call can have
+    w = mg().quantize_fp4(blocky((256, 8, 32), 1), "nvfp4")
+    x = blocky((5, 32), 2)
+    out = sentinel_bf16((5, 8), DEV)
+    ws = torch.zeros(B().mgemm_gmm_fp4_workspace_bytes(w.code, 5, 32, 256), dtype=torch.uint8, device=DEV)
+    mg().gmm_fp4(x, w, torch.ones(256, dtype=torch.int64, device=DEV), out=out, workspace=ws)
+    assert B().args_status(ws) == 2 and is_sentinel(out)
+
+
+@pytest.mark.parametrize("active", [1, 127, 128, 129, 200])
+def test_many_groups_equal_one_by_one(active):
+    # up to and past the number of groups whose places the kernel keeps on chip
+    E, N, K = 200, 72, 288
+    w = mg().quantize_fp4(blocky((E, N, K), 1, -2, 2), "mxfp4")
+    sizes = torch.zeros(E, dtype=torch.int64)
+    sizes[torch.randperm(E, generator=torch.Generator().manual_seed(3))[:active]] = 1
+    sizes[int(sizes.nonzero()[active // 2])] += 2
+    M = int(sizes.sum())
+    x = blocky((M, K), 2, -2, 2)
+    out = mg().gmm_fp4(x, w, sizes.to(DEV))
+    for r, e in enumerate(torch.repeat_interleave(torch.arange(E), sizes).tolist()):
+        one = torch.zeros(E, dtype=torch.int64, device=DEV)
+        one[e] = 1
+        assert torch.equal(out[r], mg().gmm_fp4(x[r:r + 1], w, one)[0])
+
+
+def test_weights_cast_just_before_the_product():
+    # the product may start on the weights early, but not before the kernel that writes them has ended
+    E, N, K = 4, 2048, 2048
+    raw = [blocky((E, N, K), s, -2, 2) for s in range(4)]
+    x = blocky((12, K), 9, -2, 2)
+    gs = torch.tensor([3, 0, 4, 5], dtype=torch.int64, device=DEV)
+    want = []
+    for v in raw:
+        w = mg().quantize_fp4(v, "nvfp4")
+        torch.cuda.synchronize()
+        want.append(mg().gmm_fp4(x, w, gs))
+        torch.cuda.synchronize()
+    del w
+    for _ in range(5):
+        got = []
+        for v in raw:  # (each cast lands where the last one lay)
+            got.append(mg().gmm_fp4(x, mg().quantize_fp4(v, "nvfp4"), gs))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_streams_graphs_and_repeats_agree():
     w = mg().quantize_fp4(blocky((4, 520, 512), 1, -2, 2), "nvfp4")
     x = blocky((70, 512), 2, -2, 2)
