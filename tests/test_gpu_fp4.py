@@ -257,6 +257,37 @@ def test_gathered_rows_equal_the_gathered_copy(fmt):
     assert not a[0][n:].any()
 
 
+# CTAs on their own, with the schedule made from the sizes; CTA pairs; the schedule from the args block (E > 256)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("sizes,K,N", [([1, 3, 0, 40], 2080, 520), ([600, 0, 300], 1056, 520), ([2] * 300, 96, 40)])
+def test_wait_timeout_sets_status_and_leaves_the_device_usable(sizes, K, N, fmt):
+    """A second build of the library whose pipeline waits give up at once (see
+    test_gpu_wait_timeout): the kernel returns, tells, and stores nothing."""
+    import ctypes
+
+    from mixture_experts_grouped_gmm_gb300 import build
+
+    L = ctypes.CDLL(build.build_variant("mgemm_waitprobe", {"MGEMM_WAIT_LIMIT_NS": 0}))
+    for name in ("mgemm_gmm_fp4", "mgemm_last_error"):
+        res, argt = B()._SIGS[name]
+        getattr(L, name).restype = res
+        getattr(L, name).argtypes = argt
+    E, M = len(sizes), sum(sizes)
+    w = mg().quantize_fp4(blocky((E, N, K), 1, -2, 2), fmt)
+    x = blocky((M, K), 2, -2, 2)
+    gs = torch.tensor(sizes, dtype=torch.int64, device=DEV)
+    want = mg().gmm_fp4(x, w, gs)
+    p = lambda t: ctypes.c_void_p(t.data_ptr() if t is not None else None)  # noqa: E731
+    ws = torch.zeros(B().mgemm_gmm_fp4_workspace_bytes(w.code, M, K, E), dtype=torch.uint8, device=DEV)
+    out = sentinel_bf16((M, N), DEV)
+    rc = L.mgemm_gmm_fp4(p(gs), E, w.code, p(x), K, p(w.codes), p(w.scales), p(w.row_scale), p(out), M, K, N, p(ws),
+                         ws.numel(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0, f"the wait-probe build: {rc} ({L.mgemm_last_error().decode()})"
+    torch.cuda.synchronize()  # the kernel returned
+    assert B().args_status(ws) == 4 and is_sentinel(out)
+    assert torch.equal(mg().gmm_fp4(x, w, gs), want)
+
+
 def test_bad_group_sizes_write_nothing_and_tell():
     w = mg().quantize_fp4(blocky((2, 64, 64), 1), "nvfp4")
     x = blocky((8, 64), 2)
