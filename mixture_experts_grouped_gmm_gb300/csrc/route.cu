@@ -11,9 +11,9 @@
 // outside the groups kept have keys of their own, and a warp maximum is one
 // integer instruction.
 //
-// Bound by instruction issue, not by memory: an expert costs 4 bytes and some 35
-// instructions of a lane (score, key, the lane's best), a choice some 25 of the
-// warp.  So a lane keeps its three best experts in order: a choice takes the
+// Bound by instruction issue, not by memory (54 us for 65536 x 256 with groups and
+// bias, 10 of them the bytes'): an expert costs 4 bytes and some 35 instructions of
+// a lane (score, key, the lane's best), a choice some 20 of the warp.  So a lane keeps its three best experts in order: a choice takes the
 // maximum over the lanes' best and moves that lane's list up, and only a lane
 // chosen from a fourth time looks its experts over again.  Where groups are whole
 // lanes (NV divides the group, a power of two of lanes) their two best come from
@@ -32,10 +32,12 @@ constexpr uint32_t kKeyOut = 0u, kKeyOff = 1u;
 
 // Unsigned integers in the order of the floats: -0 equals +0, a NaN is the
 // largest (the sum's NaN is the positive one).
-__device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t u = __float_as_uint(v + 0.f);
+// order_bits: of a sum of which one term is at least +0, as v + 0 is.
+__device__ __forceinline__ uint32_t order_bits(float v) {
+  const uint32_t u = __float_as_uint(v);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
+__device__ __forceinline__ uint32_t order_key(float v) { return order_bits(v + 0.f); }
 
 template <typename T>
 __device__ __forceinline__ float load_logit(const T *p);
@@ -165,18 +167,21 @@ __global__ void __launch_bounds__(kRouteThreads)
   const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
   if (t >= p.T) return;  // whole warps leave together
   const int e0 = lane * NV;
+  const uint32_t below = (1u << lane) - 1;  // the lower lanes
   const L *row = logits + t * p.ld;
   uint32_t key[NV];  // the order of the choice
   float m = 0.f, sum = 1.f;
   {
-    float s[NV];  // logits, then scores, of softmax times their sum (0 where off)
+    float s[NV];  // logits, then softmax's scores times their sum (0 where off)
     load_lane<NV>(row, e0, p.E, p.vec, -INFINITY, s);
-    if (p.sigmoid) {
+    if (p.sigmoid && bias) {
+      float b[NV];
+      load_lane<NV>(bias, e0, p.E, p.vec_bias, 0.f, b);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        key[j] = s[j] <= MGEMM_ROUTE_MASKED ? kKeyOff : 2u;
-        s[j] = sigmoidf(s[j]);
-      }
+      for (int j = 0; j < NV; ++j) key[j] = s[j] <= MGEMM_ROUTE_MASKED ? kKeyOff : order_bits(sigmoidf(s[j]) + b[j]);
+    } else if (p.sigmoid) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) key[j] = s[j] <= MGEMM_ROUTE_MASKED ? kKeyOff : order_key(sigmoidf(s[j]));
     } else {
       uint32_t most = kKeyOff;
 #pragma unroll
@@ -194,16 +199,12 @@ __global__ void __launch_bounds__(kRouteThreads)
       }
       sum = lanes_sum(sum);
       if (sum == 0.f) sum = 1.f;  // every expert is off
-    }
-    if (bias) {
-      float b[NV];
-      load_lane<NV>(bias, e0, p.E, p.vec_bias, 0.f, b);
+      if (bias) {
+        float b[NV];
+        load_lane<NV>(bias, e0, p.E, p.vec_bias, 0.f, b);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) s[j] = (p.sigmoid ? s[j] : s[j] / sum) + b[j];
-    }
-    if (p.sigmoid || bias) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) key[j] = key[j] == kKeyOff ? kKeyOff : order_key(s[j]);
+        for (int j = 0; j < NV; ++j) key[j] = key[j] == kKeyOff ? kKeyOff : order_bits(s[j] / sum + b[j]);
+      }
     }
   }
   if (p.E < 32 * NV) {
@@ -281,32 +282,30 @@ __global__ void __launch_bounds__(kRouteThreads)
     best = three_best(key);
   }
 
-  // the top_k keys, largest first; lane r keeps the id of pick r (top_k <= 32).
-  // A lane's own picks are bits of `taken`, `left` what remains of its list.
-  int my_id = 0, left = 3;
-  uint32_t taken = 0;
+  // the top_k keys, largest first (top_k <= 32); the lane a pick comes from notes it
+  // and moves its list up
+  __shared__ int picks[kRouteThreads];
+  int *pick = picks + (threadIdx.x & ~31);
   for (int r = 0; r < p.top_k; ++r) {
     const uint32_t top = __reduce_max_sync(kFull, best.k1);
-    const int src = __ffs(__ballot_sync(kFull, best.k1 == top)) - 1;
-    const int id = __shfl_sync(kFull, e0 + best.j1, src);
-    if (lane == r) my_id = id;
-    if (lane == src) {
-      taken |= 1u << best.j1;
-      best.k1 = best.k2;
-      best.j1 = best.j2;
-      best.k2 = best.k3;
-      best.j2 = best.j3;
-      best.k3 = kKeyOut;
-      --left;
-    }
-    if (NV > 3 && left == 0) {
+    const uint32_t tied = __ballot_sync(kFull, best.k1 == top);
+    const bool mine = best.k1 == top && (tied & below) == 0;
+    const int j = best.j1;
+    if (mine) pick[r] = e0 + j;
+    best.k1 = mine ? best.k2 : best.k1;
+    best.j1 = mine ? best.j2 : j;
+    best.k2 = mine ? best.k3 : best.k2;
+    best.j2 = mine ? best.j3 : best.j2;
+    best.k3 = mine ? kKeyOut : best.k3;
+    if (NV > 3 && mine && best.k1 == kKeyOut) {  // what comes after this pick
       uint32_t rest[NV];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) rest[j] = (taken >> j) & 1u ? kKeyOut : key[j];
+      for (int i = 0; i < NV; ++i) rest[i] = key[i] < top || (key[i] == top && i > j) ? key[i] : kKeyOut;
       best = three_best(rest);
-      left = 3;
     }
   }
+  __syncwarp();
+  const int my_id = lane < p.top_k ? pick[lane] : 0;
   // the picks' scores, one per lane
   float s = 0.f;
   if (lane < p.top_k) {
@@ -355,7 +354,7 @@ __device__ __forceinline__ float route_score_rest(float l) {  // 1 - sigmoid(l);
 // zeros written around them: a CTA clears the rows of its kBwdTokens tokens with
 // 16-byte stores, computes a pick per thread meanwhile, and stores the picks after
 // a barrier.  (A warp per token spends 230 instructions on it, 26 us for 65536 x
-// 256; so they are 13.)
+// 256; so they are 15.)
 constexpr int kBwdTokens = 32;
 
 template <typename L>
