@@ -84,7 +84,9 @@ struct RowCast {
   uint32_t v[NB][P][8];
   float amax[NB];
 
-  __device__ __forceinline__ void load(const RowReader &rd, int q0, int nblk, int tid) {
+  // (meanwhile() runs while the loads are under way)
+  template <typename Work>
+  __device__ __forceinline__ void load(const RowReader &rd, int q0, int nblk, int tid, Work &&meanwhile) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int q = q0 + i * TPR + tid;
@@ -98,6 +100,7 @@ struct RowCast {
         }
       }
     }
+    meanwhile();
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       amax[i] = amax16(v[i][0]);
@@ -166,29 +169,32 @@ __device__ __forceinline__ float row_max(float a, float *sh) {
   return a;
 }
 
-template <int FMT, int NB, int TPR>
-__device__ __forceinline__ void cast_row(const RowReader &rd, int K, int64_t tile_row, int W, uint8_t *codes, uint8_t *sf,
+// place(): the row's place in the scale tiles
+template <int FMT, int NB, int TPR, typename Place>
+__device__ __forceinline__ void cast_row(const RowReader &rd, int K, Place &&place, int W, uint8_t *codes, uint8_t *sf,
                                          float *row_scale, int tid, float *sh) {
   using F = Fp4<FMT>;
   const int nblk = K / F::BLOCK;
   RowCast<FMT, NB, TPR> c;
   float R = 1.f, Rinv = 1.f;
   const bool once = nblk <= NB * TPR;  // the whole row is held
-  c.load(rd, 0, nblk, tid);
+  int64_t tile_row;
+  auto nothing = [] {};
+  c.load(rd, 0, nblk, tid, [&] { tile_row = place(); });
   if (F::NV) {
     float a = c.most();
     for (int q0 = NB * TPR; q0 < nblk; q0 += NB * TPR) {
-      c.load(rd, q0, nblk, tid);
+      c.load(rd, q0, nblk, tid, nothing);
       a = fmaxf(a, c.most());
     }
     R = fp4_pow2_scale(kNvfp4RowMax, row_max<TPR>(a, sh));
     Rinv = __frcp_rn(R);  // a power of two
     if (tid == 0) *row_scale = R;
-    if (!once) c.load(rd, 0, nblk, tid);
+    if (!once) c.load(rd, 0, nblk, tid, nothing);
   }
   c.store(0, nblk, W, R, Rinv, tile_row, codes, sf, tid);
   for (int q0 = NB * TPR; q0 < 4 * W; q0 += NB * TPR) {
-    c.load(rd, q0, nblk, tid);
+    c.load(rd, q0, nblk, tid, nothing);
     c.store(q0, nblk, W, R, Rinv, tile_row, codes, sf, tid);
   }
 }
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(kQuantThreads)
       }
       const int64_t row = e * S.N + n;
       const RowReader rd{S.in + row * S.ld, nullptr, S.vec32};
-      cast_row<FMT, NB, TPR>(rd, K, i, W, codes + row * (K / 2), sf, row_scale + row, tid, sh[odd ^= 1]);
+      cast_row<FMT, NB, TPR>(rd, K, [&] { return i; }, W, codes + row * (K / 2), sf, row_scale + row, tid, sh[odd ^= 1]);
     }
     return;
   }
@@ -224,11 +230,12 @@ __global__ void __launch_bounds__(kQuantThreads)
   const int64_t total = __ldg(av.offsets + S.E);
   const int64_t rows = total < S.M ? total : S.M;
   for (int64_t i = first; i < rows; i += step) {
-    // the group of row i: as many groups end at or before it
-    int e = 0;
-    for (int j = lane; j < S.E; j += 32) e += __ldg(av.offsets + j + 1) <= i;
-    e = __reduce_add_sync(0xffffffffu, e);
-    const int64_t tile_row = __ldg(av.poffsets + e) + (i - __ldg(av.offsets + e));
+    auto place = [&] {  // the group of row i: as many groups end at or before it
+      int e = 0;
+      for (int j = lane; j < S.E; j += 32) e += __ldg(av.offsets + j + 1) <= i;
+      e = __reduce_add_sync(0xffffffffu, e);
+      return (int64_t)__ldg(av.poffsets + e) + (i - (int64_t)__ldg(av.offsets + e));
+    };
     RowReader rd{nullptr, nullptr, S.vec32};
     if (S.ids) {
       const int32_t id = __ldg(S.ids + i);
@@ -237,7 +244,7 @@ __global__ void __launch_bounds__(kQuantThreads)
       rd.row = S.in + i * S.ld;
       if (S.gated) rd.up = rd.row + K;
     }
-    cast_row<FMT, NB, TPR>(rd, K, tile_row, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1]);
+    cast_row<FMT, NB, TPR>(rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1]);
   }
 }
 
@@ -275,12 +282,14 @@ __global__ void __launch_bounds__(kQuantThreads)
   const int W = fp4_words(FMT, K);
   int odd = 0;
   for (int64_t i = (int64_t)(blockIdx.x - 1) * kRows + threadIdx.x / TPR; i < S.M; i += (int64_t)(gridDim.x - 1) * kRows) {
-    int e = 0;
-    for (int j = lane; j < S.E; j += 32) e += ends[j] <= (int)i;
-    e = __reduce_add_sync(0xffffffffu, e);
-    const int64_t tile_row = starts[e] + (i - (e > 0 ? ends[e - 1] : 0));
+    auto place = [&] {
+      int e = 0;
+      for (int j = lane; j < S.E; j += 32) e += ends[j] <= (int)i;
+      e = __reduce_add_sync(0xffffffffu, e);
+      return starts[e] + (i - (e > 0 ? ends[e - 1] : 0));
+    };
     const RowReader rd{S.in + i * S.ld, nullptr, S.vec32};
-    cast_row<FMT, NB, TPR>(rd, K, tile_row, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1]);
+    cast_row<FMT, NB, TPR>(rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1]);
   }
 }
 
@@ -374,7 +383,8 @@ int launch_quant(QuantSource S, int64_t rows, int K, uint8_t *codes, uint8_t *sf
   const int nblk = K / Fp4<FMT>::BLOCK;
   constexpr int U = Fp4<FMT>::BLOCK / 16;
   auto go = [&](auto kernel, auto fill_kernel, int per_cta) {
-    const int64_t want = (rows + per_cta - 1) / per_cta, cap = (int64_t)sms * 16;
+    // (with the fill every CTA scans the sizes first: fewer of them)
+    const int64_t want = (rows + per_cta - 1) / per_cta, cap = (int64_t)sms * (sizes ? 6 : 16);
     const unsigned grid = (unsigned)(want < cap ? want : cap);
     if (sizes)
       return launch_pdl(fill_kernel, dim3(grid + 1), dim3(kQuantThreads), 0, s, 1, what, sizes, args, S, K, codes, sf,
@@ -447,8 +457,10 @@ extern "C" int mgemm_dequant_fp4(const uint8_t *codes, const uint8_t *sf, const 
   if (grid < 0) return MGEMM_ECUDA;
   const int steps = (K / 16 + 31) / 32, room = sm_count_cached() * 2 / grid;  // warps a row: two CTAs for each SM
   const int parts = room < 1 ? 1 : room < steps ? room : steps;
-  auto *kernel = parts > 1 ? (fmt == MGEMM_NVFP4 ? dequant_fp4_kernel<MGEMM_NVFP4, true> : dequant_fp4_kernel<MGEMM_MXFP4, true>)
-                           : (fmt == MGEMM_NVFP4 ? dequant_fp4_kernel<MGEMM_NVFP4, false> : dequant_fp4_kernel<MGEMM_MXFP4, false>);
+  const bool nv = fmt == MGEMM_NVFP4;
+  auto *kernel = parts > 1 ? nv ? dequant_fp4_kernel<MGEMM_NVFP4, true> : dequant_fp4_kernel<MGEMM_MXFP4, true>
+                 : nv      ? dequant_fp4_kernel<MGEMM_NVFP4, false>
+                           : dequant_fp4_kernel<MGEMM_MXFP4, false>;
   return launch_pdl(kernel, dim3((unsigned)grid, (unsigned)parts), dim3(256), 0, (cudaStream_t)stream, 1,
                     "mgemm_dequant_fp4 launch", codes, sf, row_scale, (int64_t)E, N, K, (__nv_bfloat16 *)out, ld_out,
                     ((uintptr_t)out & 31) == 0 && ld_out % 16 == 0);
