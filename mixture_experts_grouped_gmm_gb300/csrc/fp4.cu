@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kQuantThreads)
 
 // mgemm_fill_args and the cast of the token rows in one launch, for at most
 // kQuantThreads groups: CTA 0 fills the args block, the others scan the group
-// sizes themselves (a thread per group, two block scans) for the rows' places, so
+// sizes themselves (a thread per group) for the rows' places, so
 // that they need not wait for it.  Rows are cast as above, and under the same
 // conditions: none when the sizes are not valid.
 template <int FMT, int NB, int TPR>
@@ -265,18 +265,15 @@ __global__ void __launch_bounds__(kQuantThreads)
     return;
   }
   __shared__ int ends[kQuantThreads], starts[kQuantThreads];  // a group's last row + 1, its first tile row
-  __shared__ int64_t tot[kQuantThreads / 32];
-  __shared__ int64_t all;
+  __shared__ GroupSums sums;
   __shared__ float sh[2][kQuantThreads / 32];
-  const bool bad = __syncthreads_or(m < 0);
-  const int64_t end = block_inclusive_scan<int64_t, kQuantThreads>(m, tot);
-  const int64_t padded = (m + kColPad - 1) / kColPad * kColPad;
-  const int64_t pend = block_inclusive_scan<int64_t, kQuantThreads>(padded, tot);
-  if (threadIdx.x == kQuantThreads - 1) all = end;
+  int64_t end;
+  uint64_t tiles;
+  const bool valid = scan_groups<kQuantThreads>(m, S.M, sums, end, tiles);
+  if (!valid) return;
   ends[threadIdx.x] = (int)end;
-  starts[threadIdx.x] = (int)(pend - padded);
+  starts[threadIdx.x] = ((int)tiles - (int)((m + 127) / 128)) * 128;
   __syncthreads();
-  if (bad || all != S.M) return;
   constexpr int kRows = kQuantThreads / TPR;
   const int lane = threadIdx.x & 31, tid = threadIdx.x % TPR;
   const int W = fp4_words(FMT, K);

@@ -64,6 +64,47 @@ __device__ __forceinline__ float fp4_pow2_scale(float num, float amax) {
 }
 constexpr float kMxfp4Max = 6.f, kNvfp4RowMax = 2688.f;  // 6 x 448
 
+static_assert(kColPad == 128, "a padded group is whole scale tiles");
+
+// Sums over the groups, one thread a group (m: its rows, 0 past the last): through
+// this one, its rows, and its 128-row tiles | the groups with rows << 32.  False, in
+// every thread, where a size is negative or the sizes do not sum to M < 2^31.
+struct GroupSums {
+  int64_t rows[32];
+  uint64_t tiles[32];
+};
+template <int THREADS>
+__device__ __forceinline__ bool scan_groups(int64_t m, int64_t M, GroupSums &sums, int64_t &rows, uint64_t &tiles) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool bad = m < 0 || m > M;  // (a sum of such sizes stays below 2^41)
+  rows = bad ? 0 : m;
+  tiles = (uint64_t)(rows + 127) / 128 | (uint64_t)(rows > 0) << 32;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int64_t r = __shfl_up_sync(0xffffffffu, rows, d);
+    const uint64_t t = __shfl_up_sync(0xffffffffu, tiles, d);
+    if (lane >= d) {
+      rows += r;
+      tiles += t;
+    }
+  }
+  if (lane == 31) {
+    sums.rows[warp] = rows;
+    sums.tiles[warp] = tiles;
+  }
+  const bool any_bad = __syncthreads_or(bad);
+  int64_t all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) {
+      rows += sums.rows[w];
+      tiles += sums.tiles[w];
+    }
+    all += sums.rows[w];
+  }
+  return !any_bad && all == M;
+}
+
 // mgemm_fill_args and mgemm_quant_fp4_rows (plain rows) in one launch; E <= kFp4FillMaxE.
 constexpr int kFp4FillMaxE = 256;
 int fp4_fill_quant_rows(const int64_t *sizes, int E, int64_t M, uint8_t *args, const __nv_bfloat16 *x, int K,

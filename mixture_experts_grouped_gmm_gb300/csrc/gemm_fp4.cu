@@ -94,8 +94,7 @@ struct F4Shared {
   uint32_t tmem_slot;
   int abort_flag;
   float cinv[kF4EpiWarps][128];  // the warps' column factors
-  int64_t rows_of[kF4Threads / 32];   // a warp's totals, for the scans over the groups
-  uint64_t tiles_of[kF4Threads / 32];
+  GroupSums sums;
   int na;
   // the active groups' first tile, expert, rows and first scale tile
   int start[kF4Groups + 1], expert[kF4Groups], row[kF4Groups], end[kF4Groups], sf[kF4Groups];
@@ -145,44 +144,22 @@ __device__ __forceinline__ F4Tile f4_tile(int t, int &g, const Fp4Params &p, con
   return ti;
 }
 
-// The schedule of E <= 256 groups (at most kF4Groups of them active) from their
-// sizes: one thread per group, sums over the groups by warp scans.  Sizes that
-// are negative or do not sum to M leave no tile (the call's fill reports them).
+// The schedule of E <= 256 groups, at most kF4Groups of them with rows, from their
+// sizes.  Sizes that do not fit leave no tile (the call's fill reports them).
 __device__ __forceinline__ void f4_schedule(const Fp4Params &p, F4Shared &S) {
-  const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
+  const int i = threadIdx.x;
   const int64_t m = i < p.E ? __ldcg(p.sizes + i) : 0;
-  const bool bad = m < 0 || m > p.M;
-  const uint64_t n = bad ? 0 : (uint64_t)m;
-  const uint64_t own = (n + 127) / 128 | (uint64_t)(n > 0) << 32;  // row tiles, which are the scale tiles | active
-  uint64_t rows = n, tiles = own;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    const uint64_t r = __shfl_up_sync(0xffffffffu, rows, d), t = __shfl_up_sync(0xffffffffu, tiles, d);
-    if (lane >= d) {
-      rows += r;
-      tiles += t;
-    }
-  }
-  if (lane == 31) {
-    S.rows_of[warp] = (int64_t)rows;
-    S.tiles_of[warp] = tiles;
-  }
-  const bool any_bad = __syncthreads_or(bad);
-  for (int w = 0; w < warp; ++w) {
-    rows += (uint64_t)S.rows_of[w];
-    tiles += S.tiles_of[w];
-  }
-  const uint64_t before = tiles - own;
-  const int a = (int)(before >> 32);
-  if (n > 0 && !any_bad && a < kF4Groups) {
-    S.start[a] = (int)before;
+  int64_t rows;
+  uint64_t tiles;
+  const bool valid = scan_groups<kF4Threads>(m, p.M, S.sums, rows, tiles);
+  if (valid && m > 0) {
+    const int a = (int)(tiles >> 32) - 1;
     S.expert[a] = i;
-    S.row[a] = (int)(rows - n);
+    S.row[a] = (int)(rows - m);
     S.end[a] = (int)rows;
-    S.sf[a] = (int)before;
+    S.start[a] = S.sf[a] = (int)tiles - (int)((m + 127) / 128);  // (row tiles are scale tiles)
   }
   if (i == kF4Threads - 1) {
-    const bool valid = !any_bad && (int64_t)rows == p.M;  // (then at most kF4Groups are active)
     S.na = valid ? (int)(tiles >> 32) : 0;
     S.start[S.na] = valid ? (int)tiles : 0;
   }
