@@ -53,12 +53,41 @@ __device__ __forceinline__ float load_logit<__nv_bfloat16>(const __nv_bfloat16 *
 // (a correctly rounded reciprocal is the correctly rounded quotient 1 / x)
 __device__ __forceinline__ float sigmoidf(float l) { return __frcp_rn(1.f + expf(-l)); }
 
-// Sum over SW lanes (a warp, or an aligned part of one).
-template <int SW = 32>
+// Sum over SW lanes (a warp, or an aligned part of one), neighbours first; and over
+// a lane's values likewise, so that a token's sum does not change with its lanes.
+template <int SW>
 __device__ __forceinline__ float lanes_sum(float a) {
 #pragma unroll
-  for (int o = SW / 2; o > 0; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
+  for (int o = 1; o < SW; o <<= 1) a += __shfl_xor_sync(kFull, a, o);
   return a;
+}
+template <int N>
+__device__ __forceinline__ float pairs_sum(const float (&v)[N]) {
+  float t[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) t[j] = v[j];
+#pragma unroll
+  for (int o = 1; o < N; o <<= 1)
+#pragma unroll
+    for (int j = 0; j + o < N; j += 2 * o) t[j] += t[j + o];
+  return t[0];
+}
+
+// The maximum of SW lanes' values, and which of them a predicate holds for.
+template <int SW>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (SW == 32) {
+    return __reduce_max_sync(kFull, v);
+  } else {
+#pragma unroll
+    for (int o = SW / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+  }
+}
+template <int SW>
+__device__ __forceinline__ uint32_t lanes_where(bool b) {
+  const uint32_t all = __ballot_sync(kFull, b);
+  return SW == 32 ? all : (all >> (threadIdx.x & 31 & ~(SW - 1))) & ((1u << (SW & 31)) - 1);
 }
 
 constexpr int kRouteThreads = 256;
@@ -157,15 +186,22 @@ __device__ __forceinline__ Best three_best(const uint32_t (&key)[N]) {
 }
 
 // GROUPS: 0 none; 1 groups of p.lanes_per_group whole lanes; 2 any groups.
-template <int NV, int GROUPS, typename L>
+// SW lanes per token: half a warp for many tokens of at most 64 experts, 8 picks and
+// no groups (a step then serves two tokens: 131072 x 64, 6 picks, 29.7 us, 36.4 with
+// whole warps, and 16384 of them 5.3 and 5.6; but a maximum takes longer: 4096 x 32,
+// where the tokens do not fill the SMs' warps, 2.2 and 2.05; 16 picks: no gain).
+template <int NV, int GROUPS, int SW, typename L>
 __global__ void __launch_bounds__(kRouteThreads)
     route_kernel(const L *__restrict__ logits, const float *__restrict__ bias, const RouteParams p,
                  float *__restrict__ weights, int32_t *__restrict__ ids) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / 32) + (threadIdx.x >> 5);
-  if (t >= p.T) return;  // whole warps leave together
+  static_assert(SW == 32 || GROUPS == 0, "groups take a warp per token");
+  const int lane = threadIdx.x & (SW - 1);
+  const int64_t t0 = (int64_t)blockIdx.x * (kRouteThreads / SW) + threadIdx.x / SW;
+  if (t0 - (threadIdx.x & 31) / SW >= p.T) return;  // whole warps leave together
+  const bool live = SW == 32 || t0 < p.T;
+  const int64_t t = live ? t0 : p.T - 1;
   const int e0 = lane * NV;
   const uint32_t below = (1u << lane) - 1;  // the lower lanes
   const L *row = logits + t * p.ld;
@@ -189,15 +225,11 @@ __global__ void __launch_bounds__(kRouteThreads)
         key[j] = s[j] <= MGEMM_ROUTE_MASKED ? kKeyOff : order_key(s[j]);
         most = max(most, key[j]);
       }
-      most = __reduce_max_sync(kFull, most);
+      most = lanes_max<SW>(most);
       m = most == kKeyOff ? 0.f : key_value(most);
-      sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        s[j] = key[j] == kKeyOff ? 0.f : expf(s[j] - m);
-        sum += s[j];
-      }
-      sum = lanes_sum(sum);
+      for (int j = 0; j < NV; ++j) s[j] = key[j] == kKeyOff ? 0.f : expf(s[j] - m);
+      sum = lanes_sum<SW>(pairs_sum(s));
       if (sum == 0.f) sum = 1.f;  // every expert is off
       if (bias) {
         float b[NV];
@@ -207,7 +239,7 @@ __global__ void __launch_bounds__(kRouteThreads)
       }
     }
   }
-  if (p.E < 32 * NV) {
+  if (p.E < SW * NV) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (e0 + j >= p.E) key[j] = kKeyOut;
@@ -282,13 +314,13 @@ __global__ void __launch_bounds__(kRouteThreads)
     best = three_best(key);
   }
 
-  // the top_k keys, largest first (top_k <= 32); the lane a pick comes from notes it
+  // the top_k keys, largest first (top_k <= SW); the lane a pick comes from notes it
   // and moves its list up
   __shared__ int picks[kRouteThreads];
-  int *pick = picks + (threadIdx.x & ~31);
+  int *pick = picks + (threadIdx.x & ~(SW - 1));
   for (int r = 0; r < p.top_k; ++r) {
-    const uint32_t top = __reduce_max_sync(kFull, best.k1);
-    const uint32_t tied = __ballot_sync(kFull, best.k1 == top);
+    const uint32_t top = lanes_max<SW>(best.k1);
+    const uint32_t tied = lanes_where<SW>(best.k1 == top);
     const bool mine = best.k1 == top && (tied & below) == 0;
     const int j = best.j1;
     if (mine) pick[r] = e0 + j;
@@ -313,10 +345,10 @@ __global__ void __launch_bounds__(kRouteThreads)
     if (!(l <= MGEMM_ROUTE_MASKED)) s = p.sigmoid ? sigmoidf(l) : expf(l - m) / sum;
   }
   if (p.renormalize) {
-    const float total = lanes_sum(s);
+    const float total = lanes_sum<SW>(s);
     s = total == 0.f ? 0.f : s / total;
   }
-  if (lane < p.top_k) {
+  if (live && lane < p.top_k) {
     weights[t * p.top_k + lane] = s * p.scale;
     ids[t * p.top_k + lane] = my_id;
   }
@@ -441,35 +473,66 @@ __global__ void __launch_bounds__(kRouteThreads)
     const int id = __ldg(ids + t * p.top_k + r);
     if (id >= 0 && id < p.E) f += __ldg(grad_w + t * p.top_k + r) * __ldg(weights + t * p.top_k + r);
   }
-  for (int u = lane; u < n; u += SW) {
-    float v[U];
-    load_values<U>(row + u * U, true, v);
+  // the lane's first two units stay in registers
+  constexpr int H = 2;
+  float v[H][U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) m = fmaxf(m, v[i]);
+  for (int h = 0; h < H; ++h) {
+    if (h * SW + lane < n) {
+      load_values<U>(row + (h * SW + lane) * U, true, v[h]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < U; ++i) v[h][i] = -INFINITY;
+    }
   }
+#pragma unroll
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int i = 0; i < U; ++i) m = fmaxf(m, v[h][i]);
+  // the others are read again for each use
+  auto others = [&](auto &&use) {
+    for (int u = H * SW + lane; u < n; u += SW) {
+      float x[U];
+      load_values<U>(row + u * U, true, x);
+      use(u, x);
+    }
+  };
+  others([&](int, const float(&x)[U]) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) m = fmaxf(m, x[i]);
+  });
   for (int e = n * U + lane; e < p.E; e += SW) m = fmaxf(m, load_logit(row + e));
 #pragma unroll
   for (int o = SW / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
   if (m <= MGEMM_ROUTE_MASKED) m = 0.f;
   auto term = [&](float l) { return l <= MGEMM_ROUTE_MASKED ? 0.f : expf(l - m); };
-  for (int u = lane; u < n; u += SW) {
-    float v[U];
-    load_values<U>(row + u * U, true, v);
 #pragma unroll
-    for (int i = 0; i < U; ++i) sum += term(v[i]);
-  }
+  for (int h = 0; h < H; ++h)
+    if (h * SW < n) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) sum += v[h][i] = term(v[h][i]);
+    }
+  others([&](int, const float(&x)[U]) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) sum += term(x[i]);
+  });
   for (int e = n * U + lane; e < p.E; e += SW) sum += term(load_logit(row + e));
   sum = lanes_sum<SW>(sum);
   f = lanes_sum<SW>(f);
   const float c = sum == 0.f ? 0.f : -f / sum;
   if (live) {
-    for (int u = lane; u < n; u += SW) {
-      float v[U];
-      load_values<U>(row + u * U, true, v);
 #pragma unroll
-      for (int i = 0; i < U; ++i) v[i] = term(v[i]) * c;
-      store_unit(out + u * U, v);
-    }
+    for (int h = 0; h < H; ++h)
+      if (h * SW + lane < n) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) v[h][i] *= c;
+        store_unit(out + (h * SW + lane) * U, v[h]);
+      }
+    others([&](int u, float(&x)[U]) {
+#pragma unroll
+      for (int i = 0; i < U; ++i) x[i] = term(x[i]) * c;
+      store_unit(out + u * U, x);
+    });
     for (int e = n * U + lane; e < p.E; e += SW) store_grad(out + e, term(load_logit(row + e)) * c);
   }
   __syncwarp();
@@ -503,25 +566,31 @@ bool route_sizes_ok(int64_t T, int E, int top_k, int64_t ld) {
 template <typename L, int GROUPS>
 int launch_route_nv(int nv, const void *logits, const float *bias, const RouteParams &p, float *weights, int32_t *ids,
                     cudaStream_t s) {
-  const int per_cta = kRouteThreads / 32;
-  const unsigned blocks = (unsigned)((p.T + per_cta - 1) / per_cta);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, dim3(blocks), dim3(kRouteThreads), 0, s, 1, "mgemm_route launch", (const L *)logits, bias,
-                      p, weights, ids);
+  auto go = [&](auto kernel, int per_cta = kRouteThreads / 32) {
+    return launch_pdl(kernel, dim3((unsigned)((p.T + per_cta - 1) / per_cta)), dim3(kRouteThreads), 0, s, 1,
+                      "mgemm_route launch", (const L *)logits, bias, p, weights, ids);
   };
+  if constexpr (GROUPS == 0) {
+    if (p.E <= 64 && p.top_k <= 8 && p.T > (int64_t)sm_count_cached() * 64) {
+      constexpr int per = kRouteThreads / 16;
+      return p.E <= 16   ? go(route_kernel<1, 0, 16, L>, per)
+             : p.E <= 32 ? go(route_kernel<2, 0, 16, L>, per)
+                         : go(route_kernel<4, 0, 16, L>, per);
+    }
+  }
   switch (nv) {  // (the sizes route_lanes chooses from)
-    case 1: return go(route_kernel<1, GROUPS, L>);
-    case 2: return go(route_kernel<2, GROUPS, L>);
-    case 4: return go(route_kernel<4, GROUPS, L>);
-    case 8: return go(route_kernel<8, GROUPS, L>);
-    case 16: return go(route_kernel<16, GROUPS, L>);
-    case 32: return go(route_kernel<32, GROUPS, L>);
+    case 1: return go(route_kernel<1, GROUPS, 32, L>);
+    case 2: return go(route_kernel<2, GROUPS, 32, L>);
+    case 4: return go(route_kernel<4, GROUPS, 32, L>);
+    case 8: return go(route_kernel<8, GROUPS, 32, L>);
+    case 16: return go(route_kernel<16, GROUPS, 32, L>);
+    case 32: return go(route_kernel<32, GROUPS, 32, L>);
   }
   if constexpr (GROUPS == 1) {
-    if (nv == 3) return go(route_kernel<3, GROUPS, L>);
-    if (nv == 5) return go(route_kernel<5, GROUPS, L>);
-    if (nv == 10) return go(route_kernel<10, GROUPS, L>);
-    if (nv == 12) return go(route_kernel<12, GROUPS, L>);
+    if (nv == 3) return go(route_kernel<3, GROUPS, 32, L>);
+    if (nv == 5) return go(route_kernel<5, GROUPS, 32, L>);
+    if (nv == 10) return go(route_kernel<10, GROUPS, 32, L>);
+    if (nv == 12) return go(route_kernel<12, GROUPS, 32, L>);
   }
   return MGEMM_EINVAL;
 }

@@ -188,6 +188,28 @@ def test_no_tokens_and_repeatable():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k", [(1, 1), (5, 3), (16, 8), (17, 8), (33, 6), (64, 6), (64, 9), (65, 6), (128, 8)])
+def test_a_token_alone_equals_a_token_of_many(scoring, E, k):
+    # (many tokens of few experts are laid out otherwise)
+    T = 20001
+    l = torch.randn(T, E, generator=torch.Generator(device=DEV).manual_seed(E), device=DEV)
+    l[::7, E // 2] = -torch.inf
+    b = torch.linspace(-0.1, 0.1, E, device=DEV)
+    g = torch.randn(T, k, device=DEV)
+    for renorm in (False, True):
+        w, ids = moe().route_experts(l, k, scoring, b, renormalize=renorm)
+        d = moe().route_experts_backward(g, l, w, ids, scoring, renorm)
+        for a in (0, 11, T - 21):
+            n = slice(a, a + 21)
+            w1, ids1 = moe().route_experts(l[n], k, scoring, b, renormalize=renorm)
+            assert torch.equal(ids[n], ids1) and torch.equal(w[n], w1)
+            assert torch.equal(d[n], moe().route_experts_backward(g[n], l[n], w1, ids1, scoring, renorm))
+            _, want = router.route(l[n].double().cpu().numpy(), k, scoring, None, renormalize=renorm)
+            w2, ids2 = moe().route_experts(l, k, scoring, renormalize=renorm)
+            assert np.array_equal(ids2[n].cpu().numpy(), want)
+
+
 def test_offsets_past_32_bits():
     T, E, k = (1 << 21) + 5, 1024, 4                       # T E > 2^31 elements
     l = torch.zeros(T, E, dtype=torch.bfloat16, device=DEV)
