@@ -381,7 +381,7 @@ int launch_quant(QuantSource S, int64_t rows, int K, uint8_t *codes, uint8_t *sf
   constexpr int U = Fp4<FMT>::BLOCK / 16;
   auto go = [&](auto kernel, auto fill_kernel, int per_cta) {
     // (with the fill every CTA scans the sizes first: fewer of them)
-    const int64_t want = (rows + per_cta - 1) / per_cta, cap = (int64_t)sms * (sizes ? 6 : 16);
+    const int64_t want = (rows + per_cta - 1) / per_cta, cap = (int64_t)sms * (sizes ? 6 : 32);
     const unsigned grid = (unsigned)(want < cap ? want : cap);
     if (sizes)
       return launch_pdl(fill_kernel, dim3(grid + 1), dim3(kQuantThreads), 0, s, 1, what, sizes, args, S, K, codes, sf,
