@@ -32,7 +32,7 @@
 // TMEM: one accumulator of 256 columns or two narrower ones, then as many slots
 // of scales as fit (two to sixteen).  A slot is rewritten once the MMAs that read it
 // have completed: the stage's empty barrier says so.
-// PAIR (groups of 256 rows and more): a cluster of two CTAs computes 256 rows by
+// PAIR (most groups of 256 rows and more, some of 128; see launch_fp4): a cluster of two CTAs computes 256 rows by
 // bn columns with cta_group::2 MMAs of the even CTA.  Each CTA copies its 128
 // rows of A, half of B's columns and the scales of its rows and of all columns;
 // the odd CTA's copies complete on the even CTA's barriers, and commits free a
@@ -46,6 +46,8 @@
 // which leave scales two slots, hide that and cost more (154 us for the above).
 // Every wait is bounded; on expiry the kernel records MGEMM_STATUS_TIMEOUT,
 // drains the copies and MMAs it issued, frees TMEM and returns.
+#include <cmath>
+
 #include "fp4.cuh"
 
 namespace mgemm {
@@ -743,29 +745,52 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
                     PAIR ? "mgemm_fwd_fp4 launch (CTA pairs)" : "mgemm_fwd_fp4 launch", ta, tb, tsa, tsb, to, p);
 }
 
+// The tiles of h rows that a group of about `rows` rows takes on average (its size anywhere within an eighth of that).
+double tiles_of(double rows, int h) {
+  auto sum = [h](double v) {  // the integral of ceil(n / h) up to v
+    const double k = floor(v / h);
+    return h * k * (k + 1) / 2 + (v - k * h) * (k + 1);
+  };
+  const double lo = 0.875 * rows, hi = 1.125 * rows;
+  return (sum(hi) - sum(lo)) / (hi - lo);
+}
+
 template <int FMT>
 int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, const Fp4Params &p, int64_t M,
                int sms, cudaStream_t s) {
   const int64_t groups = M < p.E ? M : p.E;
-  // pairs where the groups hold 256 rows on average
-  if (M >= 256 * groups)
-    return p.N > 128 ? launch_fp4<FMT, true, 2>(x, sx, w, sw, p, M, 256, sms, s)
-                     : launch_fp4<FMT, true, 1>(x, sx, w, sw, p, M, 128, sms, s);
-  // columns per tile: the fewest rounds of tiles over the SMs, weighted by the bytes of a stage
-  // (A's rows, the columns and their scales); wider at equal cost (fewer reads of A)
-  // (row tiles: half a tile of each group is its ragged end, but no group has less than one.  1024 rows in 8
-  // groups of about 128 are 12 tiles, not 8: 256 columns, 29.7 us; at 8 it would be 192 and 31.8.)
-  const int64_t ragged = (M + 127) / 128 + groups / 2, m_est = ragged > groups ? ragged : groups;
+  const double rows = (double)M / groups;
+  auto rounds = [&](double row_tiles, int bn, int places) {
+    return ceil(groups * row_tiles * ((p.N + bn - 1) / bn) / places);
+  };
+  // Columns per tile: the fewest rounds of tiles over the SMs, weighted by the bytes of a stage (A's rows, the
+  // columns and their scales); wider at equal cost (fewer reads of A).  1024 rows in 8 groups of about 128 are 12
+  // row tiles, not 8: 256 columns, 29.7 us; at 8 it would be 192 and 31.8.
   const int a_rows = M < 128 ? (int)M : 128;
   int bn = 256;
-  int64_t best = -1;
+  double best = -1;
   for (int c : {256, 192, 128, 64}) {
-    const int64_t cost = (m_est * ((p.N + c - 1) / c) + sms - 1) / sms * (F4Cfg<FMT, false>::stage_bytes(a_rows, c) + 2048);
+    const double cost = rounds(tiles_of(rows, 128), c, sms) * (F4Cfg<FMT, false>::stage_bytes(a_rows, c) + 2048);
     if (best < 0 || cost < best) {
       best = cost;
       bn = c;
     }
   }
+  // Pairs from 512 rows a group on (16 groups of 1000, 1408 x 2048: 30.6 us, 32.5 not), and from 128 on where fewer
+  // bytes pass through shared memory with them, in with the copies and out to the MMAs, 2^18 more counted for their
+  // start and end.  Groups of 144, 192 and 256 rows, 8 of 6400 x 4096: 30.6, 31.4 and 37.4 us in
+  // pairs, 35.8, 36.4 and 44.0 not; 5 of 1000 x 8192: 17.4, 17.9 and 18.4 in pairs, 15.7, 16.0 and 16.2 not.
+  bool pairs = rows >= 512;
+  if (!pairs && rows >= 128) {
+    const double kb2 = (p.K + 255) / 256 * 2;
+    const int pair_bn = p.N > 128 ? 256 : 128;
+    const double one = rounds(tiles_of(rows, 128), bn, sms) * F4Cfg<FMT, false>::stage_bytes(128, bn);
+    const double two = rounds(tiles_of(rows, 256), pair_bn, sms / 2) * F4Cfg<FMT, true>::stage_bytes(128, pair_bn);
+    pairs = kb2 * two + (1 << 18) < kb2 * one;
+  }
+  if (pairs)
+    return p.N > 128 ? launch_fp4<FMT, true, 2>(x, sx, w, sw, p, M, 256, sms, s)
+                     : launch_fp4<FMT, true, 1>(x, sx, w, sw, p, M, 128, sms, s);
   return bn > 128 ? launch_fp4<FMT, false, 2>(x, sx, w, sw, p, M, bn, sms, s)
                   : launch_fp4<FMT, false, 1>(x, sx, w, sw, p, M, bn, sms, s);
 }
