@@ -776,12 +776,11 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
       bn = c;
     }
   }
-  // Pairs from 512 rows a group on (16 groups of 1000, 1408 x 2048: 30.6 us, 32.5 not), and from 128 on where fewer
-  // bytes pass through shared memory with them, in with the copies and out to the MMAs, 2^18 more counted for their
-  // start and end.  Groups of 144, 192 and 256 rows, 8 of 6400 x 4096: 30.6, 31.4 and 37.4 us in
-  // pairs, 35.8, 36.4 and 44.0 not; 5 of 1000 x 8192: 17.4, 17.9 and 18.4 in pairs, 15.7, 16.0 and 16.2 not.
-  bool pairs = rows >= 512;
-  if (!pairs && rows >= 128) {
+  // Pairs where fewer bytes pass through shared memory with them, in with the copies and out to the MMAs, 2^18 more
+  // counted for their start and end.  Groups of 144, 192 and 256 rows, 8 of 6400 x 4096: 30.6, 31.4 and 37.4 us in
+  // pairs, 35.8, 36.4 and 44.5 not; 5 of 1000 x 8192: 17.4, 17.9 and 18.4 in pairs, 15.7, 16.0 and 16.2 not.
+  bool pairs = false;
+  if (rows >= 128) {
     const double kb2 = (p.K + 255) / 256 * 2;
     const int pair_bn = p.N > 128 ? 256 : 128;
     const double one = rounds(tiles_of(rows, 128), bn, sms) * F4Cfg<FMT, false>::stage_bytes(128, bn);
