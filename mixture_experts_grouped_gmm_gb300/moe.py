@@ -44,6 +44,7 @@ CUDA library, and nothing waits on the host.
 """
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 from .fp4 import Fp4Tensor
@@ -150,6 +151,7 @@ class Router(torch.autograd.Function):
         return w, ids
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_weights, _grad_ids):
         logits, w, ids = ctx.saved_tensors
         return (route_experts_backward(grad_weights, logits, w, ids, *ctx.how),) + (None,) * 8

@@ -177,6 +177,16 @@ def test_router_autograd_and_other_stream():
     assert torch.equal(w, w2) and torch.equal(ids, ids2) and torch.equal(a.grad, b.grad)
 
 
+def test_router_refuses_a_second_derivative_and_takes_a_broadcast_gradient():
+    l = torch.randn(9, 16, device=DEV).requires_grad_(True)
+    w, ids = moe().Router.apply(l, 4, "sigmoid", None, 1, 1, 1, False)
+    (d,) = torch.autograd.grad(w.sum(), l, create_graph=True)  # (the gradient of a sum has strides of 0)
+    ref = router.route_grad(np.ones((9, 4)), l.detach().double().cpu().numpy(), ids.cpu().numpy(), "sigmoid", False)
+    assert np.abs(d.detach().double().cpu().numpy() - ref).max() <= 2.0 ** -17
+    with pytest.raises(RuntimeError):
+        d.sum().backward()
+
+
 def test_no_tokens_and_repeatable():
     w, ids = moe().route_experts(torch.empty(0, 16, device=DEV), 4)
     assert w.shape == (0, 4) and ids.shape == (0, 4)
