@@ -16,15 +16,18 @@
 // them there (tcgen05.cp, 512 bytes per 128 rows and word) ahead of the
 // stage's four MMAs.
 //
-// CTA (persistent, one per SM, 352 threads):
+// CTA (persistent, one per SM, 384 threads; warps 4-11 take registers from the
+// others, without which the accumulator's 128 columns spill):
 //   warp 0     TMA producer: a ring of stages, as many as fit
 //   warp 1     TMEM owner; issues the MMAs
-//   warp 10    copies a stage's scales to tensor memory ahead of its MMAs (98304
+//   warp 2     copies a stage's scales to tensor memory ahead of its MMAs (98304
 //              x 1408 x 2048 takes 137 us with one warp for copies and MMAs, 126
 //              with two)
-//   warps 2-9  epilogue, two per TMEM lane quarter, each half of the columns:
-//              the accumulator is read, scaled and rounded into registers,
-//              handed back, and then stored, 32 columns at a time, through a
+//   warps 4-11 epilogue, two per TMEM lane quarter, each half of the columns:
+//              the accumulator is read into registers and handed back, the next
+//              tile's factors are fetched (16384 x 2048 x 256, NVFP4: 23.2 us,
+//              27.8 with each tile's own fetched before its wait), and the
+//              columns are scaled, rounded and stored, 32 at a time, through a
 //              swizzled 2 KB buffer and TMA (stores of 32 rows from registers
 //              hold up the load-store unit for some 3000 clocks a tile, and
 //              with it every barrier of the pipeline); rows of a group's edge
@@ -72,8 +75,9 @@ struct Fp4Params {
   int64_t M;
 };
 
-constexpr int kF4Threads = 352;
+constexpr int kF4Threads = 384;
 constexpr int kF4EpiWarps = 8;
+constexpr int kF4Regs = 168;  // registers a thread at launch
 constexpr int kF4MaxStages = 20;
 constexpr int kF4MaxSlots = 16;  // slots of scales in tensor memory
 constexpr int kF4Groups = 128;  // active groups whose places are kept in shared memory
@@ -84,6 +88,10 @@ template <int FMT, bool kPair>
 struct F4Cfg {
   static constexpr bool NV = FMT == MGEMM_NVFP4, PAIR = kPair;
   static constexpr int WPS = 256 / Fp4<FMT>::WORD;  // scale words of a row per stage: 4 or 2
+  // Registers a thread after the launch, of the first four warps and of the epilogue's (where nothing spills). Were
+  // they more than the launch's, the epilogue would wait for registers that nobody gives up.
+  static constexpr int FEW_REGS = NV && PAIR ? 88 : 104, EPI_REGS = NV && PAIR ? 208 : 200;
+  static_assert(128 * FEW_REGS + 32 * kF4EpiWarps * EPI_REGS <= kF4Threads * kF4Regs, "registers");
   // a CTA's codes and scales; nt = scale tiles (128 columns) of the B tile
   static int stage_bytes(int a_rows, int bn) {
     const int nt = (bn + 127) / 128;
@@ -238,6 +246,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2_u64(uint64_t v) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
   return *reinterpret_cast<const uint32_t *>(&h);
 }
+template <int N>
+__device__ __forceinline__ void reg_alloc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dealloc() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // 1 / s of a power of two s
 __device__ __forceinline__ float f4_recip(float s) { return __uint_as_float(0x7F000000u - __float_as_uint(s)); }
 
@@ -352,231 +368,255 @@ __global__ void __launch_bounds__(kF4Threads, 1)
     pdl_trigger();
   }
 
-  if (warp == 0) {
-    bool ok = true;
-    const uint32_t tx = (PAIR ? 2u : 1u) * (uint32_t)p.stage_bytes;
-    const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert's weights
-    // body(step, stage, phase, kb, expert, columns, rows and their scale tiles), for every stage until it returns false
-    auto for_stages = [&](auto &&body) {
-      int step = 0, stage = 0;
-      uint32_t phase = 0;
-      g = 0;
-      for (int t = t_first; t < total; t += t_step) {
+  if (warp < 4) {
+    reg_dealloc<C::FEW_REGS>();
+    if (warp == 0) {
+      bool ok = true;
+      const uint32_t tx = (PAIR ? 2u : 1u) * (uint32_t)p.stage_bytes;
+      const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert's weights
+      // body(step, stage, phase, kb, expert, columns, rows and their scale tiles), for every stage until it returns false
+      auto for_stages = [&](auto &&body) {
+        int step = 0, stage = 0;
+        uint32_t phase = 0;
+        g = 0;
+        for (int t = t_first; t < total; t += t_step) {
+          const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
+          const int e = uniform(ti.e), n0 = uniform(ti.n0), row0 = uniform(ti.row0), sfa_tile = uniform(ti.sf_tile);
+          const int sfb_tile = e * wtiles + n0 / 128, b_row = n0 + rank * (tile_cols(n0) / 2);
+          for (int kb = 0; kb < kb_count; ++kb) {
+            if (!body(step, stage, phase, kb, e, b_row, sfb_tile, row0, sfa_tile)) return;
+            ++step;
+            if (++stage == nst) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+        }
+      };
+      auto put = [&](bool w, bool x, int stage, int kb, int e, int b_row, int sfb_tile, int row0, int sfa_tile) {
+        if (elect_one()) {
+          uint8_t *a = smem + (size_t)stage * op_bytes, *sf = sSF + (size_t)stage * sf_bytes;
+          if (!PAIR || rank == 0) {
+            if (w) {
+              mbar_arrive_expect_tx(&S.full[stage], tx);
+              tma_load_3d(a + p.a_rows * 128, &tmB, &S.full[stage], kb * 128, b_row, e);
+              tma_load_3d(sf + C::WPS * 512, &tmSB, &S.full[stage], 0, kb * C::WPS, sfb_tile);
+            }
+            if (x) {
+              tma_load_2d(a, &tmA, &S.full[stage], kb * 128, row0);
+              tma_load_3d(sf, &tmSA, &S.full[stage], 0, kb * C::WPS, sfa_tile);
+            }
+          } else {  // complete on the even CTA's barrier
+            const uint32_t bar = cluster_addr(&S.full[stage], 0);
+            tma_load_3d_pair(a + p.a_rows * 128, &tmB, bar, kb * 128, b_row, e);
+            tma_load_3d_pair(sf + C::WPS * 512, &tmSB, bar, 0, kb * C::WPS, sfb_tile);
+            tma_load_2d_pair(a, &tmA, bar, kb * 128, row0);
+            tma_load_3d_pair(sf, &tmSA, bar, 0, kb * C::WPS, sfa_tile);
+          }
+        }
+        __syncwarp();
+        issued += w;
+      };
+      if (early) {
+        // The ring is filled with weights, then, the cast done, with the rows.  The
+        // weights may be read before this grid's wait: it is launched behind the
+        // cast alone, every CTA of which has waited for whatever came before it
+        // when it lets this grid start.
+        for_stages([&](int step, int stage, uint32_t, int kb, auto... at) {
+          if (step >= nst) return false;
+          put(true, false, stage, kb, at...);
+          return true;
+        });
+        pdl_wait();
+        pdl_trigger();
+        for_stages([&](int step, int stage, uint32_t, int kb, auto... at) {
+          if (step >= nst) return false;
+          put(false, true, stage, kb, at...);
+          return true;
+        });
+      }
+      for_stages([&](int step, int stage, uint32_t phase, int kb, auto... at) {
+        if (early && step < nst) return true;
+        ok = mbar_wait_warp(&S.empty[stage], phase ^ 1, vabort);
+        if (ok) put(true, true, stage, kb, at...);
+        return ok;
+      });
+      if (!ok && lane == 0) timeout();
+    } else if (warp == 1) {
+      int stage = 0, acc = 0, slot = 0;
+      uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
+      bool ok = true;
+      // (a pair: the even CTA issues for both)
+      for (int t = t_first; t < total && ok && rank == 0; t += t_step) {
         const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
-        const int e = uniform(ti.e), n0 = uniform(ti.n0), row0 = uniform(ti.row0), sfa_tile = uniform(ti.sf_tile);
-        const int sfb_tile = e * wtiles + n0 / 128, b_row = n0 + rank * (tile_cols(n0) / 2);
+        const int n0 = uniform(ti.n0);
+        const uint32_t idesc = (uint32_t)uniform((int)f4_idesc(PAIR ? 256 : 128, tile_cols(n0), C::NV ? 0u : 1u));
+        // a tile of 64 or 192 columns may start in the middle of a 128-column scale tile
+        const uint32_t sfb_off = (uint32_t)uniform((n0 & 64) ? 2 : 0);
+        const uint32_t d_tmem = (uint32_t)uniform((int)tmem_base + acc * acc_cols);
+        if (!mbar_wait_warp(&S.tempty[acc], acc_phase ^ 1, vabort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
         for (int kb = 0; kb < kb_count; ++kb) {
-          if (!body(step, stage, phase, kb, e, b_row, sfb_tile, row0, sfa_tile)) return;
-          ++step;
+          const uint32_t a = (uint32_t)uniform((int)op0 + stage * op_bytes);
+          const uint32_t sfa_t = (uint32_t)uniform((int)tmem_base + sf_col0 + slot * kSlotCols), sfb_t = sfa_t + 4 * C::WPS;
+          const bool here = mbar_wait(&S.full[stage], phase, vabort) && mbar_wait(&S.sf_ready[slot], slot_phase, vabort);
+          if (!__all_sync(0xffffffffu, here)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t ad = smem_desc_sw128(a, 16, 1024), bd = smem_desc_sw128(a + p.a_rows * 128, 16, 1024);
+            auto step = [&](int k) {  // (descriptors advance by bytes >> 4)
+              const int j = C::NV ? k : k / 2;
+              const uint32_t id = C::NV ? 0u : (uint32_t)(k & 1) * 2u;
+              mma_f4<FMT, PAIR>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), sfa_t + 4 * j,
+                                sfb_t + 4 * j * NT + sfb_off, (kb | k) != 0);
+            };
+            if (kb * 256 + 256 <= p.K) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) step(k);
+            } else {  // the contraction ends inside this stage
+              const int steps = (p.K - kb * 256 + 63) / 64;
+              for (int k = 0; k < steps; ++k) step(k);
+            }
+            if constexpr (PAIR) mma_commit_pair(&S.empty[stage], 0x3);
+            else mma_commit(&S.empty[stage]);
+          }
+          __syncwarp();
+          if (++slot == slots) {
+            slot = 0;
+            slot_phase ^= 1;
+          }
+          if (++stage == nst) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          if constexpr (PAIR) mma_commit_pair(&S.tfull[acc], 0x3);
+          else mma_commit(&S.tfull[acc]);
+        }
+        __syncwarp();
+        if (++acc == nacc) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      if (!ok && lane == 0) timeout();
+      if (rank == 0 && elect_one()) {
+        if constexpr (PAIR) mma_commit_pair(&S.drain, 0x1);
+        else mma_commit(&S.drain);
+        mbar_wait_drain(&S.drain, 0);
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      int stage = 0, slot = 0, old = 0, it = 0;  // old: the stage of `slots` iterations ago
+      uint32_t phase = 0, old_phase = 0;
+      bool ok = true;
+      for (int t = t_first; t < total && ok && rank == 0; t += t_step) {
+        for (int kb = 0; kb < kb_count; ++kb) {
+          const uint32_t sf = (uint32_t)uniform((int)sf0 + stage * sf_bytes);
+          const uint32_t sfa_t = (uint32_t)uniform((int)tmem_base + sf_col0 + slot * kSlotCols), sfb_t = sfa_t + 4 * C::WPS;
+          bool here = mbar_wait(&S.full[stage], phase, vabort);
+          // the slot's last readers have completed (a ring of no more stages than slots says so by itself)
+          const bool reuse = it >= slots && nst > slots;
+          if (reuse) here = here && mbar_wait(&S.empty[old], old_phase, vabort);
+          if (!__all_sync(0xffffffffu, here)) {
+            ok = false;
+            break;
+          }
+          if (reuse && ++old == nst) {
+            old = 0;
+            old_phase ^= 1;
+          }
+          it += it < slots;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t sd = smem_desc_rows16(sf);
+            auto copy = [&](int j) {
+              copy_scale_tile<PAIR>(sfa_t + 4 * j, sd + 32 * j);
+              copy_scale_tile<PAIR>(sfb_t + 4 * j * NT, sd + 32 * (C::WPS + j));
+              if (NT == 2) copy_scale_tile<PAIR>(sfb_t + 4 * j * NT + 4, sd + 32 * (2 * C::WPS + j));
+            };
+            if (kb * 256 + 256 <= p.K) {
+#pragma unroll
+              for (int j = 0; j < C::WPS; ++j) copy(j);
+            } else {  // the words of the last steps
+              const int steps = (p.K - kb * 256 + 63) / 64, words = C::NV ? steps : (steps + 1) / 2;
+              for (int j = 0; j < words; ++j) copy(j);
+            }
+            if constexpr (PAIR) mma_commit_pair(&S.sf_ready[slot], 0x1);
+            else mma_commit(&S.sf_ready[slot]);
+          }
+          __syncwarp();
+          if (++slot == slots) slot = 0;
           if (++stage == nst) {
             stage = 0;
             phase ^= 1;
           }
         }
       }
-    };
-    auto put = [&](bool w, bool x, int stage, int kb, int e, int b_row, int sfb_tile, int row0, int sfa_tile) {
-      if (elect_one()) {
-        uint8_t *a = smem + (size_t)stage * op_bytes, *sf = sSF + (size_t)stage * sf_bytes;
-        if (!PAIR || rank == 0) {
-          if (w) {
-            mbar_arrive_expect_tx(&S.full[stage], tx);
-            tma_load_3d(a + p.a_rows * 128, &tmB, &S.full[stage], kb * 128, b_row, e);
-            tma_load_3d(sf + C::WPS * 512, &tmSB, &S.full[stage], 0, kb * C::WPS, sfb_tile);
-          }
-          if (x) {
-            tma_load_2d(a, &tmA, &S.full[stage], kb * 128, row0);
-            tma_load_3d(sf, &tmSA, &S.full[stage], 0, kb * C::WPS, sfa_tile);
-          }
-        } else {  // complete on the even CTA's barrier
-          const uint32_t bar = cluster_addr(&S.full[stage], 0);
-          tma_load_3d_pair(a + p.a_rows * 128, &tmB, bar, kb * 128, b_row, e);
-          tma_load_3d_pair(sf + C::WPS * 512, &tmSB, bar, 0, kb * C::WPS, sfb_tile);
-          tma_load_2d_pair(a, &tmA, bar, kb * 128, row0);
-          tma_load_3d_pair(sf, &tmSA, bar, 0, kb * C::WPS, sfa_tile);
-        }
+      if (!ok && lane == 0) timeout();
+      if (rank == 0 && elect_one()) {  // every copy has landed before tensor memory is freed
+        if constexpr (PAIR) mma_commit_pair(&S.sf_drain, 0x1);
+        else mma_commit(&S.sf_drain);
+        mbar_wait_drain(&S.sf_drain, 0);
       }
       __syncwarp();
-      issued += w;
-    };
-    if (early) {
-      // The ring is filled with weights, then, the cast done, with the rows.  The
-      // weights may be read before this grid's wait: it is launched behind the
-      // cast alone, every CTA of which has waited for whatever came before it
-      // when it lets this grid start.
-      for_stages([&](int step, int stage, uint32_t, int kb, auto... at) {
-        if (step >= nst) return false;
-        put(true, false, stage, kb, at...);
-        return true;
-      });
-      pdl_wait();
-      pdl_trigger();
-      for_stages([&](int step, int stage, uint32_t, int kb, auto... at) {
-        if (step >= nst) return false;
-        put(false, true, stage, kb, at...);
-        return true;
-      });
     }
-    for_stages([&](int step, int stage, uint32_t phase, int kb, auto... at) {
-      if (early && step < nst) return true;
-      ok = mbar_wait_warp(&S.empty[stage], phase ^ 1, vabort);
-      if (ok) put(true, true, stage, kb, at...);
-      return ok;
-    });
-    if (!ok && lane == 0) timeout();
-  } else if (warp == 1) {
-    int stage = 0, acc = 0, slot = 0;
-    uint32_t phase = 0, acc_phase = 0, slot_phase = 0;
-    bool ok = true;
-    // (a pair: the even CTA issues for both)
-    for (int t = t_first; t < total && ok && rank == 0; t += t_step) {
-      const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
-      const int n0 = uniform(ti.n0);
-      const uint32_t idesc = (uint32_t)uniform((int)f4_idesc(PAIR ? 256 : 128, tile_cols(n0), C::NV ? 0u : 1u));
-      // a tile of 64 or 192 columns may start in the middle of a 128-column scale tile
-      const uint32_t sfb_off = (uint32_t)uniform((n0 & 64) ? 2 : 0);
-      const uint32_t d_tmem = (uint32_t)uniform((int)tmem_base + acc * acc_cols);
-      if (!mbar_wait_warp(&S.tempty[acc], acc_phase ^ 1, vabort)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      for (int kb = 0; kb < kb_count; ++kb) {
-        const uint32_t a = (uint32_t)uniform((int)op0 + stage * op_bytes);
-        const uint32_t sfa_t = (uint32_t)uniform((int)tmem_base + sf_col0 + slot * kSlotCols), sfb_t = sfa_t + 4 * C::WPS;
-        const bool here = mbar_wait(&S.full[stage], phase, vabort) && mbar_wait(&S.sf_ready[slot], slot_phase, vabort);
-        if (!__all_sync(0xffffffffu, here)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t ad = smem_desc_sw128(a, 16, 1024), bd = smem_desc_sw128(a + p.a_rows * 128, 16, 1024);
-          auto step = [&](int k) {  // (descriptors advance by bytes >> 4)
-            const int j = C::NV ? k : k / 2;
-            const uint32_t id = C::NV ? 0u : (uint32_t)(k & 1) * 2u;
-            mma_f4<FMT, PAIR>(d_tmem, ad + 2 * k, bd + 2 * k, idesc | (id << 4) | (id << 29), sfa_t + 4 * j,
-                              sfb_t + 4 * j * NT + sfb_off, (kb | k) != 0);
-          };
-          if (kb * 256 + 256 <= p.K) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) step(k);
-          } else {  // the contraction ends inside this stage
-            const int steps = (p.K - kb * 256 + 63) / 64;
-            for (int k = 0; k < steps; ++k) step(k);
-          }
-          if constexpr (PAIR) mma_commit_pair(&S.empty[stage], 0x3);
-          else mma_commit(&S.empty[stage]);
-        }
-        __syncwarp();
-        if (++slot == slots) {
-          slot = 0;
-          slot_phase ^= 1;
-        }
-        if (++stage == nst) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-      if (!ok) break;
-      if (elect_one()) {
-        if constexpr (PAIR) mma_commit_pair(&S.tfull[acc], 0x3);
-        else mma_commit(&S.tfull[acc]);
-      }
-      __syncwarp();
-      if (++acc == nacc) {
-        acc = 0;
-        acc_phase ^= 1;
-      }
-    }
-    if (!ok && lane == 0) timeout();
-    if (rank == 0 && elect_one()) {
-      if constexpr (PAIR) mma_commit_pair(&S.drain, 0x1);
-      else mma_commit(&S.drain);
-      mbar_wait_drain(&S.drain, 0);
-    }
-    __syncwarp();
-  } else if (warp == 2 + kF4EpiWarps) {
-    int stage = 0, slot = 0, old = 0, it = 0;  // old: the stage of `slots` iterations ago
-    uint32_t phase = 0, old_phase = 0;
-    bool ok = true;
-    for (int t = t_first; t < total && ok && rank == 0; t += t_step) {
-      for (int kb = 0; kb < kb_count; ++kb) {
-        const uint32_t sf = (uint32_t)uniform((int)sf0 + stage * sf_bytes);
-        const uint32_t sfa_t = (uint32_t)uniform((int)tmem_base + sf_col0 + slot * kSlotCols), sfb_t = sfa_t + 4 * C::WPS;
-        bool here = mbar_wait(&S.full[stage], phase, vabort);
-        // the slot's last readers have completed (a ring of no more stages than slots says so by itself)
-        const bool reuse = it >= slots && nst > slots;
-        if (reuse) here = here && mbar_wait(&S.empty[old], old_phase, vabort);
-        if (!__all_sync(0xffffffffu, here)) {
-          ok = false;
-          break;
-        }
-        if (reuse && ++old == nst) {
-          old = 0;
-          old_phase ^= 1;
-        }
-        it += it < slots;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t sd = smem_desc_rows16(sf);
-          auto copy = [&](int j) {
-            copy_scale_tile<PAIR>(sfa_t + 4 * j, sd + 32 * j);
-            copy_scale_tile<PAIR>(sfb_t + 4 * j * NT, sd + 32 * (C::WPS + j));
-            if (NT == 2) copy_scale_tile<PAIR>(sfb_t + 4 * j * NT + 4, sd + 32 * (2 * C::WPS + j));
-          };
-          if (kb * 256 + 256 <= p.K) {
-#pragma unroll
-            for (int j = 0; j < C::WPS; ++j) copy(j);
-          } else {  // the words of the last steps
-            const int steps = (p.K - kb * 256 + 63) / 64, words = C::NV ? steps : (steps + 1) / 2;
-            for (int j = 0; j < words; ++j) copy(j);
-          }
-          if constexpr (PAIR) mma_commit_pair(&S.sf_ready[slot], 0x1);
-          else mma_commit(&S.sf_ready[slot]);
-        }
-        __syncwarp();
-        if (++slot == slots) slot = 0;
-        if (++stage == nst) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-    }
-    if (!ok && lane == 0) timeout();
-    if (rank == 0 && elect_one()) {  // every copy has landed before tensor memory is freed
-      if constexpr (PAIR) mma_commit_pair(&S.sf_drain, 0x1);
-      else mma_commit(&S.sf_drain);
-      mbar_wait_drain(&S.sf_drain, 0);
-    }
-    __syncwarp();
   } else {
-    const int ew = warp - 2, q = warp & 3, h = ew >> 2;
-    const int r = q * 32 + lane;   // the thread's row of the tile
-    const int half = bn / 2;       // columns per warp: 32, 64, 96 or 128
+    reg_alloc<C::EPI_REGS>();
+    const int ew = warp - 4, q = warp & 3, h = ew >> 2;
+    const int r = q * 32 + lane;  // the thread's row of the tile
+    const int half = bn / 2;      // columns per warp: 32, 64, 96 or 128
     float *cinv = S.cinv[ew];
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = t_first; t < total; t += t_step) {
-      const F4Tile ti = f4_tile<PAIR>(t, g, p, S, av, na, rank);
-      const int col0 = ti.n0 + h * half;
-      bool row_ok = r < ti.rows;
-      int64_t dst = (int64_t)ti.row0 + r;
-      float f = 1.f;  // the row's factor
+    // A tile's factors are fetched while the one before it is scaled and stored.
+    F4Tile ti{};
+    bool row_ok = false;
+    int64_t dst = 0;
+    float weight = 1.f, rx = 1.f, rw[4] = {};
+    auto fetch = [&]() {
+      row_ok = r < ti.rows;
+      dst = (int64_t)ti.row0 + r;
+      if (C::NV && row_ok) rx = __ldg(p.rx + dst);
       if (p.row_map) {
         const int32_t d = row_ok ? __ldg(p.row_map + dst) : -1;
         row_ok = d >= 0 && d < p.map_limit;
-        if (row_ok && p.row_weight) f = __ldg(p.row_weight + d);
-        if (C::NV && row_ok) f *= f4_recip(__ldg(p.rx + dst));
+        if (row_ok && p.row_weight) weight = __ldg(p.row_weight + d);
         dst = row_ok ? d : 0;
-      } else if (C::NV && row_ok) {
-        f = f4_recip(__ldg(p.rx + dst));
       }
       if (C::NV) {
-        for (int c = lane; c < half; c += 32)
-          cinv[c] = col0 + c < p.N ? f4_recip(__ldg(p.rw + (int64_t)ti.e * p.N + col0 + c)) : 0.f;
+        const int n = ti.n0 + h * half + lane;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c * 32 < half) rw[c] = n + c * 32 < p.N ? __ldg(p.rw + (int64_t)ti.e * p.N + n + c * 32) : 1.f;
+      }
+    };
+    if (t_first < total) {
+      ti = f4_tile<PAIR>(t_first, g, p, S, av, na, rank);
+      fetch();
+    }
+    for (int t = t_first; t < total; t += t_step) {
+      if (C::NV) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c * 32 < half) cinv[c * 32 + lane] = f4_recip(rw[c]);
         __syncwarp();
       }
+      // the row's factor, its place and the tile's
+      const float f = C::NV ? weight * f4_recip(rx) : weight;
+      const int col0 = ti.n0 + h * half, row0 = ti.row0 + q * 32;
+      const bool store = row_ok, whole = !p.row_map && q * 32 + 32 <= ti.rows;  // the warp's 32 rows are all the group's
+      __nv_bfloat16 *o = p.out + dst * p.N + col0;
+      // (the next tile's place before the wait, or, where its factors follow, after the accumulator's read)
+      if (!C::NV && t + t_step < total) ti = f4_tile<PAIR>(t + t_step, g, p, S, av, na, rank);
       if (!mbar_wait_warp(&S.tfull[acc], acc_phase, vabort)) {
         if (lane == 0) timeout();
         break;
@@ -599,10 +639,12 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         acc = 0;
         acc_phase ^= 1;
       }
+      if (t + t_step < total) {
+        if (C::NV) ti = f4_tile<PAIR>(t + t_step, g, p, S, av, na, rank);
+        fetch();
+      }
       const uint64_t f2 = f32x2(f, f);
-      const bool whole = !p.row_map && q * 32 + 32 <= ti.rows;  // the warp's 32 rows are all the group's
       uint8_t *buf = sOut + ew * kF4Stage;
-      __nv_bfloat16 *o = p.out + dst * p.N + col0;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if (c * 32 >= half || col0 + c * 32 >= p.N) break;
@@ -634,10 +676,10 @@ __global__ void __launch_bounds__(kF4Threads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_2d(&tmOut, buf, col0 + c * 32, ti.row0 + q * 32);
+            tma_store_2d(&tmOut, buf, col0 + c * 32, row0);
             bulk_commit();
           }
-        } else if (row_ok) {
+        } else if (store) {
           if (p.vec32) {  // whole 32-byte sectors (N % 16 == 0)
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -735,6 +777,10 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
                                       (int)kF4Limit),
                  "cudaFuncSetAttribute");
     if (rc) return rc;
+    cudaFuncAttributes attr;
+    rc = cuda_rc(cudaFuncGetAttributes(&attr, fp4_gemm_kernel<FMT, PAIR, NT>), "cudaFuncGetAttributes");
+    if (rc) return rc;
+    if (attr.numRegs != kF4Regs) return MGEMM_ECUDA;  // see FEW_REGS
     attr_done[dev] = true;
   }
   const int64_t groups = M < E ? M : E;
