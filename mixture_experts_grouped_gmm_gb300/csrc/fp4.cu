@@ -7,8 +7,8 @@
 //          code = e2m1(x R / b)
 //
 // Memory-bound: 2 bytes read and about 0.55 written per element.  A thread
-// takes whole blocks, and 32 threads a row, or 256 where there are few rows
-// (a row of 5120 on one warp alone takes 6 us).  NVFP4 needs the row's maximum
+// takes whole blocks; a row takes 8 to 128 threads by its length, or 256 where
+// there are few rows (a row of 5120 on one warp alone takes 6 us).  NVFP4 needs the row's maximum
 // before its first code, so the thread's blocks stay in registers as they were
 // read (up to NB of them; longer rows are read twice, the second time from
 // cache).  Four threads' scale bytes make a word.
@@ -115,7 +115,7 @@ struct RowCast {
   }
   // codes and scale bytes of the blocks held (R: the row's power of two and its inverse, NVFP4)
   __device__ __forceinline__ void store(int q0, int nblk, int W, float R, float Rinv, int64_t tile_row, uint8_t *codes,
-                                        uint8_t *sf, int tid) const {
+                                        uint8_t *sf, int tid, bool live) const {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int qw = q0 + i * TPR;  // uniform over the row's threads
@@ -136,8 +136,9 @@ struct RowCast {
       uint32_t word = q < nblk ? byte << (8 * (q & 3)) : 0u;  // an empty block past the row
       word |= __shfl_xor_sync(0xffffffffu, word, 1);
       word |= __shfl_xor_sync(0xffffffffu, word, 2);
-      if ((q & 3) == 0 && q < 4 * W) *reinterpret_cast<uint32_t *>(sf + fp4_sf_offset(tile_row, q >> 2, W)) = word;
-      if (q < nblk) {
+      if (live && (q & 3) == 0 && q < 4 * W)
+        *reinterpret_cast<uint32_t *>(sf + fp4_sf_offset(tile_row, q >> 2, W)) = word;
+      if (live && q < nblk) {
         uint32_t out[2 * P];
 #pragma unroll
         for (int k = 0; k < 2 * P; ++k) out[k] = fp4_codes8(&v[i][k / 2][(k & 1) * 4], r2);
@@ -156,8 +157,10 @@ constexpr int kQuantThreads = 256;
 // The largest of a over the TPR threads of a row (every one of them).
 template <int TPR>
 __device__ __forceinline__ float row_max(float a, float *sh) {
-  a = warp_max(a);
-  if (TPR == 32) return a;
+  constexpr int LANES = TPR < 32 ? TPR : 32;
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  if (TPR <= 32) return a;
   // (the rows of a CTA go on by themselves: a barrier each; an even and an odd set of values, so
   // one barrier a row does)
   const int row = threadIdx.x / TPR, w0 = row * (TPR / 32);
@@ -169,10 +172,27 @@ __device__ __forceinline__ float row_max(float a, float *sh) {
   return a;
 }
 
-// place(): the row's place in the scale tiles
+// The group of row i: as many groups end at or before it (each row's threads of a warp ask for it together).
+template <int TPR, typename End>
+__device__ __forceinline__ int row_group(int E, int tid, End &&ended) {
+  constexpr int LANES = TPR < 32 ? TPR : 32;
+  int e = 0;
+  for (int j = tid & (LANES - 1); j < E; j += LANES) e += ended(j);
+  if constexpr (LANES == 32) {
+    return __reduce_add_sync(0xffffffffu, e);
+  } else {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) e += __shfl_xor_sync(0xffffffffu, e, o);
+    return e;
+  }
+}
+
+// place(): the row's place in the scale tiles.  live: false for threads whose row
+// is past the last (rd reads zeros, nothing is stored), which come along where a
+// warp holds several rows.
 template <int FMT, int NB, int TPR, typename Place>
 __device__ __forceinline__ void cast_row(const RowReader &rd, int K, Place &&place, int W, uint8_t *codes, uint8_t *sf,
-                                         float *row_scale, int tid, float *sh) {
+                                         float *row_scale, int tid, float *sh, bool live = true) {
   using F = Fp4<FMT>;
   const int nblk = K / F::BLOCK;
   RowCast<FMT, NB, TPR> c;
@@ -189,13 +209,13 @@ __device__ __forceinline__ void cast_row(const RowReader &rd, int K, Place &&pla
     }
     R = fp4_pow2_scale(kNvfp4RowMax, row_max<TPR>(a, sh));
     Rinv = __frcp_rn(R);  // a power of two
-    if (tid == 0) *row_scale = R;
+    if (live && tid == 0) *row_scale = R;
     if (!once) c.load(rd, 0, nblk, tid, nothing);
   }
-  c.store(0, nblk, W, R, Rinv, tile_row, codes, sf, tid);
+  c.store(0, nblk, W, R, Rinv, tile_row, codes, sf, tid, live);
   for (int q0 = NB * TPR; q0 < 4 * W; q0 += NB * TPR) {
     c.load(rd, q0, nblk, tid, nothing);
-    c.store(q0, nblk, W, R, Rinv, tile_row, codes, sf, tid);
+    c.store(q0, nblk, W, R, Rinv, tile_row, codes, sf, tid, live);
   }
 }
 
@@ -208,20 +228,22 @@ __global__ void __launch_bounds__(kQuantThreads)
   __shared__ float sh[2][kQuantThreads / 32];
   int odd = 0;
   constexpr int kRows = kQuantThreads / TPR;  // rows of a CTA at a time
-  const int lane = threadIdx.x & 31, tid = threadIdx.x % TPR;
+  const int tid = threadIdx.x % TPR;
   const int64_t step = (int64_t)gridDim.x * kRows, first = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+  const int sub = TPR < 32 ? (int)(threadIdx.x & 31) / TPR : 0;  // the row's number among its warp's
   const int W = fp4_words(FMT, K);
   if (!S.args) {
     const int64_t npad = (S.N + 127) / 128 * 128;
-    for (int64_t i = first; i < S.E * npad; i += step) {
+    for (int64_t i = first; i - sub < S.E * npad; i += step) {
       const int64_t e = i / npad, n = i - e * npad;
-      if (n >= S.N) {  // scale rows that fill up the group's last tile
+      const bool live = i < S.E * npad && n < S.N;
+      if (i < S.E * npad && n >= S.N)  // scale rows that fill up the group's last tile
         for (int j = tid; j < W; j += TPR) *reinterpret_cast<uint32_t *>(sf + fp4_sf_offset(i, j, W)) = 0u;
-        continue;
-      }
+      if (TPR >= 32 && !live) continue;
       const int64_t row = e * S.N + n;
-      const RowReader rd{S.in + row * S.ld, nullptr, S.vec32};
-      cast_row<FMT, NB, TPR>(rd, K, [&] { return i; }, W, codes + row * (K / 2), sf, row_scale + row, tid, sh[odd ^= 1]);
+      const RowReader rd{live ? S.in + row * S.ld : nullptr, nullptr, S.vec32};
+      cast_row<FMT, NB, TPR>(
+          rd, K, [&] { return i; }, W, codes + row * (K / 2), sf, row_scale + row, tid, sh[odd ^= 1], live);
     }
     return;
   }
@@ -229,11 +251,11 @@ __global__ void __launch_bounds__(kQuantThreads)
   if (*av.status != 0) return;
   const int64_t total = __ldg(av.offsets + S.E);
   const int64_t rows = total < S.M ? total : S.M;
-  for (int64_t i = first; i < rows; i += step) {
-    auto place = [&] {  // the group of row i: as many groups end at or before it
-      int e = 0;
-      for (int j = lane; j < S.E; j += 32) e += __ldg(av.offsets + j + 1) <= i;
-      e = __reduce_add_sync(0xffffffffu, e);
+  for (int64_t i0 = first; i0 - sub < rows; i0 += step) {
+    const bool live = TPR >= 32 || i0 < rows;
+    const int64_t i = live ? i0 : rows - 1;
+    auto place = [&] {
+      const int e = row_group<TPR>(S.E, tid, [&](int j) { return __ldg(av.offsets + j + 1) <= i; });
       return (int64_t)__ldg(av.poffsets + e) + (i - (int64_t)__ldg(av.offsets + e));
     };
     RowReader rd{nullptr, nullptr, S.vec32};
@@ -244,7 +266,7 @@ __global__ void __launch_bounds__(kQuantThreads)
       rd.row = S.in + i * S.ld;
       if (S.gated) rd.up = rd.row + K;
     }
-    cast_row<FMT, NB, TPR>(rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1]);
+    cast_row<FMT, NB, TPR>(rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1], live);
   }
 }
 
@@ -275,18 +297,19 @@ __global__ void __launch_bounds__(kQuantThreads)
   starts[threadIdx.x] = ((int)tiles - (int)((m + 127) / 128)) * 128;
   __syncthreads();
   constexpr int kRows = kQuantThreads / TPR;
-  const int lane = threadIdx.x & 31, tid = threadIdx.x % TPR;
+  const int tid = threadIdx.x % TPR, sub = TPR < 32 ? (int)(threadIdx.x & 31) / TPR : 0;
   const int W = fp4_words(FMT, K);
+  const int64_t step = (int64_t)(gridDim.x - 1) * kRows;
   int odd = 0;
-  for (int64_t i = (int64_t)(blockIdx.x - 1) * kRows + threadIdx.x / TPR; i < S.M; i += (int64_t)(gridDim.x - 1) * kRows) {
+  for (int64_t i0 = (int64_t)(blockIdx.x - 1) * kRows + threadIdx.x / TPR; i0 - sub < S.M; i0 += step) {
+    const bool live = TPR >= 32 || i0 < S.M;
+    const int64_t i = live ? i0 : S.M - 1;
     auto place = [&] {
-      int e = 0;
-      for (int j = lane; j < S.E; j += 32) e += ends[j] <= (int)i;
-      e = __reduce_add_sync(0xffffffffu, e);
+      const int e = row_group<TPR>(S.E, tid, [&](int j) { return ends[j] <= (int)i; });
       return starts[e] + (i - (e > 0 ? ends[e - 1] : 0));
     };
     const RowReader rd{S.in + i * S.ld, nullptr, S.vec32};
-    cast_row<FMT, NB, TPR>(rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1]);
+    cast_row<FMT, NB, TPR>(rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1], live);
   }
 }
 
@@ -299,12 +322,13 @@ __device__ __forceinline__ uint32_t e2m1x2_to_f16(uint32_t byte) {
   return r;
 }
 
-// A warp per row, 16 elements per lane and step.  SPLIT, where rows are too few to
+// LPR lanes per row (a warp, 8 for rows of at most 512: 52805 x 288 8 us, 13 with a
+// warp), 16 elements per lane and step.  SPLIT, where rows are too few to
 // fill the SMs: gridDim.y warps per row (16 rows of 5120: 1.7 us, 3.6 without; 3003
 // rows of 1440, which do: 3.6 split, 3.3 not).  NVFP4: code times the block's
 // e4m3 scale is exact in f16 (6 significant bits, at most 2688), then times the
 // power of two 1 / R; MXFP4: code times the block's power of two.  Both exact.
-template <int FMT, bool SPLIT>
+template <int FMT, int LPR, bool SPLIT>
 __global__ void __launch_bounds__(256)
     dequant_fp4_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ sf,
                        const float *__restrict__ row_scale, int64_t E, int64_t N, int K, __nv_bfloat16 *__restrict__ out,
@@ -312,18 +336,20 @@ __global__ void __launch_bounds__(256)
   using F = Fp4<FMT>;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t nwarps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  constexpr int kShift = LPR == 32 ? 5 : 3;
+  static_assert(1 << kShift == LPR, "lanes per row");
+  const int lane = threadIdx.x & (LPR - 1);
+  const int64_t step = (int64_t)gridDim.x * (blockDim.x >> kShift);
   const int W = fp4_words(FMT, K), units = K / 16;
   const int64_t npad = (N + 127) / 128 * 128;
-  for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < E * N; i += nwarps) {
+  for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> kShift) + (threadIdx.x >> kShift); i < E * N; i += step) {
     const int64_t e = i / N, tile_row = e * npad + (i - e * N);
     const float inv = F::NV ? __frcp_rn(__ldg(row_scale + i)) : 1.f;
     const uint2 *src = reinterpret_cast<const uint2 *>(codes + i * (K / 2));
     const uint8_t *sfr = sf + fp4_sf_offset(tile_row, 0, W);
     __nv_bfloat16 *dst = out + i * ld;
 #pragma unroll 2
-    for (int c = SPLIT ? blockIdx.y * 32 + lane : lane; c < units; c += SPLIT ? 32 * (int)gridDim.y : 32) {
+    for (int c = SPLIT ? blockIdx.y * LPR + lane : lane; c < units; c += SPLIT ? LPR * (int)gridDim.y : LPR) {
       const int q = F::NV ? c : c >> 1;  // the block
       const uint2 w = __ldg(src + c);
       const uint32_t byte = __ldg(sfr + (int64_t)(q >> 2) * 512 + (q & 3));
@@ -359,18 +385,24 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-int rows_grid(int64_t rows) {
+int rows_grid(int64_t rows, int per_cta) {
   const int sms = sm_count_cached();
   if (sms <= 0) return -1;
-  const int64_t want = (rows + 7) / 8, cap = (int64_t)sms * 16;
+  const int64_t want = (rows + per_cta - 1) / per_cta, cap = (int64_t)sms * 16;
   return (int)(want < cap ? want : cap);
 }
 
 bool a16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 // rows: those of the call (device-known: at most).  Below two CTAs' worth of rows
-// for every SM, a CTA takes a row; else a warp does, or two for NVFP4 rows past
-// 2048 (of which a warp would need twice the registers).
+// for every SM, a CTA takes a row.  Else a row takes the threads that hold its
+// blocks with few of them idle: parts of a warp for short rows, where there are
+// enough for all SMs (52805 rows of 96, 288 and 512, NVFP4: 5.3, 10.7 and 13.9 us,
+// 18 to 21 with a warp each), a warp, or two or four for NVFP4's long rows, whose
+// maximum must be known before the first code (52805 x 2560 on 32 threads of 5
+// blocks: 55 us, 63 on 64 of 3, 72 on 64 of 4; 20000 x 4608 on 64 of 5: 42.5, read
+// twice by 64 of 4: 58.5; wider than needed costs barriers: 51200 x 4096 on 64, 128
+// and 256 threads: 88, 97 and 141).
 template <int FMT>
 int launch_quant(QuantSource S, int64_t rows, int K, uint8_t *codes, uint8_t *sf, float *row_scale, cudaStream_t s,
                  const char *what, const int64_t *sizes = nullptr, uint8_t *args = nullptr) {
@@ -394,11 +426,25 @@ int launch_quant(QuantSource S, int64_t rows, int K, uint8_t *codes, uint8_t *sf
     if (nblk <= 256) MGEMM_QUANT_LAUNCH(1, 256);
     MGEMM_QUANT_LAUNCH(4 / U, 256);
   }
-  if (nblk <= 64 / U) MGEMM_QUANT_LAUNCH(2 / U, 32);
+  const bool many = rows >= (int64_t)sms * 32;
+  if (many && nblk <= 8) MGEMM_QUANT_LAUNCH(1, 8);
+  if (many && nblk <= 16) MGEMM_QUANT_LAUNCH(2, 8);
   if constexpr (Fp4<FMT>::NV) {
-    if (nblk > 128) MGEMM_QUANT_LAUNCH(4, 64);
+    if (many && nblk <= 32) MGEMM_QUANT_LAUNCH(4, 8);
+    if (many && nblk <= 64) MGEMM_QUANT_LAUNCH(4, 16);
+    if (nblk <= 64) MGEMM_QUANT_LAUNCH(2, 32);
+    if (nblk <= 96) MGEMM_QUANT_LAUNCH(3, 32);
+    if (nblk <= 128) MGEMM_QUANT_LAUNCH(4, 32);
+    if (nblk <= 160) MGEMM_QUANT_LAUNCH(5, 32);
+    if (nblk <= 192) MGEMM_QUANT_LAUNCH(3, 64);
+    if (nblk <= 256) MGEMM_QUANT_LAUNCH(4, 64);
+    if (nblk <= 320) MGEMM_QUANT_LAUNCH(5, 64);
+    MGEMM_QUANT_LAUNCH(4, 128);
+  } else {
+    if (many && nblk <= 32) MGEMM_QUANT_LAUNCH(2, 16);
+    if (nblk <= 32) MGEMM_QUANT_LAUNCH(1, 32);
+    MGEMM_QUANT_LAUNCH(2, 32);
   }
-  MGEMM_QUANT_LAUNCH(4 / U, 32);
 #undef MGEMM_QUANT_LAUNCH
 }
 
@@ -450,14 +496,16 @@ extern "C" int mgemm_dequant_fp4(const uint8_t *codes, const uint8_t *sf, const 
   if (E == 0 || N == 0) return MGEMM_OK;
   if (!out || !codes || !sf || (fmt == MGEMM_NVFP4 && !row_scale)) return MGEMM_EINVAL;
   if (!a16(out) || !a16(codes) || !a16(sf) || ((uintptr_t)row_scale & 3)) return MGEMM_EALIGN;
-  const int grid = rows_grid(E * N);
+  const bool brief = K <= 512 && E * N >= (int64_t)sm_count_cached() * 32;  // short rows that fill the SMs take 8 lanes
+  const int grid = rows_grid(E * N, brief ? 32 : 8);
   if (grid < 0) return MGEMM_ECUDA;
   const int steps = (K / 16 + 31) / 32, room = sm_count_cached() * 2 / grid;  // warps a row: two CTAs for each SM
-  const int parts = room < 1 ? 1 : room < steps ? room : steps;
+  const int parts = brief || room < 1 ? 1 : room < steps ? room : steps;
   const bool nv = fmt == MGEMM_NVFP4;
-  auto *kernel = parts > 1 ? nv ? dequant_fp4_kernel<MGEMM_NVFP4, true> : dequant_fp4_kernel<MGEMM_MXFP4, true>
-                 : nv      ? dequant_fp4_kernel<MGEMM_NVFP4, false>
-                           : dequant_fp4_kernel<MGEMM_MXFP4, false>;
+  auto *kernel = brief       ? nv ? dequant_fp4_kernel<MGEMM_NVFP4, 8, false> : dequant_fp4_kernel<MGEMM_MXFP4, 8, false>
+                 : parts > 1 ? nv ? dequant_fp4_kernel<MGEMM_NVFP4, 32, true> : dequant_fp4_kernel<MGEMM_MXFP4, 32, true>
+                 : nv        ? dequant_fp4_kernel<MGEMM_NVFP4, 32, false>
+                             : dequant_fp4_kernel<MGEMM_MXFP4, 32, false>;
   return launch_pdl(kernel, dim3((unsigned)grid, (unsigned)parts), dim3(256), 0, (cudaStream_t)stream, 1,
                     "mgemm_dequant_fp4 launch", codes, sf, row_scale, (int64_t)E, N, K, (__nv_bfloat16 *)out, ld_out,
                     ((uintptr_t)out & 31) == 0 && ld_out % 16 == 0);

@@ -72,6 +72,47 @@ def test_cast_shapes(fmt, shape):
     check_cast(x, fmt)
 
 
+# enough rows for parts of a warp each (short ones), and for one to four warps each (long ones)
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("shape", [(4901, 32), (4901, 96), (3, 1651, 160), (4903, 288), (4901, 512), (2, 2433, 576),
+                                   (4867, 1024), (1301, 1440), (1301, 2560), (1237, 2880), (1301, 4608), (1231, 5120),
+                                   (1229, 8224)])
+def test_casts_of_many_rows(fmt, shape):
+    check_cast(blocky(shape, sum(shape)), fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("K", [96, 288, 512, 992])
+def test_many_token_rows_are_cast_as_weights_are(fmt, K):
+    sizes = [3001, 0, 1, 2500, 7]
+    M, E, code = sum(sizes), len(sizes), {"mxfp4": 2, "nvfp4": 3}[fmt]
+    x = blocky((M, K), K, -3, 3)
+    want = mg().quantize_fp4(x, fmt)
+    args = new_args(E, DEV)
+    B().mgemm_fill_args(torch.tensor(sizes, dtype=torch.int64, device=DEV), E, M, args)
+    ids = torch.randperm(M, generator=torch.Generator().manual_seed(1)).to(DEV)
+    inv = torch.empty_like(ids)
+    inv[ids] = torch.arange(M, device=DEV)
+    shuffled = x[inv]  # row i of x is row ids[i] of it
+    for src, kw in ((x, {}), (shuffled, dict(sorted_ids=ids.to(torch.int32), numel=M, top_k=1))):
+        c = torch.zeros(M, K // 2, dtype=torch.uint8, device=DEV)
+        sf = torch.zeros(B().mgemm_fp4_scale_bytes(code, B().mgemm_colwise_ld(M, E), K), dtype=torch.uint8, device=DEV)
+        rs = torch.zeros(M, device=DEV)
+        B().mgemm_quant_fp4_rows(args, E, M, src, K, code, c, sf, rs, **kw)
+        assert torch.equal(c, want.codes.view(M, K // 2))
+        if fmt == "nvfp4":
+            assert torch.equal(rs, want.row_scale.view(M))
+        o = r = 0
+        for m in sizes:  # a group's scales, in tiles of their own
+            n = B().mgemm_fp4_scale_bytes(code, m, K)
+            if m:
+                ref = mg().quantize_fp4(x[r:r + m].contiguous(), fmt).scales
+                a, b = sf[o:o + n].view(-1, 32, 4, 4), ref.view(-1, 32, 4, 4)
+                a, b = (t.view(-(-m // 128), -1, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(-(-m // 128) * 128, -1)[:m] for t in (a, b))
+                assert torch.equal(a, b)
+            o, r = o + n, r + m
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_cast_ties_extremes_and_strides(fmt):
     # every positive bf16 of two binades against several block maxima: all ties of the grid among them
