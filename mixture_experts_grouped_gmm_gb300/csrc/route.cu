@@ -13,13 +13,13 @@
 //
 // Bound by instruction issue, not by memory (54 us for 65536 x 256 with groups and
 // bias, 10 of them the bytes'): an expert costs 4 bytes and some 35 instructions of
-// a lane (score, key, the lane's best), a choice some 20 of the warp.  So a lane keeps its three best experts in order: a choice takes the
-// maximum over the lanes' best and moves that lane's list up, and only a lane
-// chosen from a fourth time looks its experts over again.  Where groups are whole
-// lanes (NV divides the group, a power of two of lanes) their two best come from
-// the same lists by shuffles; otherwise the groups are scanned in turn.  (Half a
-// warp per token measured slower: the lanes' longer lists cost what the shared
-// choices save.)
+// a lane (score, key, the lane's best), a choice some 20 of the warp.  So a lane
+// keeps its three best experts in order: a choice takes the maximum over the lanes'
+// best and moves that lane's list up, and only a lane chosen from a fourth time
+// looks its experts over again.  Groups of experts take lanes of their own, so their
+// two best come from the same lists by shuffles; only where lanes are too few are
+// the groups scanned in turn.  (At 256 experts half a warp per token measured
+// slower: the lanes' longer lists cost what the shared choices save.)
 #include "common.cuh"
 
 namespace mgemm {
@@ -97,7 +97,8 @@ struct RouteParams {
   int E, top_k, sigmoid, n_group, topk_group, group_top, renormalize;
   float scale;
   int vec, vec_bias;     // rows of logits / the bias start on 16-byte boundaries
-  int lanes_per_group;   // whole-lane groups: a power of two
+  int lanes_per_group;   // groups of whole lanes: a power of two
+  int group_size;        // where a group does not fill its lanes, else 0
 };
 
 // The float of an order key of a number.
@@ -152,14 +153,14 @@ __device__ __forceinline__ void load_values(const __nv_bfloat16 *p, bool vec, fl
     for (int i = 0; i < N; ++i) v[i] = __bfloat162float(p[i]);
   }
 }
-// The lane's N values of a row of E, `fill` past its end.
+// Values e0 .. e1 - 1 of a row, `fill` in what remains of N.
 template <int N, typename L>
-__device__ __forceinline__ void load_lane(const L *row, int e0, int E, bool vec, float fill, float (&v)[N]) {
-  if (e0 + N <= E) {
+__device__ __forceinline__ void load_lane(const L *row, int e0, int e1, bool vec, float fill, float (&v)[N]) {
+  if (e0 + N <= e1) {
     load_values<N>(row + e0, vec, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = e0 + j < E ? load_logit(row + e0 + j) : fill;
+    for (int j = 0; j < N; ++j) v[j] = e0 + j < e1 ? load_logit(row + e0 + j) : fill;
   }
 }
 
@@ -185,7 +186,7 @@ __device__ __forceinline__ Best three_best(const uint32_t (&key)[N]) {
   return b;
 }
 
-// GROUPS: 0 none; 1 groups of p.lanes_per_group whole lanes; 2 any groups.
+// GROUPS: 0 none; 1 a group takes p.lanes_per_group lanes to itself; 2 any groups.
 // SW lanes per token: half a warp for many tokens of at most 64 experts, 8 picks and
 // no groups (a step then serves two tokens: 131072 x 64, 6 picks, 29.7 us, 36.4 with
 // whole warps, and 16384 of them 5.3 and 5.6; but a maximum takes longer: 4096 x 32,
@@ -202,17 +203,23 @@ __global__ void __launch_bounds__(kRouteThreads)
   if (t0 - (threadIdx.x & 31) / SW >= p.T) return;  // whole warps leave together
   const bool live = SW == 32 || t0 < p.T;
   const int64_t t = live ? t0 : p.T - 1;
-  const int e0 = lane * NV;
+  // the lane's experts: e0 .. e1 - 1, at most NV (a group's last lanes may hold fewer, or none)
+  int e0 = lane * NV, e1 = min(e0 + NV, p.E);
+  if (GROUPS == 1 && p.group_size) {
+    const int first = (lane & (p.lanes_per_group - 1)) * NV, g0 = lane / p.lanes_per_group * p.group_size;
+    e0 = min(g0 + min(first, p.group_size), p.E);
+    e1 = min(min(e0 + NV, g0 + p.group_size), p.E);
+  }
   const uint32_t below = (1u << lane) - 1;  // the lower lanes
   const L *row = logits + t * p.ld;
   uint32_t key[NV];  // the order of the choice
   float m = 0.f, sum = 1.f;
   {
     float s[NV];  // logits, then softmax's scores times their sum (0 where off)
-    load_lane<NV>(row, e0, p.E, p.vec, -INFINITY, s);
+    load_lane<NV>(row, e0, e1, p.vec, -INFINITY, s);
     if (p.sigmoid && bias) {
       float b[NV];
-      load_lane<NV>(bias, e0, p.E, p.vec_bias, 0.f, b);
+      load_lane<NV>(bias, e0, e1, p.vec_bias, 0.f, b);
 #pragma unroll
       for (int j = 0; j < NV; ++j) key[j] = s[j] <= MGEMM_ROUTE_MASKED ? kKeyOff : order_bits(sigmoidf(s[j]) + b[j]);
     } else if (p.sigmoid) {
@@ -233,7 +240,7 @@ __global__ void __launch_bounds__(kRouteThreads)
       if (sum == 0.f) sum = 1.f;  // every expert is off
       if (bias) {
         float b[NV];
-        load_lane<NV>(bias, e0, p.E, p.vec_bias, 0.f, b);
+        load_lane<NV>(bias, e0, e1, p.vec_bias, 0.f, b);
 #pragma unroll
         for (int j = 0; j < NV; ++j) key[j] = key[j] == kKeyOff ? kKeyOff : order_bits(s[j] / sum + b[j]);
       }
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(kRouteThreads)
   if (p.E < SW * NV) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (e0 + j >= p.E) key[j] = kKeyOut;
+      if (e0 + j >= e1) key[j] = kKeyOut;
   }
 
   // a group's score from its best keys: the largest, or the sum of two terms
@@ -578,19 +585,23 @@ int launch_route_nv(int nv, const void *logits, const float *bias, const RoutePa
                          : go(route_kernel<4, 0, 16, L>, per);
     }
   }
-  switch (nv) {  // (the sizes route_lanes chooses from)
-    case 1: return go(route_kernel<1, GROUPS, 32, L>);
-    case 2: return go(route_kernel<2, GROUPS, 32, L>);
-    case 4: return go(route_kernel<4, GROUPS, 32, L>);
-    case 8: return go(route_kernel<8, GROUPS, 32, L>);
-    case 16: return go(route_kernel<16, GROUPS, 32, L>);
-    case 32: return go(route_kernel<32, GROUPS, 32, L>);
-  }
-  if constexpr (GROUPS == 1) {
-    if (nv == 3) return go(route_kernel<3, GROUPS, 32, L>);
-    if (nv == 5) return go(route_kernel<5, GROUPS, 32, L>);
-    if (nv == 10) return go(route_kernel<10, GROUPS, 32, L>);
-    if (nv == 12) return go(route_kernel<12, GROUPS, 32, L>);
+  if constexpr (GROUPS == 2) {  // (more groups than lanes, or more experts than theirs can hold)
+    return nv <= 8    ? go(route_kernel<8, 2, 32, L>)
+           : nv <= 16 ? go(route_kernel<16, 2, 32, L>)
+                      : go(route_kernel<32, 2, 32, L>);
+  } else {
+    switch (nv) {  // (the sizes launch_route chooses from)
+      case 1: return go(route_kernel<1, GROUPS, 32, L>);
+      case 2: return go(route_kernel<2, GROUPS, 32, L>);
+      case 3: return go(route_kernel<3, GROUPS, 32, L>);
+      case 4: return go(route_kernel<4, GROUPS, 32, L>);
+      case 5: return go(route_kernel<5, GROUPS, 32, L>);
+      case 8: return go(route_kernel<8, GROUPS, 32, L>);
+      case 10: return go(route_kernel<10, GROUPS, 32, L>);
+      case 12: return go(route_kernel<12, GROUPS, 32, L>);
+      case 16: return go(route_kernel<16, GROUPS, 32, L>);
+      case 32: return go(route_kernel<32, GROUPS, 32, L>);
+    }
   }
   return MGEMM_EINVAL;
 }
@@ -599,19 +610,24 @@ template <typename L>
 int launch_route(const void *logits, const float *bias, RouteParams p, float *weights, int32_t *ids, cudaStream_t s) {
   p.vec = ((uintptr_t)logits & 15) == 0 && p.ld * (int64_t)sizeof(L) % 16 == 0;
   p.vec_bias = ((uintptr_t)bias & 15) == 0;
-  // experts per lane: the fewest that are compiled; for groups of whole lanes the fewest of those
-  // that divide a group into a power of two of lanes
-  static constexpr int kPlain[] = {1, 2, 4, 8, 16, 32}, kWhole[] = {1, 2, 3, 4, 5, 8, 10, 12, 16, 32};
-  const int gs = p.E / p.n_group;
-  if (p.n_group > 1)
-    for (int c : kWhole) {
-      const int lanes = gs / c;
-      if (c * 32 < p.E || gs % c || (lanes & (lanes - 1))) continue;
-      p.lanes_per_group = lanes;
+  // experts per lane: the fewest that are compiled
+  static constexpr int kLane[] = {1, 2, 3, 4, 5, 8, 10, 12, 16, 32};
+  if (p.n_group > 1) {
+    // a group on lanes of its own, a power of two of them, where a lane can hold its share (65535 x 104, 8 groups
+    // of 13: 47 us, 91 with the groups scanned in turn)
+    const int size = p.E / p.n_group;
+    p.lanes_per_group = 32;
+    while (p.lanes_per_group * p.n_group > 32 && p.lanes_per_group > 0) p.lanes_per_group /= 2;
+    for (int c : kLane) {
+      if (p.lanes_per_group * c < size) continue;
+      p.group_size = p.lanes_per_group * c == size ? 0 : size;
+      p.vec = p.vec && size % c == 0;  // (else lanes start anywhere)
+      p.vec_bias = p.vec_bias && size % c == 0;
       return launch_route_nv<L, 1>(c, logits, bias, p, weights, ids, s);
     }
+  }
   int nv = 32;
-  for (int c : kPlain)
+  for (int c : kLane)
     if (c * 32 >= p.E) {
       nv = c;
       break;

@@ -88,6 +88,22 @@ def test_groups(scoring, E, G, keep, top, k):
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,G,keep,top,k", [(104, 8, 4, 2, 8), (296, 8, 4, 2, 8), (44, 4, 2, 2, 6), (33, 11, 4, 2, 5),
+                                            (21, 3, 2, 1, 9), (62, 31, 9, 2, 10), (66, 33, 9, 2, 7), (10, 2, 1, 2, 5),
+                                            (960, 3, 1, 2, 32), (333, 9, 5, 1, 10), (7, 7, 3, 2, 3), (400, 4, 2, 2, 8)])
+def test_groups_of_any_size(scoring, dtype, E, G, keep, top, k):
+    step = 0.25 if dtype == torch.bfloat16 else 0.01  # (bf16: distinct up to 2^7 steps; beyond that ties)
+    l = spread_logits(11, min(E, 90), E, step)
+    l = np.concatenate([l] + [l - 0.25 * step * i for i in range(1, -(-E // l.shape[1]))], 1)[:, :E]
+    l = torch.from_numpy(l.astype(np.float32)).to(dtype).float().numpy()
+    if scoring == "softmax" or dtype == torch.float32:
+        check(l, k, scoring, dtype=dtype, n_group=G, topk_group=keep, group_top=top)
+    bias = np.random.default_rng(E).permutation(E).astype(np.float32) * 4.0
+    check(l, k, scoring, bias=bias, dtype=dtype, n_group=G, topk_group=keep, group_top=top)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_picks_that_crowd_into_a_lane(scoring):
     # the best experts are neighbours: lanes of 2 to 32 experts give up many, or all, of theirs
     for E, k in ((64, 16), (96, 32), (256, 32), (512, 32), (1024, 32)):
