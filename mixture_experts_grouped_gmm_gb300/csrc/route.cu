@@ -458,13 +458,14 @@ __global__ void __launch_bounds__(kRouteThreads)
 }
 
 // Softmax with raw weights: every expert's probability is needed,
-// - s_e sum g w everywhere and the picks over it.  SW lanes per token.
-template <typename L, int SW>
+// - s_e sum g w everywhere and the picks over it.  SW lanes per token; VEC: rows
+// in 16-byte units, else value by value.
+template <typename L, int SW, bool VEC>
 __global__ void __launch_bounds__(kRouteThreads)
     route_bwd_rows_kernel(const float *__restrict__ grad_w, const L *__restrict__ logits,
                           const float *__restrict__ weights, const int32_t *__restrict__ ids, const RouteBwdParams p,
                           L *__restrict__ grad) {
-  constexpr int U = 16 / sizeof(L);
+  constexpr int U = VEC ? 16 / sizeof(L) : 1;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & (SW - 1);
@@ -474,19 +475,23 @@ __global__ void __launch_bounds__(kRouteThreads)
   const int64_t t = live ? t0 : p.T - 1;
   const L *row = logits + t * p.ld;
   L *out = grad + t * p.ld_grad;
-  const int n = p.vec && p.vec_grad ? p.E / U : 0;  // whole 16-byte units, then single values
+  const int n = p.E / U;  // whole units, then single values
   float m = -INFINITY, sum = 0.f, f = 0.f;
   for (int r = lane; r < p.top_k; r += SW) {
     const int id = __ldg(ids + t * p.top_k + r);
     if (id >= 0 && id < p.E) f += __ldg(grad_w + t * p.top_k + r) * __ldg(weights + t * p.top_k + r);
   }
-  // the lane's first two units stay in registers
-  constexpr int H = 2;
+  auto put = [&](int u, const float(&x)[U]) {
+    if constexpr (VEC) store_unit(out + u * U, x);
+    else store_grad(out + u, x[0]);
+  };
+  // the lane's first units stay in registers
+  constexpr int H = VEC ? 2 : 16;
   float v[H][U];
 #pragma unroll
   for (int h = 0; h < H; ++h) {
     if (h * SW + lane < n) {
-      load_values<U>(row + (h * SW + lane) * U, true, v[h]);
+      load_values<U>(row + (h * SW + lane) * U, VEC, v[h]);
     } else {
 #pragma unroll
       for (int i = 0; i < U; ++i) v[h][i] = -INFINITY;
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(kRouteThreads)
   auto others = [&](auto &&use) {
     for (int u = H * SW + lane; u < n; u += SW) {
       float x[U];
-      load_values<U>(row + u * U, true, x);
+      load_values<U>(row + u * U, VEC, x);
       use(u, x);
     }
   };
@@ -533,12 +538,12 @@ __global__ void __launch_bounds__(kRouteThreads)
       if (h * SW + lane < n) {
 #pragma unroll
         for (int i = 0; i < U; ++i) v[h][i] *= c;
-        store_unit(out + (h * SW + lane) * U, v[h]);
+        put(h * SW + lane, v[h]);
       }
     others([&](int u, float(&x)[U]) {
 #pragma unroll
       for (int i = 0; i < U; ++i) x[i] = term(x[i]) * c;
-      store_unit(out + u * U, x);
+      put(u, x);
     });
     for (int e = n * U + lane; e < p.E; e += SW) store_grad(out + e, term(load_logit(row + e)) * c);
   }
@@ -560,9 +565,13 @@ int launch_route_bwd(const float *grad_w, const void *logits, const float *weigh
   if (p.sigmoid || p.renormalize) return go(route_bwd_picks_kernel<L>, kBwdTokens);
   // as many lanes as a row has 16-byte units, up to a warp
   const int units = p.E * (int)sizeof(L) / 16;
-  if (units <= 8) return go(route_bwd_rows_kernel<L, 8>, kRouteThreads / 8);
-  if (units <= 16) return go(route_bwd_rows_kernel<L, 16>, kRouteThreads / 16);
-  return go(route_bwd_rows_kernel<L, 32>, kRouteThreads / 32);
+  if (p.vec && p.vec_grad)
+    return units <= 8    ? go(route_bwd_rows_kernel<L, 8, true>, kRouteThreads / 8)
+           : units <= 16 ? go(route_bwd_rows_kernel<L, 16, true>, kRouteThreads / 16)
+                         : go(route_bwd_rows_kernel<L, 32, true>, kRouteThreads / 32);
+  return units <= 8    ? go(route_bwd_rows_kernel<L, 8, false>, kRouteThreads / 8)
+         : units <= 16 ? go(route_bwd_rows_kernel<L, 16, false>, kRouteThreads / 16)
+                       : go(route_bwd_rows_kernel<L, 32, false>, kRouteThreads / 32);
 }
 
 bool route_sizes_ok(int64_t T, int E, int top_k, int64_t ld) {
