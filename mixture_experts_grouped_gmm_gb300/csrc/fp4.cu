@@ -84,9 +84,8 @@ struct RowCast {
   uint32_t v[NB][P][8];
   float amax[NB];
 
-  // (meanwhile() runs while the loads are under way)
-  template <typename Work>
-  __device__ __forceinline__ void load(const RowReader &rd, int q0, int nblk, int tid, Work &&meanwhile) {
+  // The loads of the blocks from q0 on; then, once they are there, their maxima.
+  __device__ __forceinline__ void issue(const RowReader &rd, int q0, int nblk, int tid) {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       const int q = q0 + i * TPR + tid;
@@ -100,12 +99,17 @@ struct RowCast {
         }
       }
     }
-    meanwhile();
+  }
+  __device__ __forceinline__ void maxima() {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       amax[i] = amax16(v[i][0]);
       if (P > 1) amax[i] = fmaxf(amax[i], amax16(v[i][P - 1]));
     }
+  }
+  __device__ __forceinline__ void load(const RowReader &rd, int q0, int nblk, int tid) {
+    issue(rd, q0, nblk, tid);
+    maxima();
   }
   __device__ __forceinline__ float most() const {
     float a = amax[0];
@@ -187,34 +191,32 @@ __device__ __forceinline__ int row_group(int E, int tid, End &&ended) {
   }
 }
 
-// place(): the row's place in the scale tiles.  live: false for threads whose row
-// is past the last (rd reads zeros, nothing is stored), which come along where a
-// warp holds several rows.
+// c: the row's first blocks, whose loads are under way.  place(): the row's place in
+// the scale tiles, looked up meanwhile.  live: false for threads whose row is past
+// the last (nothing is stored), which come along where a warp holds several rows.
 template <int FMT, int NB, int TPR, typename Place>
-__device__ __forceinline__ void cast_row(const RowReader &rd, int K, Place &&place, int W, uint8_t *codes, uint8_t *sf,
-                                         float *row_scale, int tid, float *sh, bool live = true) {
+__device__ __forceinline__ void cast_row(RowCast<FMT, NB, TPR> &c, const RowReader &rd, int K, Place &&place, int W,
+                                         uint8_t *codes, uint8_t *sf, float *row_scale, int tid, float *sh, bool live) {
   using F = Fp4<FMT>;
   const int nblk = K / F::BLOCK;
-  RowCast<FMT, NB, TPR> c;
   float R = 1.f, Rinv = 1.f;
   const bool once = nblk <= NB * TPR;  // the whole row is held
-  int64_t tile_row;
-  auto nothing = [] {};
-  c.load(rd, 0, nblk, tid, [&] { tile_row = place(); });
+  const int64_t tile_row = place();
+  c.maxima();
   if (F::NV) {
     float a = c.most();
     for (int q0 = NB * TPR; q0 < nblk; q0 += NB * TPR) {
-      c.load(rd, q0, nblk, tid, nothing);
+      c.load(rd, q0, nblk, tid);
       a = fmaxf(a, c.most());
     }
     R = fp4_pow2_scale(kNvfp4RowMax, row_max<TPR>(a, sh));
     Rinv = __frcp_rn(R);  // a power of two
     if (live && tid == 0) *row_scale = R;
-    if (!once) c.load(rd, 0, nblk, tid, nothing);
+    if (!once) c.load(rd, 0, nblk, tid);
   }
   c.store(0, nblk, W, R, Rinv, tile_row, codes, sf, tid, live);
   for (int q0 = NB * TPR; q0 < 4 * W; q0 += NB * TPR) {
-    c.load(rd, q0, nblk, tid, nothing);
+    c.load(rd, q0, nblk, tid);
     c.store(q0, nblk, W, R, Rinv, tile_row, codes, sf, tid, live);
   }
 }
@@ -242,8 +244,10 @@ __global__ void __launch_bounds__(kQuantThreads)
       if (TPR >= 32 && !live) continue;
       const int64_t row = e * S.N + n;
       const RowReader rd{live ? S.in + row * S.ld : nullptr, nullptr, S.vec32};
+      RowCast<FMT, NB, TPR> c;
+      c.issue(rd, 0, K / Fp4<FMT>::BLOCK, tid);
       cast_row<FMT, NB, TPR>(
-          rd, K, [&] { return i; }, W, codes + row * (K / 2), sf, row_scale + row, tid, sh[odd ^= 1], live);
+          c, rd, K, [&] { return i; }, W, codes + row * (K / 2), sf, row_scale + row, tid, sh[odd ^= 1], live);
     }
     return;
   }
@@ -266,14 +270,16 @@ __global__ void __launch_bounds__(kQuantThreads)
       rd.row = S.in + i * S.ld;
       if (S.gated) rd.up = rd.row + K;
     }
-    cast_row<FMT, NB, TPR>(rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1], live);
+    RowCast<FMT, NB, TPR> c;
+    c.issue(rd, 0, K / Fp4<FMT>::BLOCK, tid);
+    cast_row<FMT, NB, TPR>(c, rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1], live);
   }
 }
 
 // mgemm_fill_args and the cast of the token rows in one launch, for at most
 // kQuantThreads groups: CTA 0 fills the args block, the others scan the group
-// sizes themselves (a thread per group) for the rows' places, so
-// that they need not wait for it.  Rows are cast as above, and under the same
+// sizes themselves (a thread per group) for the rows' places, so that they need
+// not wait for it, with their first row's loads under way.  Rows are cast as above, and under the same
 // conditions: none when the sizes are not valid.
 template <int FMT, int NB, int TPR>
 __global__ void __launch_bounds__(kQuantThreads)
@@ -286,6 +292,14 @@ __global__ void __launch_bounds__(kQuantThreads)
     fill_args_body<kQuantThreads>(m, S.E, S.M, args);
     return;
   }
+  // (the first row's loads before the scan)
+  constexpr int kRows = kQuantThreads / TPR;
+  const int tid = threadIdx.x % TPR, sub = TPR < 32 ? (int)(threadIdx.x & 31) / TPR : 0;
+  const int nblk = K / Fp4<FMT>::BLOCK;
+  int64_t i0 = (int64_t)(blockIdx.x - 1) * kRows + threadIdx.x / TPR;
+  auto reader = [&](int64_t i) { return RowReader{S.in + (i < S.M ? i : S.M - 1) * S.ld, nullptr, S.vec32}; };
+  RowCast<FMT, NB, TPR> c;
+  c.issue(reader(i0), 0, nblk, tid);
   __shared__ int ends[kQuantThreads], starts[kQuantThreads];  // a group's last row + 1, its first tile row
   __shared__ GroupSums sums;
   __shared__ float sh[2][kQuantThreads / 32];
@@ -296,20 +310,19 @@ __global__ void __launch_bounds__(kQuantThreads)
   ends[threadIdx.x] = (int)end;
   starts[threadIdx.x] = ((int)tiles - (int)((m + 127) / 128)) * 128;
   __syncthreads();
-  constexpr int kRows = kQuantThreads / TPR;
-  const int tid = threadIdx.x % TPR, sub = TPR < 32 ? (int)(threadIdx.x & 31) / TPR : 0;
   const int W = fp4_words(FMT, K);
   const int64_t step = (int64_t)(gridDim.x - 1) * kRows;
   int odd = 0;
-  for (int64_t i0 = (int64_t)(blockIdx.x - 1) * kRows + threadIdx.x / TPR; i0 - sub < S.M; i0 += step) {
+  for (bool loaded = true; i0 - sub < S.M; i0 += step, loaded = false) {
     const bool live = TPR >= 32 || i0 < S.M;
     const int64_t i = live ? i0 : S.M - 1;
     auto place = [&] {
       const int e = row_group<TPR>(S.E, tid, [&](int j) { return ends[j] <= (int)i; });
       return starts[e] + (i - (e > 0 ? ends[e - 1] : 0));
     };
-    const RowReader rd{S.in + i * S.ld, nullptr, S.vec32};
-    cast_row<FMT, NB, TPR>(rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1], live);
+    const RowReader rd = reader(i);
+    if (!loaded) c.issue(rd, 0, nblk, tid);
+    cast_row<FMT, NB, TPR>(c, rd, K, place, W, codes + i * (K / 2), sf, row_scale + i, tid, sh[odd ^= 1], live);
   }
 }
 
