@@ -195,12 +195,24 @@ def _check_layer(hidden_states, w1, w2):
         raise B.MgemmError("fused_moe takes bf16 activations and weights")
 
 
+def _check_tokens(hidden_states, T):
+    if hidden_states.shape[0] != T:
+        raise B.MgemmError(f"{T} tokens are routed, the hidden states have {hidden_states.shape[0]}")
+
+
+def _check_weights(topk_weights, topk_ids):
+    # (the second product reads a weight for every entry of the ids)
+    if topk_weights.numel() != topk_ids.numel():
+        raise B.MgemmError(f"topk_weights {tuple(topk_weights.shape)} do not fit topk_ids {tuple(topk_ids.shape)}")
+
+
 def fused_moe(hidden_states, w1, w2, gating_output, topk, renormalize):
     """The page's fused_moe: route by gating_output [T, E] (top-k of the
     softmax, renormalized when asked), then fused_experts."""
     T = gating_output.shape[0]
     if T <= ROUTE_ALIGN_TOKENS and T * topk <= B.MGEMM_ROUTE_ALIGN_MAX_ENTRIES:
         _check_layer(hidden_states, w1, w2)
+        _check_tokens(hidden_states, T)
         tw, _, sorted_ids, _, npp, _, args = route_align(gating_output, topk, renormalize)
         return _experts(hidden_states, w1, w2, tw, sorted_ids, npp, args, T, topk)
     topk_weights, topk_ids = route(gating_output, topk, renormalize)
@@ -214,6 +226,8 @@ def fused_experts(hidden_states, w1, w2, topk_weights, topk_ids):
     not placed leaves its rows undefined).  Returns bf16 [T, H]."""
     _check_layer(hidden_states, w1, w2)
     T, top_k = topk_ids.shape
+    _check_tokens(hidden_states, T)
+    _check_weights(topk_weights, topk_ids)
     E = w1.shape[0]
     n = T * top_k
     if n <= B.MGEMM_ROUTE_ALIGN_MAX_ENTRIES:
@@ -283,7 +297,11 @@ def fused_experts_fp4(hidden_states, w1, w2, topk_weights, topk_ids):
         raise B.MgemmError(f"fused_experts_fp4: w1 {w1.shape} and w2 {w2.shape} do not belong together")
     if hidden_states.dtype != torch.bfloat16 or hidden_states.dim() != 2 or hidden_states.shape[1] != H:
         raise B.MgemmError(f"fused_experts_fp4 takes bf16 hidden states [T, {H}]")
+    if topk_ids.dim() != 2 or topk_weights.shape != topk_ids.shape:
+        raise B.MgemmError(f"fused_experts_fp4 takes topk_weights and topk_ids [T, top_k], not {tuple(topk_weights.shape)} "
+                           f"and {tuple(topk_ids.shape)}")
     T, top_k = topk_ids.shape
+    _check_tokens(hidden_states, T)
     x = hidden_states.contiguous()
     dev, n, code = x.device, T * top_k, w1.code
     bf, u8 = torch.bfloat16, torch.uint8
