@@ -117,7 +117,7 @@ def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
 
     x: bf16 [M, K] on the GPU, rows contiguous by expert; w: Fp4Tensor [E, N, K];
     group_sizes: int64 [E] on the GPU, summing to M.  ``out`` (bf16 [M, N]) is
-    allocated when not given.  ``workspace`` (uint8, see
+    allocated when not given.  ``workspace`` (contiguous uint8, see
     mgemm_gmm_fp4_workspace_bytes; scratch that starts with the args block, for
     ``binding.args_status``) is too.  Returns bf16 [M, N]."""
     if type(w) is not Fp4Tensor:
@@ -134,6 +134,8 @@ def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
         raise B.MgemmError("gmm_fp4 has no gradient: call it under torch.no_grad() or on x.detach()")
     if group_sizes.dtype != torch.int64 or group_sizes.numel() != E or not group_sizes.is_contiguous():
         raise B.MgemmError("group_sizes must be contiguous int64 [E]")
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+        raise B.MgemmError("gmm_fp4: the workspace must be contiguous uint8")
     B._cuda(x, group_sizes, out, workspace)
     M = x.shape[0]
     if x.stride(1) != 1 or x.stride(0) % 8 or x.stride(0) < K or x.data_ptr() % 16:

@@ -50,3 +50,12 @@ def test_bf16_layer_refuses_weights_and_tokens_that_do_not_fit_the_ids():
         moe.fused_experts(x[:5], w1, w2, wts, ids)
     with pytest.raises(B.MgemmError, match="hidden states"):
         moe.fused_moe(x[:5], w1, w2, torch.zeros(6, 4), 2, True)
+
+
+def test_product_refuses_a_workspace_that_is_no_plain_bytes():
+    x, w, gs = torch.zeros(8, 64, dtype=BF), fake(2, 64, 64), torch.tensor([4, 4])
+    need = 1 << 20
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(2 * need, dtype=torch.uint8)[::2],
+                torch.zeros(need, dtype=torch.int8), torch.zeros(need, dtype=torch.float32)):
+        with pytest.raises(B.MgemmError, match="workspace"):
+            fp4.gmm_fp4(x, w, gs, workspace=bad)
