@@ -7,7 +7,8 @@
 // (kind::mxf4nvf4): D += sum over the 64 elements of a step of (a sfa)(b sfb),
 // with one scale per 32 (MXFP4, e8m0) or 16 (NVFP4, e4m3) elements of each row
 // read from tensor memory.  NVFP4's two row scales are powers of two outside
-// the sum: the epilogue multiplies by 1 / rx[r] and 1 / rw[e, n].
+// the sum: the epilogue multiplies by 1 / rx[r] and 1 / rw[e, n] (f4_far: the
+// one may be far from 1 where the other brings the output back).
 //
 // A tile is 128 token rows of one group by bn columns; a stage holds 256
 // elements of the contraction (128 bytes of a row): the operands' codes,
@@ -256,6 +257,17 @@ __device__ __forceinline__ void reg_dealloc() {
 }
 // 1 / s of a power of two s
 __device__ __forceinline__ float f4_recip(float s) { return __uint_as_float(0x7F000000u - __float_as_uint(s)); }
+
+// A row's factor f times a column's (2^-51 .. 2^117) has the range of a float, and that times the accumulator (0, or
+// 2^-20 .. 2^23 K) leaves it only where the output does, for f in 2^-64 .. 2.  From any other f a power of two is taken
+// out and returned: it multiplies the outputs once they are rounded, which is exact, and may take them out of range only
+// where they are.  (Row times accumulator first, 1 / rx being up to 2^117, is past a float for rows of about 1e33 on
+// whatever the column's factor.)
+__device__ __forceinline__ float f4_far(float &f) {
+  const int a = (int)((__float_as_uint(f) >> 23) & 0xFFu) - 127, h = a > 0 ? min(a, 126) : a < -64 ? a / 2 : 0;
+  f *= __uint_as_float((uint32_t)(127 - h) << 23);
+  return __uint_as_float((uint32_t)(127 + h) << 23);
+}
 
 __device__ __forceinline__ void store_32b(void *dst, const uint32_t *v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -611,7 +623,7 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         __syncwarp();
       }
       // the row's factor, its place and the tile's
-      const float f = C::NV ? weight * f4_recip(rx) : weight;
+      float f = C::NV ? weight * f4_recip(rx) : weight;
       const int col0 = ti.n0 + h * half, row0 = ti.row0 + q * 32;
       const bool store = row_ok, whole = !p.row_map && q * 32 + 32 <= ti.rows;  // the warp's 32 rows are all the group's
       __nv_bfloat16 *o = p.out + dst * p.N + col0;
@@ -643,6 +655,8 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         if (C::NV) ti = f4_tile<PAIR>(t + t_step, g, p, S, av, na, rank);
         fetch();
       }
+      const float far = C::NV ? f4_far(f) : 1.f;
+      const bool any_far = C::NV && __any_sync(0xffffffffu, far != 1.f);
       const uint64_t f2 = f32x2(f, f);
       uint8_t *buf = sOut + ew * kF4Stage;
 #pragma unroll
@@ -653,17 +667,24 @@ __global__ void __launch_bounds__(kF4Threads, 1)
         for (int j = 0; j < 16; j += 2) {
           const uint32_t *w = &v[c][2 * j];
           uint64_t a = f32x2(w[0], w[1]), b = f32x2(w[2], w[3]);
-          if (C::NV || p.row_weight) {
+          if (C::NV) {
+            const float4 ci = *reinterpret_cast<const float4 *>(cinv + c * 32 + 2 * j);
+            a = mul_f32x2(a, mul_f32x2(f2, f32x2(ci.x, ci.y)));
+            b = mul_f32x2(b, mul_f32x2(f2, f32x2(ci.z, ci.w)));
+          } else if (p.row_weight) {
             a = mul_f32x2(a, f2);
             b = mul_f32x2(b, f2);
           }
-          if (C::NV) {
-            const float4 ci = *reinterpret_cast<const float4 *>(cinv + c * 32 + 2 * j);
-            a = mul_f32x2(a, f32x2(ci.x, ci.y));
-            b = mul_f32x2(b, f32x2(ci.z, ci.w));
-          }
           pk[j] = pack_bf16x2_u64(a);
           pk[j + 1] = pack_bf16x2_u64(b);
+        }
+        if (any_far) {
+          const __nv_bfloat162 m = __float2bfloat162_rn(far);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&pk[j]), m);
+            pk[j] = *reinterpret_cast<const uint32_t *>(&y);
+          }
         }
         if (whole) {
           if (lane == 0) bulk_wait_read<0>();  // the buffer's last store has read it

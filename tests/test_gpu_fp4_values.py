@@ -1,0 +1,90 @@
+"""GPU checks of the 4-bit product's scale factors against oracle.fp4, at the ends
+of their ranges and beside powers of two.
+
+Both sides contract the same decoded values.  As in test_gpu_fp4: the MMAs' partial
+sums are off by at most 2^-14 of sum |x w|, the one rounding to bf16 by 2^-8 of the
+value (or half the smallest bf16 step, below the sums here).  A row scale that is no
+power of two adds three fp32 roundings (its reciprocal and two products), 2^-22 of
+the value: inside what the 2^-14 leaves."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp4 as of
+from tests.helpers import new_args, sentinel_bf16, to_np
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+FORMATS = ["mxfp4", "nvfp4"]
+
+
+def mg():
+    import mixture_experts_grouped_gmm_gb300 as m
+
+    return m
+
+
+def values(shape, seed, exponent=0):
+    """bf16 whose 16-element blocks span 2^-3 .. 2^3, times 2^exponent."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    v = torch.randn(shape, generator=g, device=DEV)
+    sc = torch.exp2(torch.randint(-3, 3, (*shape[:-1], shape[-1] // 16), generator=g, device=DEV).float())
+    return (v * sc.repeat_interleave(16, dim=-1)).to(BF) * 2.0 ** exponent
+
+
+def decoded(x, fmt):
+    return of.values(*of.quant_rows(to_np(x), fmt), fmt)
+
+
+def check(got, ref, mag, fmt):
+    got = to_np(got)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -14 * mag).all()
+
+
+# the rows' factor alone, the columns' alone, or both far from 1: every output is finite
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("xe,we", [(110, -17), (119, -30), (-30, 110), (-30, 118), (1, 0), (45, 45), (-30, -30)])
+def test_product_of_far_magnitudes(fmt, xe, we):
+    sizes, K, N = [40, 0, 133], 288, 136
+    M, E = sum(sizes), len(sizes)
+    x, w = values((M, K), 1, xe), values((E, N, K), 2, we)
+    x[3] = values((K,), 3, -20 if xe > 0 else -10)  # a row of another magnitude among them
+    gs = torch.tensor(sizes, dtype=torch.int64, device=DEV)
+    out = mg().gmm_fp4(x, mg().quantize_fp4(w, fmt), gs)
+    xv, wv = decoded(x, fmt), decoded(w.view(E * N, K), fmt).reshape(E, N, K)
+    check(out, of.gmm(xv, wv, sizes), of.gmm(np.abs(xv), np.abs(wv), sizes), fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_sum_of_zeros_is_zero_at_any_scale(fmt):
+    x, w = torch.zeros(5, 64, dtype=BF, device=DEV), torch.full((1, 24, 64), 2.0 ** 120, dtype=BF, device=DEV)
+    x[:, :32] = 2.0 ** 120
+    w[:, :, :32] = 0
+    assert not mg().gmm_fp4(x, mg().quantize_fp4(w, fmt), torch.tensor([5], device=DEV)).any()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("xe,we", [(0, 0), (110, -17), (-30, 110)])
+def test_weighted_rows_of_far_magnitudes(fmt, xe, we):
+    sizes, K, N = [7, 130], 160, 72
+    M, E = sum(sizes), len(sizes)
+    B = mg().binding
+    x, w = values((M, K), 4, xe), values((E, N, K), 5, we)
+    q = mg().quantize_fp4(w, fmt)
+    args = new_args(E, DEV)
+    B.mgemm_fill_args(torch.tensor(sizes, dtype=torch.int64, device=DEV), E, M, args)
+    codes = torch.empty(M, K // 2, dtype=torch.uint8, device=DEV)
+    sf = torch.empty(B.mgemm_fp4_scale_bytes(q.code, B.mgemm_colwise_ld(M, E), K), dtype=torch.uint8, device=DEV)
+    rs = torch.empty(M, device=DEV) if fmt == "nvfp4" else None
+    B.mgemm_quant_fp4_rows(args, E, M, x, K, q.code, codes, sf, rs)
+    rmap = torch.randperm(M, generator=torch.Generator().manual_seed(1)).to(DEV, torch.int32)
+    wt = torch.tensor([0.3, -2.5, 1e-6, 7.0, 0.0], device=DEV).repeat(M)[:M].contiguous()
+    out = sentinel_bf16((M, N), DEV)
+    B.mgemm_fwd_fp4(args, q.code, codes, sf, rs, q.codes, q.scales, q.row_scale, out, M, K, N, E, rmap, M, wt)
+    xv, wv = decoded(x, fmt), decoded(w.view(E * N, K), fmt).reshape(E, N, K)
+    to = rmap.long()
+    f = to_np(wt[to])[:, None]
+    check(out[to], of.gmm(xv, wv, sizes) * f, of.gmm(np.abs(xv), np.abs(wv), sizes) * np.abs(f), fmt)
