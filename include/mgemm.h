@@ -694,7 +694,9 @@ int mgemm_route_bwd(const float *grad_weights, const void *logits, int logits_bf
  *                448), b = e4m3_rne(amax16 R / 6), code = e2m1_rne_sat(x R / b), 0
  *                where b = 0; value code b / R
  * (finite inputs; others give unspecified codes, and the sign of a zero is
- * unspecified).
+ * unspecified).  Tensors from elsewhere may have row scales that are no powers of
+ * two (positive, from 2^-120 to 2^120): mgemm_dequant_fp4 multiplies by their
+ * reciprocals, correctly rounded, mgemm_fwd_fp4 by reciprocals within 2^-23.
  *
  * Scale bytes lie in tiles of 128 rows by one 4-byte word of each row, a word
  * being the row's scales of 128 (MXFP4) or 64 (NVFP4) consecutive elements:
@@ -718,9 +720,9 @@ int64_t mgemm_fp4_scale_bytes(int fmt, int64_t rows, int K);
  *              written (zeros for rows past N and blocks past K)
  *   row_scale  float32 [E * N] (MGEMM_NVFP4), else ignored
  * K % 32 == 0.  E, N >= 0; nothing is launched when either is 0.
- * mgemm_dequant_fp4 -- the values the codes stand for, to bf16 (exact: a code
- * times its scales has at most 6 significant bits; below 2^-133 they round, and
- * past bf16's range they stay at its largest value).
+ * mgemm_dequant_fp4 -- the values the codes stand for, to bf16 (exact for the
+ * casts' scales: a code times them has at most 6 significant bits; below 2^-133
+ * they round, and past bf16's range they stay at its largest value).
  *   out        bf16, row i at out + i * ld_out elements (ld_out >= K, % 8 == 0)
  * Errors: -1 (sizes, format, NULL), -2 (alignment), -4 (CUDA).
  */

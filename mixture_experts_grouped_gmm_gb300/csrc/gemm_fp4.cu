@@ -6,9 +6,10 @@
 // over the tile schedule of mgemm_fill_args.  The MMAs are block-scaled
 // (kind::mxf4nvf4): D += sum over the 64 elements of a step of (a sfa)(b sfb),
 // with one scale per 32 (MXFP4, e8m0) or 16 (NVFP4, e4m3) elements of each row
-// read from tensor memory.  NVFP4's two row scales are powers of two outside
-// the sum: the epilogue multiplies by 1 / rx[r] and 1 / rw[e, n] (f4_far: the
-// one may be far from 1 where the other brings the output back).
+// read from tensor memory.  NVFP4's two row scales lie outside the sum: the
+// epilogue multiplies by 1 / rx[r] and 1 / rw[e, n] (f4_far: the one may be far
+// from 1 where the other brings the output back).  The casts' are powers of two,
+// weights from elsewhere may have any.
 //
 // A tile is 128 token rows of one group by bn columns; a stage holds 256
 // elements of the contraction (128 bytes of a row): the operands' codes,
@@ -255,8 +256,13 @@ template <int N>
 __device__ __forceinline__ void reg_dealloc() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// 1 / s of a power of two s
-__device__ __forceinline__ float f4_recip(float s) { return __uint_as_float(0x7F000000u - __float_as_uint(s)); }
+
+// 1 / s within 2^-23 of it; exact where s is a power of two (2^-120 .. 2^120), as the casts' scales are
+__device__ __forceinline__ float f4_recip(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return r;
+}
 
 // A row's factor f times a column's (2^-51 .. 2^117) has the range of a float, and that times the accumulator (0, or
 // 2^-20 .. 2^23 K) leaves it only where the output does, for f in 2^-64 .. 2.  From any other f a power of two is taken

@@ -37,7 +37,9 @@ def _format(fmt):
 class Fp4Tensor:
     """A [E, N, K] tensor in 4-bit codes: ``codes`` uint8 [E, N, K / 2], ``scales``
     uint8 (the tiled scale factors of mgemm.h), ``row_scale`` float32 [E, N] for
-    "nvfp4" and None for "mxfp4"; ``fmt``, ``shape`` and ``device``."""
+    "nvfp4" and None for "mxfp4"; ``fmt``, ``shape`` and ``device``.  The values are
+    code * scale, for "nvfp4" code * scale / row_scale: a power of two from
+    quantize_fp4, any positive one where the tensor comes from elsewhere."""
 
     def __init__(self, codes, scales, row_scale, fmt):
         self.code = _format(fmt)

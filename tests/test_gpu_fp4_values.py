@@ -88,3 +88,33 @@ def test_weighted_rows_of_far_magnitudes(fmt, xe, we):
     to = rmap.long()
     f = to_np(wt[to])[:, None]
     check(out[to], of.gmm(xv, wv, sizes) * f, of.gmm(np.abs(xv), np.abs(wv), sizes) * np.abs(f), fmt)
+
+
+# a checkpoint's row scale is any float: the value is code * b / row_scale for the product as for the way back
+def test_row_scales_that_are_no_powers_of_two():
+    sizes, K, N = [3, 70, 0, 160], 320, 200
+    M, E = sum(sizes), len(sizes)
+    x, w = values((M, K), 6), values((E, N, K), 7)
+    q = mg().quantize_fp4(w, "nvfp4")
+    factor = torch.tensor([1.5, 1.0, 0.7, 3.1e-3, 1.999999, 448.0], device=DEV).repeat(E * N)[:E * N].view(E, N)
+    rows = (q.row_scale * factor).contiguous()
+    q2 = mg().Fp4Tensor(q.codes, q.scales, rows, "nvfp4")
+    codes, byte, _ = of.quant_rows(to_np(w).reshape(E * N, K), "nvfp4")
+    wv = of.values(codes, byte, to_np(rows).reshape(-1), "nvfp4").reshape(E, N, K)
+    back = to_np(mg().dequantize_fp4(q2))
+    assert (np.abs(back - wv) <= 2.0 ** -8 * np.abs(wv)).all()
+    out = mg().gmm_fp4(x, q2, torch.tensor(sizes, dtype=torch.int64, device=DEV))
+    xv = decoded(x, "nvfp4")
+    check(out, of.gmm(xv, wv, sizes), of.gmm(np.abs(xv), np.abs(wv), sizes), "nvfp4")
+
+
+def test_row_scales_of_powers_of_two_are_exact():
+    K, N = 64, 208
+    x, w = values((5, K), 12), values((1, N, K), 13)
+    gs = torch.tensor([5], device=DEV)
+    q = mg().quantize_fp4(w, "nvfp4")
+    one = mg().gmm_fp4(x, mg().Fp4Tensor(q.codes, q.scales, torch.full_like(q.row_scale, 2.0 ** 10), "nvfp4"), gs)
+    e = torch.arange(N, device=DEV) - 100                # 2^-100 .. 2^107
+    rows = torch.exp2(e.double()).float().view(1, N)
+    far = mg().gmm_fp4(x, mg().Fp4Tensor(q.codes, q.scales, rows, "nvfp4"), gs)
+    assert torch.equal((far.double() * torch.exp2(e.double() - 10)).to(BF), one)
