@@ -91,7 +91,8 @@ def _route_logits(logits, scoring):
     if logits.dim() != 2 or (logits.dtype != torch.float32 and logits.dtype != torch.bfloat16):
         raise B.MgemmError("routing takes float32 or bf16 logits [T, E]")
     ld, unit = logits.stride()
-    return logits if unit == 1 and ld >= logits.shape[1] else logits.contiguous()
+    # (clone, not contiguous(): a single row of strides (1, 1) is contiguous to torch)
+    return logits if unit == 1 and ld >= logits.shape[1] else logits.clone(memory_format=torch.contiguous_format)
 
 
 def route_experts(logits, topk, scoring="softmax", bias=None, n_group=1, topk_group=1, group_top=1, renormalize=True,
@@ -302,7 +303,9 @@ def fused_experts_fp4(hidden_states, w1, w2, topk_weights, topk_ids):
                            f"and {tuple(topk_ids.shape)}")
     T, top_k = topk_ids.shape
     _check_tokens(hidden_states, T)
-    x = hidden_states.contiguous()
+    x = hidden_states
+    if x.stride(1) != 1 or x.stride(0) % 8 or x.stride(0) < H or x.data_ptr() % 16:
+        x = x.clone(memory_format=torch.contiguous_format)
     dev, n, code = x.device, T * top_k, w1.code
     bf, u8 = torch.bfloat16, torch.uint8
     out = torch.empty(T, H, dtype=bf, device=dev)

@@ -1,0 +1,59 @@
+"""GPU checks of how the routing and 4-bit calls take their arguments: layouts of
+single rows and of rows that start anywhere."""
+
+import pytest
+import torch
+
+from tests.helpers import sentinel_bf16
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def mg():
+    import mixture_experts_grouped_gmm_gb300 as m
+
+    return m
+
+
+def fp4_layer(T, E=8, k=2, H=96, F=64, fmt="nvfp4"):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    w1, w2 = (mg().quantize_fp4((torch.randn(s, generator=g, device=DEV) * 0.1).to(BF), fmt)
+              for s in ((E, 2 * F, H), (E, H, F)))
+    return torch.randn(T, H, generator=g, device=DEV).to(BF), w1, w2, torch.randn(T, E, generator=g, device=DEV)
+
+
+# [1, n] as the transpose of a column: strides (1, 1), "contiguous" to torch
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_routing_takes_one_token_as_a_transposed_column(scoring, dtype):
+    col = torch.randn(64, 1, device=DEV).to(dtype)
+    row = col.flatten().clone()[None]
+    m = mg().moe
+    g = torch.randn(1, 6, device=DEV)
+    for renorm in (True, False):
+        w, ids = m.route_experts(col.t(), 6, scoring, renormalize=renorm)
+        w2, ids2 = m.route_experts(row, 6, scoring, renormalize=renorm)
+        assert torch.equal(w, w2) and torch.equal(ids, ids2)
+        d = m.route_experts_backward(g, col.t(), w, ids, scoring, renorm)
+        assert torch.equal(d, m.route_experts_backward(g, row, w, ids, scoring, renorm))
+
+
+@pytest.mark.parametrize("k", [2, 5])
+def test_fp4_layer_takes_any_layout_of_the_tokens(k):
+    x, w1, w2, lg = fp4_layer(9)
+    m = mg().moe
+    ref = m.fused_moe_fp4(x, w1, w2, lg, k)
+    wide = sentinel_bf16((9, 104), DEV)
+    wide[:, :96] = x
+    odd = sentinel_bf16((9, 97), DEV)
+    odd[:, :96] = x
+    shifted = torch.empty(9 * 96 + 1, dtype=BF, device=DEV)[1:].view(9, 96)  # 2 bytes past a 16-byte boundary
+    shifted.copy_(x)
+    for v in (wide[:, :96], odd[:, :96], shifted, x.t().contiguous().t()):
+        assert torch.equal(m.fused_moe_fp4(v, w1, w2, lg, k), ref)
+    one, lg1 = (t[:1].flatten().clone().view(-1, 1).t() for t in (x, lg))
+    assert one.stride() == (1, 1) and lg1.stride() == (1, 1)
+    assert torch.equal(m.fused_moe_fp4(one, w1, w2, lg1, k),
+                       m.fused_moe_fp4(x[:1], w1, w2, lg[:1], k))
