@@ -13,6 +13,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -110,6 +111,7 @@ PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     const at::Tensor *l = tensor(a[0]), *b = tensor(a[3]);
     const int type = logits_type(l);
+    if (type >= 0 && l->requires_grad() && c10::GradMode::is_enabled()) Py_RETURN_NONE;  // (a differentiable call)
     if (type < 0 || (a[3] != Py_None && !(on_gpu(b, at::kFloat) && b->numel() == l->size(1) && b->is_contiguous())))
       Py_RETURN_NONE;
     bool bad = false;

@@ -103,11 +103,13 @@ def route_experts(logits, topk, scoring="softmax", bias=None, n_group=1, topk_gr
     ``group_top=2`` their two best experts), the topk largest, weights renormalized
     when asked and times ``scale``.  A logit of -inf (or its type's lowest value)
     switches the expert off.  Returns (topk_weights float32 [T, topk], topk_ids
-    int32 [T, topk]); ``Router`` is the same with a gradient."""
+    int32 [T, topk]); logits that require a gradient go through ``Router``."""
     r = B.calls().route(logits, topk, SCORES.get(scoring), bias, n_group, topk_group, group_top, renormalize, scale)
     if r is not None:
         return r if type(r) is tuple else B._check(r, "mgemm_route")
     # not the plain case: looked at, mended or refused here
+    if logits.requires_grad and torch.is_grad_enabled():
+        return Router.apply(logits, topk, scoring, bias, n_group, topk_group, group_top, renormalize, scale)
     logits = _route_logits(logits, scoring)
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != logits.shape[1] or
                              not bias.is_contiguous()):
@@ -289,7 +291,7 @@ def fused_experts_fp4(hidden_states, w1, w2, topk_weights, topk_ids):
     padding), the token rows gathered and cast to 4 bits, the first product, its
     gate applied and the result cast to 4 bits in one pass, the second product
     with each row times its routed weight and stored at its entry, the sum over a
-    token's entries."""
+    token's entries.  No gradient flows through it."""
     if type(w1) is not Fp4Tensor or type(w2) is not Fp4Tensor or w1.fmt != w2.fmt:
         raise B.MgemmError("fused_experts_fp4 takes two Fp4Tensors of one format")
     E, F2, H = w1.shape
@@ -301,6 +303,8 @@ def fused_experts_fp4(hidden_states, w1, w2, topk_weights, topk_ids):
     if topk_ids.dim() != 2 or topk_weights.shape != topk_ids.shape:
         raise B.MgemmError(f"fused_experts_fp4 takes topk_weights and topk_ids [T, top_k], not {tuple(topk_weights.shape)} "
                            f"and {tuple(topk_ids.shape)}")
+    if torch.is_grad_enabled() and (hidden_states.requires_grad or topk_weights.requires_grad):
+        raise B.MgemmError("the 4-bit layer has no gradient: call it under torch.no_grad() or on detached tensors")
     T, top_k = topk_ids.shape
     _check_tokens(hidden_states, T)
     x = hidden_states

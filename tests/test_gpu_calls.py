@@ -1,5 +1,5 @@
 """GPU checks of how the routing and 4-bit calls take their arguments: layouts of
-single rows and of rows that start anywhere."""
+single rows and of rows that start anywhere, and tensors that require a gradient."""
 
 import pytest
 import torch
@@ -57,3 +57,40 @@ def test_fp4_layer_takes_any_layout_of_the_tokens(k):
     assert one.stride() == (1, 1) and lg1.stride() == (1, 1)
     assert torch.equal(m.fused_moe_fp4(one, w1, w2, lg1, k),
                        m.fused_moe_fp4(x[:1], w1, w2, lg[:1], k))
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_routing_of_logits_that_require_a_gradient_has_one(scoring, dtype):
+    l = torch.randn(33, 64, device=DEV).to(dtype)
+    g = torch.randn(33, 6, device=DEV)
+    a, b = l.clone().requires_grad_(True), l.clone().requires_grad_(True)
+    m = mg().moe
+    how = (6, scoring, None, 8, 4, 2, False, 2.5)
+    w, ids = m.route_experts(a, *how)
+    assert w.requires_grad and not ids.requires_grad
+    (w * g).sum().backward()
+    w2, ids2 = m.Router.apply(b, *how)
+    (w2 * g).sum().backward()
+    assert torch.equal(w, w2) and torch.equal(ids, ids2) and torch.equal(a.grad, b.grad) and a.grad.any()
+    with torch.no_grad():
+        w3, _ = m.route_experts(a, *how)
+    assert not w3.requires_grad and torch.equal(w3, w)
+    assert not m.route_experts(l, *how)[0].requires_grad
+
+
+def test_fp4_layer_refuses_what_requires_a_gradient():
+    x, w1, w2, lg = fp4_layer(5)
+    m, E = mg().moe, mg().binding.MgemmError
+    wts, ids = m.route_experts(lg, 2)
+    xg, lgg, wg = (t.clone().requires_grad_(True) for t in (x, lg, wts))
+    calls = (lambda: m.fused_moe_fp4(xg, w1, w2, lg, 2), lambda: m.fused_moe_fp4(x, w1, w2, lgg, 2),
+             lambda: m.fused_experts_fp4(xg, w1, w2, wts, ids), lambda: m.fused_experts_fp4(x, w1, w2, wg, ids))
+    for bad in calls:
+        with pytest.raises(E, match="gradient"):
+            bad()
+    ref = m.fused_moe_fp4(x, w1, w2, lg, 2)
+    with torch.no_grad():
+        for f in calls:
+            y = f()
+            assert not y.requires_grad and torch.equal(y, ref)
