@@ -693,8 +693,10 @@ int mgemm_route_bwd(const float *grad_weights, const void *logits, int logits_bf
  *                R = 2^floor(log2(fp32(2688 / max(row amax, 1e-12)))) (2688 = 6 x
  *                448), b = e4m3_rne(amax16 R / 6), code = e2m1_rne_sat(x R / b), 0
  *                where b = 0; value code b / R
- * (finite inputs; others give unspecified codes, and the sign of a zero is
- * unspecified).  Tensors from elsewhere may have row scales that are no powers of
+ * (the sign of a zero is unspecified).  NaN and infinity show: a block (MXFP4) or
+ * row (NVFP4) that holds one gets NaN scales (byte 0xFF; 0x7F and R = NaN) and
+ * unspecified codes, its values are NaN, and so is every output of a product that
+ * takes them.  Tensors from elsewhere may have row scales that are no powers of
  * two (positive, from 2^-120 to 2^120): mgemm_dequant_fp4 multiplies by their
  * reciprocals, correctly rounded, mgemm_fwd_fp4 by reciprocals within 2^-23.
  *

@@ -5,6 +5,7 @@
 //   MXFP4  s = 2^floor(log2(6 / amax32)),  code = e2m1(x s)
 //   NVFP4  R = 2^floor(log2(2688 / row amax)),  b = e4m3(amax16 R / 6),
 //          code = e2m1(x R / b)
+//   NaN or infinity in a block (MXFP4) or row (NVFP4): its scales are NaN
 //
 // Memory-bound: 2 bytes read and about 0.55 written per element.  A thread
 // takes whole blocks; a row takes 8 to 128 threads by its length, or 256 where
@@ -12,6 +13,8 @@
 // before its first code, so the thread's blocks stay in registers as they were
 // read (up to NB of them; longer rows are read twice, the second time from
 // cache).  Four threads' scale bytes make a word.
+#include <cfloat>
+
 #include "fill_args.cuh"
 #include "fp4.cuh"
 
@@ -67,12 +70,19 @@ struct RowReader {
   }
 };
 
-// Magnitude maximum of 16 bf16 (a NaN is passed over).
+// The larger one; NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
+// Magnitude maximum of 16 bf16, NaN where one is.
 __device__ __forceinline__ float amax16(const uint32_t (&v)[8]) {
   __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v[0]));
 #pragma unroll
-  for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v[i])));
-  return fmaxf(__low2float(m), __high2float(m));
+  for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&v[i])));
+  return max_nan(__low2float(m), __high2float(m));
 }
 
 // A row by TPR threads (tid of them), NB blocks each at a time: block q is held
@@ -104,7 +114,7 @@ struct RowCast {
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
       amax[i] = amax16(v[i][0]);
-      if (P > 1) amax[i] = fmaxf(amax[i], amax16(v[i][P - 1]));
+      if (P > 1) amax[i] = max_nan(amax[i], amax16(v[i][P - 1]));
     }
   }
   __device__ __forceinline__ void load(const RowReader &rd, int q0, int nblk, int tid) {
@@ -114,7 +124,7 @@ struct RowCast {
   __device__ __forceinline__ float most() const {
     float a = amax[0];
 #pragma unroll
-    for (int i = 1; i < NB; ++i) a = fmaxf(a, amax[i]);
+    for (int i = 1; i < NB; ++i) a = max_nan(a, amax[i]);
     return a;
   }
   // codes and scale bytes of the blocks held (R: the row's power of two and its inverse, NVFP4)
@@ -134,7 +144,7 @@ struct RowCast {
         r = byte ? r : 0.f;
       } else {
         r = fp4_pow2_scale(kMxfp4Max, amax[i]);
-        byte = 254u - (__float_as_uint(r) >> 23);
+        byte = amax[i] <= FLT_MAX ? 254u - (__float_as_uint(r) >> 23) : 0xFFu;  // (0xFF: NaN)
       }
       const uint64_t r2 = ((uint64_t)__float_as_uint(r) << 32) | __float_as_uint(r);
       uint32_t word = q < nblk ? byte << (8 * (q & 3)) : 0u;  // an empty block past the row
@@ -163,7 +173,7 @@ template <int TPR>
 __device__ __forceinline__ float row_max(float a, float *sh) {
   constexpr int LANES = TPR < 32 ? TPR : 32;
 #pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  for (int o = LANES / 2; o > 0; o >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
   if (TPR <= 32) return a;
   // (the rows of a CTA go on by themselves: a barrier each; an even and an odd set of values, so
   // one barrier a row does)
@@ -172,7 +182,7 @@ __device__ __forceinline__ float row_max(float a, float *sh) {
   asm volatile("bar.sync %0, %1;" ::"r"(row + 1), "n"(TPR) : "memory");
   a = sh[w0];
 #pragma unroll
-  for (int i = 1; i < TPR / 32; ++i) a = fmaxf(a, sh[w0 + i]);
+  for (int i = 1; i < TPR / 32; ++i) a = max_nan(a, sh[w0 + i]);
   return a;
 }
 
@@ -207,9 +217,10 @@ __device__ __forceinline__ void cast_row(RowCast<FMT, NB, TPR> &c, const RowRead
     float a = c.most();
     for (int q0 = NB * TPR; q0 < nblk; q0 += NB * TPR) {
       c.load(rd, q0, nblk, tid);
-      a = fmaxf(a, c.most());
+      a = max_nan(a, c.most());
     }
-    R = fp4_pow2_scale(kNvfp4RowMax, row_max<TPR>(a, sh));
+    a = row_max<TPR>(a, sh);
+    R = a <= FLT_MAX ? fp4_pow2_scale(kNvfp4RowMax, a) : nanf("");  // (then every scale byte of the row is NaN's too)
     Rinv = __frcp_rn(R);  // a power of two
     if (live && tid == 0) *row_scale = R;
     if (!once) c.load(rd, 0, nblk, tid);

@@ -49,13 +49,14 @@ __device__ __forceinline__ uint32_t fp4_codes8(const uint32_t *x, uint64_t r2) {
   return r;
 }
 
-// e4m3 byte (no sign here) -> value; e8m0 byte -> value (byte 0: 2^-127, below the normal range)
+// e4m3 byte (no sign here) -> value; e8m0 byte -> value (byte 0: 2^-127, below the normal range; 255: NaN)
 __device__ __forceinline__ float e4m3_value(uint32_t byte) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3);
   return __half2float(__half(h));
 }
 __device__ __forceinline__ float e8m0_value(uint32_t byte) {
-  return __uint_as_float(byte ? byte << 23 : 0x00400000u);
+  const float v = __uint_as_float(byte ? byte << 23 : 0x00400000u);
+  return __fmaf_rn(v, 0.f, v);  // (infinity, byte 255's bits, to NaN)
 }
 
 // 2^floor(log2(fp32(num / max(amax, 1e-12)))): see pow2_scale_from_amax

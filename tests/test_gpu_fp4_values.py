@@ -118,3 +118,57 @@ def test_row_scales_of_powers_of_two_are_exact():
     rows = torch.exp2(e.double()).float().view(1, N)
     far = mg().gmm_fp4(x, mg().Fp4Tensor(q.codes, q.scales, rows, "nvfp4"), gs)
     assert torch.equal((far.double() * torch.exp2(e.double() - 10)).to(BF), one)
+
+
+# a NaN or an infinity shows: in the way back, in the product and in the routed layer
+NON_FINITE = [float("nan"), float("inf"), -float("inf")]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("shape", [(9, 96), (4901, 96), (40, 1440), (1301, 2560), (9, 8224)])
+def test_casts_of_non_finite_elements_are_nan(fmt, shape):
+    R, K = shape
+    x = values(shape, 8)
+    ref = mg().dequantize_fp4(mg().quantize_fp4(x, fmt))[0]
+    block = 32 if fmt == "mxfp4" else K                  # one block, or (the row's scale) the whole row
+    for i, v in enumerate(NON_FINITE):
+        row, col = (3 * i + 1) % R, (K // 3) * i + 5
+        x[row, col] = v
+        ref[row, col // block * block:(col // block + 1) * block] = float("nan")
+    got = mg().dequantize_fp4(mg().quantize_fp4(x, fmt))[0]
+    assert torch.equal(got.isnan(), ref.isnan())
+    assert torch.equal(got.nan_to_num(0.0), ref.nan_to_num(0.0))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("sizes,K,N", [([20, 0, 150], 320, 136), ([3, 5, 8], 5120, 264)])
+def test_products_of_non_finite_operands_are_nan(fmt, sizes, K, N):
+    M, E = sum(sizes), len(sizes)
+    x, w = values((M, K), 9), values((E, N, K), 10)
+    gs = torch.tensor(sizes, dtype=torch.int64, device=DEV)
+    ref = mg().gmm_fp4(x, mg().quantize_fp4(w, fmt), gs)
+    for i, v in enumerate(NON_FINITE):
+        x[4 * i + 1, (K // 3) * i + 7] = v
+        ref[4 * i + 1] = float("nan")
+    w[2, 70, 40] = float("nan")
+    w[2, 3, K - 1] = float("inf")
+    ref[sizes[0] + sizes[1]:, [3, 70]] = float("nan")
+    got = mg().gmm_fp4(x, mg().quantize_fp4(w, fmt), gs)
+    assert torch.equal(got.isnan(), ref.isnan())
+    assert torch.equal(got.nan_to_num(0.0), ref.nan_to_num(0.0))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_non_finite_token_shows_in_the_layer(fmt):
+    T, E, k, H, F = 50, 8, 2, 96, 64
+    g = torch.Generator(device=DEV).manual_seed(11)
+    w1, w2 = (mg().quantize_fp4((torch.randn(s, generator=g, device=DEV) * 0.1).to(BF), fmt)
+              for s in ((E, 2 * F, H), (E, H, F)))
+    x = torch.randn(T, H, generator=g, device=DEV).to(BF)
+    lg = torch.randn(T, E, generator=g, device=DEV)
+    ref = mg().moe.fused_moe_fp4(x, w1, w2, lg, k)
+    x[7, 30], x[9, 95] = float("nan"), float("inf")
+    ref[[7, 9]] = float("nan")
+    got = mg().moe.fused_moe_fp4(x, w1, w2, lg, k)
+    assert torch.equal(got.isnan(), ref.isnan())
+    assert torch.equal(got.nan_to_num(0.0), ref.nan_to_num(0.0))
