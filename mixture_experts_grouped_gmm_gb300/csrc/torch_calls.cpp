@@ -6,8 +6,10 @@
 // A function takes what its Python caller (moe.py, fp4.py) was given and
 // returns the outputs; None where the arguments are not the plain case (another
 // type or layout, a CPU tensor), which the caller then checks, mends or refuses;
-// or an int, the C entry's negative return code.  No step of a computation is
-// here, and the library is reached through the addresses that bind() is given
+// or an int, the C entry's negative return code.  Where the program has other
+// Python threads, allocations and the C call run without the interpreter's lock:
+// either may wait (for memory, for a place in a full launch queue), and the other
+// threads go on meanwhile.  No step of a computation is here, and the library is reached through the addresses that bind() is given
 // (those of the loaded libmgemm.so).
 #include <Python.h>
 
@@ -70,6 +72,20 @@ PyObject *guarded(F f) {
   return nullptr;
 }
 
+// Gives up the interpreter's lock while it lives, if there is another thread that could take it (giving it up and
+// taking it back is 0.7 us of a call's 5).
+struct Unlocked {
+  PyThreadState *state = nullptr;
+  Unlocked() {
+    PyThreadState *first = PyInterpreterState_ThreadHead(PyInterpreterState_Get());
+    if (first && PyThreadState_Next(first)) state = PyEval_SaveThread();
+  }
+  Unlocked(const Unlocked &) = delete;
+  ~Unlocked() {
+    if (state) PyEval_RestoreThread(state);
+  }
+};
+
 PyObject *pair(at::Tensor a, at::Tensor b) {
   PyObject *x = THPVariable_Wrap(std::move(a)), *y = THPVariable_Wrap(std::move(b));
   PyObject *t = x && y ? PyTuple_Pack(2, x, y) : nullptr;
@@ -124,10 +140,16 @@ PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const double scale = PyFloat_Check(a[8]) ? PyFloat_AS_DOUBLE(a[8]) : (bad = true, 0.0);
     const int64_t T = l->size(0), E = l->size(1);
     if (bad || !small(E) || v[0] < 1 || v[0] > MGEMM_ROUTE_MAX_TOPK) Py_RETURN_NONE;
-    at::Tensor w = empty({T, v[0]}, at::kFloat, l->device()), ids = empty({T, v[0]}, at::kInt, l->device());
-    const int rc = p_route(l->data_ptr(), type, l->stride(0), b ? b->data_ptr<float>() : nullptr, T, (int)E, (int)v[0],
-                           (int)v[1], (int)v[2], (int)v[3], (int)v[4], v[5] != 0, (float)scale, w.data_ptr<float>(),
-                           ids.data_ptr<int32_t>(), stream_of(*l));
+    at::Tensor w, ids;
+    int rc;
+    {
+      const Unlocked unlocked;
+      w = empty({T, v[0]}, at::kFloat, l->device());
+      ids = empty({T, v[0]}, at::kInt, l->device());
+      rc = p_route(l->data_ptr(), type, l->stride(0), b ? b->data_ptr<float>() : nullptr, T, (int)E, (int)v[0], (int)v[1],
+                   (int)v[2], (int)v[3], (int)v[4], v[5] != 0, (float)scale, w.data_ptr<float>(), ids.data_ptr<int32_t>(),
+                   stream_of(*l));
+    }
     return rc ? code(rc) : pair(std::move(w), std::move(ids));
   });
 }
@@ -147,10 +169,15 @@ PyObject *route_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const double scale = PyFloat_Check(a[6]) ? PyFloat_AS_DOUBLE(a[6]) : (bad = true, 0.0);
     const int64_t T = l->size(0), E = l->size(1), k = ids->size(1);
     if (bad || !small(scoring) || !small(E) || !small(k)) Py_RETURN_NONE;
-    at::Tensor out = empty({T, E}, l->scalar_type(), l->device());
-    const int rc = p_route_bwd(g->data_ptr<float>(), l->data_ptr(), type, l->stride(0), w->data_ptr<float>(),
-                               ids->data_ptr<int32_t>(), T, (int)E, (int)k, (int)scoring, renorm != 0, (float)scale,
-                               out.data_ptr(), E, stream_of(*l));
+    at::Tensor out;
+    int rc;
+    {
+      const Unlocked unlocked;
+      out = empty({T, E}, l->scalar_type(), l->device());
+      rc = p_route_bwd(g->data_ptr<float>(), l->data_ptr(), type, l->stride(0), w->data_ptr<float>(),
+                       ids->data_ptr<int32_t>(), T, (int)E, (int)k, (int)scoring, renorm != 0, (float)scale, out.data_ptr(),
+                       E, stream_of(*l));
+    }
     return rc ? code(rc) : THPVariable_Wrap(std::move(out));
   });
 }
@@ -172,11 +199,17 @@ PyObject *quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (per < 0) Py_RETURN_NONE;
     const int64_t n_codes = (E * N * (K / 2) + 255) / 256 * 256, n_scales = E * per;
     const bool rows = fmt == MGEMM_NVFP4;
-    at::Tensor s = empty({n_codes + n_scales + (rows ? 4 * E * N : 0)}, at::kByte, x->device());
-    uint8_t *p = s.data_ptr<uint8_t>();
-    uint8_t *r = rows ? p + n_codes + n_scales : nullptr;
-    const int rc = p_quant(x->data_ptr(), (int)E, N, (int)K, ld, (int)fmt, p, p + n_codes, reinterpret_cast<float *>(r),
-                           stream_of(*x));
+    at::Tensor s;
+    uint8_t *p, *r;
+    int rc;
+    {
+      const Unlocked unlocked;
+      s = empty({n_codes + n_scales + (rows ? 4 * E * N : 0)}, at::kByte, x->device());
+      p = s.data_ptr<uint8_t>();
+      r = rows ? p + n_codes + n_scales : nullptr;
+      rc = p_quant(x->data_ptr(), (int)E, N, (int)K, ld, (int)fmt, p, p + n_codes, reinterpret_cast<float *>(r),
+                   stream_of(*x));
+    }
     if (rc) return code(rc);
     PyObject *t = THPVariable_Wrap(std::move(s));
     if (!t) return nullptr;
@@ -214,10 +247,14 @@ PyObject *dequantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
     bool bad = false;
     const int64_t fmt = integer(a[2], bad), dev = integer(a[3], bad);
     if (bad || !addresses(a[0], p) || !shape3(a[1], s) || dev < 0 || dev > 63) Py_RETURN_NONE;
-    at::Tensor out = empty({s[0], s[1], s[2]}, at::kBFloat16, at::Device(at::kCUDA, (c10::DeviceIndex)dev));
-    const int rc = p_dequant(reinterpret_cast<uint8_t *>(p[0]), reinterpret_cast<uint8_t *>(p[1]),
-                             reinterpret_cast<float *>(p[2]), (int)s[0], s[1], (int)s[2], (int)fmt, out.data_ptr(), s[2],
-                             stream_of(out));
+    at::Tensor out;
+    int rc;
+    {
+      const Unlocked unlocked;
+      out = empty({s[0], s[1], s[2]}, at::kBFloat16, at::Device(at::kCUDA, (c10::DeviceIndex)dev));
+      rc = p_dequant(reinterpret_cast<uint8_t *>(p[0]), reinterpret_cast<uint8_t *>(p[1]), reinterpret_cast<float *>(p[2]),
+                     (int)s[0], s[1], (int)s[2], (int)fmt, out.data_ptr(), s[2], stream_of(out));
+    }
     return rc ? code(rc) : THPVariable_Wrap(std::move(out));
   });
 }
@@ -239,10 +276,16 @@ PyObject *gmm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (x->stride(1) != 1 || ld < K || ld % 8 || reinterpret_cast<uintptr_t>(x->data_ptr()) % 16) Py_RETURN_NONE;
     const int64_t nb = p_workspace_bytes((int)fmt, M, (int)K, (int)E);
     if (nb < 0) Py_RETURN_NONE;
-    at::Tensor out = empty({M, N}, at::kBFloat16, x->device()), ws = empty({nb}, at::kByte, x->device());
-    const int rc = p_gmm(g->data_ptr<int64_t>(), (int)E, (int)fmt, x->data_ptr(), ld, reinterpret_cast<uint8_t *>(p[0]),
-                         reinterpret_cast<uint8_t *>(p[1]), reinterpret_cast<float *>(p[2]), out.data_ptr(), M, (int)K,
-                         (int)N, ws.data_ptr(), nb, stream_of(*x));
+    at::Tensor out, ws;
+    int rc;
+    {
+      const Unlocked unlocked;
+      out = empty({M, N}, at::kBFloat16, x->device());
+      ws = empty({nb}, at::kByte, x->device());
+      rc = p_gmm(g->data_ptr<int64_t>(), (int)E, (int)fmt, x->data_ptr(), ld, reinterpret_cast<uint8_t *>(p[0]),
+                 reinterpret_cast<uint8_t *>(p[1]), reinterpret_cast<float *>(p[2]), out.data_ptr(), M, (int)K, (int)N,
+                 ws.data_ptr(), nb, stream_of(*x));
+    }
     return rc ? code(rc) : THPVariable_Wrap(std::move(out));
   });
 }

@@ -1,5 +1,8 @@
 """GPU checks of how the routing and 4-bit calls take their arguments: layouts of
-single rows and of rows that start anywhere, and tensors that require a gradient."""
+single rows and of rows that start anywhere, tensors that require a gradient, and other threads."""
+
+import threading
+import time
 
 import pytest
 import torch
@@ -94,3 +97,35 @@ def test_fp4_layer_refuses_what_requires_a_gradient():
         for f in calls:
             y = f()
             assert not y.requires_grad and torch.equal(y, ref)
+
+
+def test_other_threads_run_while_a_call_waits_for_the_launch_queue():
+    # Some thousand launches behind a kernel of half a second fill the stream's queue, and the call that finds
+    # it full waits in the driver: another thread of the program must go on meanwhile.
+    l = torch.randn(4, 64, device=DEV)
+    mg().moe.route_experts(l, 4)
+    torch.cuda.synchronize()
+    gaps, stop = [0.0], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps[0] = max(gaps[0], now - last)
+            last = now
+
+    t = threading.Thread(target=tick)
+    t.start()
+    try:
+        t0 = time.perf_counter()
+        torch.cuda._sleep(1_000_000_000)  # about half a second at 2 GHz
+        for _ in range(4000):
+            mg().moe.route_experts(l, 4)
+        took = time.perf_counter() - t0
+    finally:
+        stop.set()
+        t.join()
+    torch.cuda.synchronize()
+    assert took > 0.25, "the queue did not fill: the test says nothing"
+    assert gaps[0] < took / 2, f"another thread stood still for {gaps[0]:.2f} of {took:.2f} s"
