@@ -207,9 +207,16 @@ def _check(rc, what):
 
 
 def _cuda(*ts):
+    dev = None
     for t in ts:
-        if t is not None and not t.is_cuda:
-            raise MgemmError("mgemm kernels take device tensors only")
+        if t is not None:
+            d = t.get_device()  # -1 on the CPU
+            if d < 0:
+                raise MgemmError("mgemm kernels take device tensors only")
+            if dev is None:
+                dev = d
+            elif d != dev:
+                raise MgemmError(f"mgemm kernels take tensors of one device, not of {dev} and {d}")
 
 
 def mgemm_args_bytes(E):

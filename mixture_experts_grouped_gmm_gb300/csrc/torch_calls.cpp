@@ -17,6 +17,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Device.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -37,6 +38,10 @@ decltype(&mgemm_gmm_fp4) p_gmm = nullptr;
 // The tensor of an argument; nullptr for anything else (None among it).
 const at::Tensor *tensor(PyObject *o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 bool on_gpu(const at::Tensor *t, at::ScalarType type) { return t && t->is_cuda() && t->scalar_type() == type; }
+// the same on the device of another tensor
+bool beside(const at::Tensor *t, at::ScalarType type, const at::Tensor &other) {
+  return on_gpu(t, type) && t->get_device() == other.get_device();
+}
 
 mgemm_stream_t stream_of(const at::Tensor &t) {
   return reinterpret_cast<mgemm_stream_t>(c10::cuda::getCurrentCUDAStream(t.get_device()).stream());
@@ -128,7 +133,7 @@ PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *l = tensor(a[0]), *b = tensor(a[3]);
     const int type = logits_type(l);
     if (type >= 0 && l->requires_grad() && c10::GradMode::is_enabled()) Py_RETURN_NONE;  // (a differentiable call)
-    if (type < 0 || (a[3] != Py_None && !(on_gpu(b, at::kFloat) && b->numel() == l->size(1) && b->is_contiguous())))
+    if (type < 0 || (a[3] != Py_None && !(beside(b, at::kFloat, *l) && b->numel() == l->size(1) && b->is_contiguous())))
       Py_RETURN_NONE;
     bool bad = false;
     int64_t v[6];
@@ -160,7 +165,7 @@ PyObject *route_bwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     const at::Tensor *g = tensor(a[0]), *l = tensor(a[1]), *w = tensor(a[2]), *ids = tensor(a[3]);
     const int type = logits_type(l);
-    if (type < 0 || !on_gpu(g, at::kFloat) || !on_gpu(w, at::kFloat) || !on_gpu(ids, at::kInt)) Py_RETURN_NONE;
+    if (type < 0 || !beside(g, at::kFloat, *l) || !beside(w, at::kFloat, *l) || !beside(ids, at::kInt, *l)) Py_RETURN_NONE;
     if (ids->dim() != 2 || ids->size(0) != l->size(0) || g->sizes() != ids->sizes() || w->sizes() != ids->sizes() ||
         !g->is_contiguous() || !w->is_contiguous() || !ids->is_contiguous())
       Py_RETURN_NONE;
@@ -259,18 +264,20 @@ PyObject *dequantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
-// gmm(x, addresses, shape, format, group_sizes, grad enabled) -> bf16 [M, N], with a workspace of its own
+// gmm(x, addresses, shape, format, their device, group_sizes, grad enabled) -> bf16 [M, N], with a workspace of its own
 PyObject *gmm(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  if (n != 6 || !p_gmm) Py_RETURN_NONE;
+  if (n != 7 || !p_gmm) Py_RETURN_NONE;
   return guarded([&]() -> PyObject * {
-    const at::Tensor *x = tensor(a[0]), *g = tensor(a[4]);
+    const at::Tensor *x = tensor(a[0]), *g = tensor(a[5]);
     uintptr_t p[3];
     int64_t s[3];
     bool bad = false;
     const int64_t fmt = integer(a[3], bad);
-    if (bad || !addresses(a[1], p) || !shape3(a[2], s) || !on_gpu(x, at::kBFloat16) || !on_gpu(g, at::kLong)) Py_RETURN_NONE;
+    if (bad || !addresses(a[1], p) || !shape3(a[2], s) || !on_gpu(x, at::kBFloat16) ||
+        !beside(g, at::kLong, *x) || !THPDevice_Check(a[4]) || reinterpret_cast<THPDevice *>(a[4])->device != x->device())
+      Py_RETURN_NONE;
     const int64_t E = s[0], N = s[1], K = s[2], M = x->dim() == 2 ? x->size(0) : -1;
-    if (M < 0 || x->size(1) != K || (x->requires_grad() && a[5] == Py_True) || g->numel() != E || !g->is_contiguous())
+    if (M < 0 || x->size(1) != K || (x->requires_grad() && a[6] == Py_True) || g->numel() != E || !g->is_contiguous())
       Py_RETURN_NONE;
     const int64_t ld = x->stride(0);
     if (x->stride(1) != 1 || ld < K || ld % 8 || reinterpret_cast<uintptr_t>(x->data_ptr()) % 16) Py_RETURN_NONE;

@@ -125,7 +125,7 @@ def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
     if type(w) is not Fp4Tensor:
         raise B.MgemmError("gmm_fp4 takes an Fp4Tensor (see quantize_fp4)")
     if out is None and workspace is None:
-        r = B.calls().gmm(x, w._ptrs, w.shape, w.code, group_sizes, torch.is_grad_enabled())
+        r = B.calls().gmm(x, w._ptrs, w.shape, w.code, w.device, group_sizes, torch.is_grad_enabled())
         if r is not None:
             return B._check(r, "mgemm_gmm_fp4") if type(r) is int else r
     # the caller's buffers, or not the plain case: looked at, mended or refused here
@@ -139,6 +139,8 @@ def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise B.MgemmError("gmm_fp4: the workspace must be contiguous uint8")
     B._cuda(x, group_sizes, out, workspace)
+    if x.device != w.device:
+        raise B.MgemmError(f"gmm_fp4 takes operands of one device, not of {x.device} and {w.device}")
     M = x.shape[0]
     if x.stride(1) != 1 or x.stride(0) % 8 or x.stride(0) < K or x.data_ptr() % 16:
         x = x.clone(memory_format=torch.contiguous_format)

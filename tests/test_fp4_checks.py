@@ -59,3 +59,19 @@ def test_product_refuses_a_workspace_that_is_no_plain_bytes():
                 torch.zeros(need, dtype=torch.int8), torch.zeros(need, dtype=torch.float32)):
         with pytest.raises(B.MgemmError, match="workspace"):
             fp4.gmm_fp4(x, w, gs, workspace=bad)
+
+
+class OnDevice:
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+
+def test_binding_takes_tensors_of_one_device():
+    B._cuda(OnDevice(0), None, OnDevice(0))
+    B._cuda(OnDevice(1), OnDevice(1))
+    for bad in ((OnDevice(0), OnDevice(1)), (OnDevice(1), None, OnDevice(0)), (OnDevice(0), OnDevice(-1))):
+        with pytest.raises(B.MgemmError, match="device"):
+            B._cuda(*bad)

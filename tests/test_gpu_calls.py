@@ -1,5 +1,5 @@
 """GPU checks of how the routing and 4-bit calls take their arguments: layouts of
-single rows and of rows that start anywhere, tensors that require a gradient, and other threads."""
+single rows and of rows that start anywhere, tensors that require a gradient, other threads and other devices."""
 
 import threading
 import time
@@ -129,3 +129,15 @@ def test_other_threads_run_while_a_call_waits_for_the_launch_queue():
     torch.cuda.synchronize()
     assert took > 0.25, "the queue did not fill: the test says nothing"
     assert gaps[0] < took / 2, f"another thread stood still for {gaps[0]:.2f} of {took:.2f} s"
+
+
+def test_operands_of_several_devices_are_refused():
+    # (the tensors lie on this device; what is compared is the device that the 4-bit tensor says it lies on)
+    w = mg().quantize_fp4(torch.randn(2, 64, 64, device=DEV).to(BF), "nvfp4")
+    x, gs = torch.randn(8, 64, device=DEV).to(BF), torch.tensor([4, 4], device=DEV)
+    mg().gmm_fp4(x, w, gs)
+    w.device = torch.device("cuda", 1)
+    out = torch.empty(8, 64, dtype=BF, device=DEV)
+    for bad in (lambda: mg().gmm_fp4(x, w, gs), lambda: mg().gmm_fp4(x, w, gs, out=out)):
+        with pytest.raises(mg().binding.MgemmError, match="device"):
+            bad()
