@@ -132,6 +132,9 @@ def route_experts_backward(grad_weights, logits, topk_weights, topk_ids, scoring
             topk_ids.dtype != torch.int32 or topk_weights.dtype != torch.float32 or \
             not topk_weights.is_contiguous() or not topk_ids.is_contiguous():
         raise B.MgemmError("route_experts_backward takes route_experts' weights and ids and a gradient of their shape")
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != logits.shape[0]:
+        raise B.MgemmError(f"route_experts_backward takes ids [T, topk] of the logits' tokens, not {tuple(topk_ids.shape)} "
+                           f"for {logits.shape[0]}")
     grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     if grad_weights.dtype != torch.float32 or not grad_weights.is_contiguous():
         grad_weights = grad_weights.to(torch.float32).contiguous()

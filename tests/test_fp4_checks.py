@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from mixture_experts_grouped_gmm_gb300 import binding as B
-from mixture_experts_grouped_gmm_gb300 import fp4, moe
+from mixture_experts_grouped_gmm_gb300 import build, fp4, moe
 
 BF = torch.bfloat16
 
@@ -75,3 +75,11 @@ def test_binding_takes_tensors_of_one_device():
     for bad in ((OnDevice(0), OnDevice(1)), (OnDevice(1), None, OnDevice(0)), (OnDevice(0), OnDevice(-1))):
         with pytest.raises(B.MgemmError, match="device"):
             B._cuda(*bad)
+
+
+def test_routing_gradient_refuses_ids_of_other_tokens():
+    build.build()  # (the extension, which looks at the arguments first)
+    logits, wts, ids = torch.zeros(6, 8), torch.zeros(4, 2), torch.zeros(4, 2, dtype=torch.int32)
+    for w, i in ((wts, ids), (wts.view(-1), ids.view(-1)), (torch.zeros(7, 2), torch.zeros(7, 2, dtype=torch.int32))):
+        with pytest.raises(B.MgemmError, match="of the logits' tokens"):
+            moe.route_experts_backward(w, logits, w, i)
