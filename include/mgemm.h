@@ -772,6 +772,14 @@ int mgemm_fwd_fp4(const void *args, int fmt, const uint8_t *x, const uint8_t *sx
                   const float *row_weight, int64_t M, int K, int N, int E, mgemm_stream_t stream);
 
 /*
+ * mgemm_fp4_form -- how mgemm_fwd_fp4 and mgemm_gmm_fp4 tile a product on `sms` SMs
+ * (0: those of the current device): returns the columns of a tile and sets *pairs
+ * where pairs of CTAs compute 256 rows of them (else each its 128).  Host only; for
+ * tests and measurements.
+ */
+int mgemm_fp4_form(int fmt, int64_t M, int K, int N, int E, int sms, int *pairs);
+
+/*
  * mgemm_gmm_fp4 -- mgemm_fill_args, mgemm_quant_fp4_rows and mgemm_fwd_fp4 in one
  * call: out[rows of group e] = x[rows of group e] . w[e]^T for bf16 token rows.
  *   group_sizes  int64 [E], device, summing to M

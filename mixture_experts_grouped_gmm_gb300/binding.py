@@ -144,6 +144,8 @@ _SIGS = {
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                      ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "mgemm_fp4_form": (ctypes.c_int, [ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                      ctypes.c_int, ctypes.POINTER(ctypes.c_int)]),
     "mgemm_gmm_fp4_workspace_bytes": (ctypes.c_int64, [ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int]),
     "mgemm_gmm_fp4": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64,
                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
@@ -542,6 +544,14 @@ def mgemm_fwd_fp4(args, fmt, x, sx, rx, w, sw, rw, out, M, K, N, E, row_map=None
     _check(lib().mgemm_fwd_fp4(_p(args), int(fmt), _p(x), _p(sx), _p(rx), _p(w), _p(sw), _p(rw), _p(out), _p(row_map),
                                int(map_limit), _p(row_weight), int(M), int(K), int(N), int(E), _stream(out)),
            "mgemm_fwd_fp4")
+
+
+def mgemm_fp4_form(fmt, M, K, N, E, sms=0):
+    """How the product is tiled on that many SMs (0: the device's): (columns of a tile, CTA pairs or not)."""
+    pairs = ctypes.c_int()
+    bn = lib().mgemm_fp4_form(int(fmt), int(M), int(K), int(N), int(E), int(sms), ctypes.byref(pairs))
+    _check(min(bn, 0), "mgemm_fp4_form")
+    return bn, bool(pairs.value)
 
 
 def mgemm_gmm_fp4_workspace_bytes(fmt, M, K, E):

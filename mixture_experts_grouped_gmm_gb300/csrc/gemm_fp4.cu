@@ -37,7 +37,7 @@
 // TMEM: one accumulator of 256 columns or two narrower ones, then as many slots
 // of scales as fit (two to sixteen).  A slot is rewritten once the MMAs that read it
 // have completed: the stage's empty barrier says so.
-// PAIR (most groups of 256 rows and more, some of 128; see launch_fp4): a cluster of two CTAs computes 256 rows by
+// PAIR (many groups of 256 rows and more, some of 128; see fp4_form): a cluster of two CTAs computes 256 rows by
 // bn columns with cta_group::2 MMAs of the even CTA.  Each CTA copies its 128
 // rows of A, half of B's columns and the scales of its rows and of all columns;
 // the odd CTA's copies complete on the even CTA's barriers, and commits free a
@@ -828,13 +828,17 @@ double tiles_of(double rows, int h) {
   return (sum(hi) - sum(lo)) / (hi - lo);
 }
 
+// How a product is tiled: columns per tile, and whether CTA pairs compute 256 rows of them.
+struct F4Form {
+  int bn;
+  bool pairs;
+};
 template <int FMT>
-int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, const Fp4Params &p, int64_t M,
-               int sms, cudaStream_t s) {
-  const int64_t groups = M < p.E ? M : p.E;
+F4Form fp4_form(int64_t M, int K, int N, int E, int sms) {
+  const int64_t groups = M < E ? M : E;
   const double rows = (double)M / groups;
   auto rounds = [&](double row_tiles, int bn, int places) {
-    return ceil(groups * row_tiles * ((p.N + bn - 1) / bn) / places);
+    return ceil(groups * row_tiles * ((N + bn - 1) / bn) / places);
   };
   // Columns per tile: the fewest rounds of tiles over the SMs, weighted by the bytes of a stage (A's rows, the
   // columns and their scales); wider at equal cost (fewer reads of A).  1024 rows in 8 groups of about 128 are 12
@@ -854,17 +858,24 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
   // pairs, 35.8, 36.4 and 44.5 not; 5 of 1000 x 8192: 17.4, 17.9 and 18.4 in pairs, 15.7, 16.0 and 16.2 not.
   bool pairs = false;
   if (rows >= 128) {
-    const double kb2 = (p.K + 255) / 256 * 2;
-    const int pair_bn = p.N > 128 ? 256 : 128;
+    const double kb2 = (K + 255) / 256 * 2;
+    const int pair_bn = N > 128 ? 256 : 128;
     const double one = rounds(tiles_of(rows, 128), bn, sms) * F4Cfg<FMT, false>::stage_bytes(128, bn);
     const double two = rounds(tiles_of(rows, 256), pair_bn, sms / 2) * F4Cfg<FMT, true>::stage_bytes(128, pair_bn);
     pairs = kb2 * two + (1 << 18) < kb2 * one;
   }
-  if (pairs)
-    return p.N > 128 ? launch_fp4<FMT, true, 2>(x, sx, w, sw, p, M, 256, sms, s)
-                     : launch_fp4<FMT, true, 1>(x, sx, w, sw, p, M, 128, sms, s);
-  return bn > 128 ? launch_fp4<FMT, false, 2>(x, sx, w, sw, p, M, bn, sms, s)
-                  : launch_fp4<FMT, false, 1>(x, sx, w, sw, p, M, bn, sms, s);
+  return {pairs ? N > 128 ? 256 : 128 : bn, pairs};
+}
+
+template <int FMT>
+int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint8_t *sw, const Fp4Params &p, int64_t M,
+               int sms, cudaStream_t s) {
+  const F4Form form = fp4_form<FMT>(M, p.K, p.N, p.E, sms);
+  if (form.pairs)
+    return form.bn > 128 ? launch_fp4<FMT, true, 2>(x, sx, w, sw, p, M, form.bn, sms, s)
+                         : launch_fp4<FMT, true, 1>(x, sx, w, sw, p, M, form.bn, sms, s);
+  return form.bn > 128 ? launch_fp4<FMT, false, 2>(x, sx, w, sw, p, M, form.bn, sms, s)
+                       : launch_fp4<FMT, false, 1>(x, sx, w, sw, p, M, form.bn, sms, s);
 }
 
 bool a16(const void *p) { return ((uintptr_t)p & 15) == 0; }
@@ -931,6 +942,16 @@ extern "C" int mgemm_fwd_fp4(const void *args, int fmt, const uint8_t *x, const 
   p.N = N;
   p.E = E;
   return fwd_fp4(fmt, x, sx, w, sw, p, M, (cudaStream_t)stream);
+}
+
+extern "C" int mgemm_fp4_form(int fmt, int64_t M, int K, int N, int E, int sms, int *pairs) {
+  if (!fp4_format(fmt) || M < 1 || M >= (int64_t(1) << 31) || K <= 0 || N <= 0 || E < 1 || !pairs) return MGEMM_EINVAL;
+  if (E > MGEMM_MAX_EXPERTS) return MGEMM_ETOOMANY;
+  if (sms <= 0) sms = sm_count_cached();
+  if (sms <= 0) return MGEMM_ECUDA;
+  const F4Form form = fmt == MGEMM_NVFP4 ? fp4_form<MGEMM_NVFP4>(M, K, N, E, sms) : fp4_form<MGEMM_MXFP4>(M, K, N, E, sms);
+  *pairs = form.pairs;
+  return form.bn;
 }
 
 extern "C" int64_t mgemm_gmm_fp4_workspace_bytes(int fmt, int64_t M, int K, int E) {
