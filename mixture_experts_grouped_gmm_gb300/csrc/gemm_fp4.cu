@@ -79,7 +79,12 @@ struct Fp4Params {
 
 constexpr int kF4Threads = 384;
 constexpr int kF4EpiWarps = 8;
-constexpr int kF4Regs = 168;  // registers a thread at launch
+// Registers a thread at launch, as ptxas gives them to kF4Threads threads (a build may say otherwise to test the
+// refusal of any other count: see FEW_REGS).
+#ifndef MGEMM_F4_REGS
+#define MGEMM_F4_REGS 168
+#endif
+constexpr int kF4Regs = MGEMM_F4_REGS;
 constexpr int kF4MaxStages = 20;
 constexpr int kF4MaxSlots = 16;  // slots of scales in tensor memory
 constexpr int kF4Groups = 128;  // active groups whose places are kept in shared memory
@@ -807,7 +812,10 @@ int launch_fp4(const uint8_t *x, const uint8_t *sx, const uint8_t *w, const uint
     cudaFuncAttributes attr;
     rc = cuda_rc(cudaFuncGetAttributes(&attr, fp4_gemm_kernel<FMT, PAIR, NT>), "cudaFuncGetAttributes");
     if (rc) return rc;
-    if (attr.numRegs != kF4Regs) return MGEMM_ECUDA;  // see FEW_REGS
+    if (attr.numRegs != kF4Regs) {  // see FEW_REGS
+      note_error("mgemm_fwd_fp4: its kernel's registers a thread are not those its warps share out", attr.numRegs);
+      return MGEMM_ECUDA;
+    }
     attr_done[dev] = true;
   }
   const int64_t groups = M < E ? M : E;
