@@ -84,6 +84,14 @@ class Fp4Tensor:
             self._parts = (base[:n].view(E, N, K // 2), base[o:o + s], rows)
         return self._parts[i]
 
+    # A copy, or a tensor that is loaded, has its own addresses.  (The parts are copied: of one allocation, they
+    # would be views of several types of it, which torch does not save.)
+    def __copy__(self):
+        return Fp4Tensor(self.codes, self.scales, self.row_scale, self.fmt)
+
+    def __reduce__(self):
+        return Fp4Tensor, (*(None if t is None else t.clone() for t in (self.codes, self.scales, self.row_scale)), self.fmt)
+
     codes = property(lambda self: self._part(0))
     scales = property(lambda self: self._part(1))
     row_scale = property(lambda self: self._part(2))

@@ -1,6 +1,8 @@
 """GPU checks of how the routing and 4-bit calls take their arguments: layouts of
-single rows and of rows that start anywhere, tensors that require a gradient, other threads and other devices."""
+single rows and of rows that start anywhere, tensors that require a gradient, other
+threads, other devices, and copies of 4-bit tensors."""
 
+import copy
 import threading
 import time
 
@@ -141,3 +143,17 @@ def test_operands_of_several_devices_are_refused():
     for bad in (lambda: mg().gmm_fp4(x, w, gs), lambda: mg().gmm_fp4(x, w, gs, out=out)):
         with pytest.raises(mg().binding.MgemmError, match="device"):
             bad()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_copies_of_4bit_tensors_lie_where_their_parts_do(fmt, tmp_path):
+    q = mg().quantize_fp4(torch.randn(2, 40, 96, device=DEV).to(BF), fmt)
+    given = mg().Fp4Tensor(q.codes.clone(), q.scales.clone(), None if q.row_scale is None else q.row_scale.clone(), fmt)
+    for t in (q, given):
+        torch.save(t, tmp_path / "t.pt")
+        for c in (copy.copy(t), copy.deepcopy(t), torch.load(tmp_path / "t.pt", weights_only=False)):
+            # (what a kernel would be given: looked at before any launch)
+            assert c._ptrs == (c.codes.data_ptr(), c.scales.data_ptr(), c.row_scale.data_ptr() if fmt == "nvfp4" else None)
+            assert (c.fmt, c.code, c.shape, c.device) == (t.fmt, t.code, t.shape, t.device)
+            assert torch.equal(c.codes, t.codes) and torch.equal(mg().dequantize_fp4(c), mg().dequantize_fp4(t))
+    assert copy.deepcopy(q).codes.data_ptr() != q.codes.data_ptr()
