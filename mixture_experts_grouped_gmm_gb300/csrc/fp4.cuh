@@ -27,7 +27,7 @@ __device__ __forceinline__ int64_t fp4_sf_offset(int64_t r, int j, int W) {
 // even, saturating), the first in the low nibble.  The products go through f16
 // on the way.  That settles the ties: x and 1 / r have 8 and 4 significant bits,
 // so a quotient that is no midpoint of two e2m1 values is at least 2^-9 of
-// itself away from one, f16 moves it by at most 2^-12, and one that is a midpoint,
+// itself away from one, f16 moves it by at most 2^-11, and one that is a midpoint,
 // off by r's and the product's rounding (2^-22), comes back to it.
 __device__ __forceinline__ uint32_t fp4_codes8(const uint32_t *x, uint64_t r2) {
   uint32_t h[4];
