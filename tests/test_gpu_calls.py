@@ -157,3 +157,26 @@ def test_copies_of_4bit_tensors_lie_where_their_parts_do(fmt, tmp_path):
             assert (c.fmt, c.code, c.shape, c.device) == (t.fmt, t.code, t.shape, t.device)
             assert torch.equal(c.codes, t.codes) and torch.equal(mg().dequantize_fp4(c), mg().dequantize_fp4(t))
     assert copy.deepcopy(q).codes.data_ptr() != q.codes.data_ptr()
+
+
+def test_an_allocation_that_fails_raises_with_and_without_other_threads():
+    T = 1 << 21
+    l = torch.zeros(T, 8, device=DEV)
+    mg().moe.route_experts(l[:4], 2)
+    torch.cuda.synchronize()
+    stop = threading.Event()
+    t = threading.Thread(target=stop.wait)
+    torch.cuda.empty_cache()
+    torch.cuda.set_per_process_memory_fraction(1e-6)  # (the allocator refuses: nothing is asked of the device)
+    try:
+        for _ in range(2):
+            with pytest.raises(torch.OutOfMemoryError):
+                mg().moe.route_experts(l, 8)
+            if not t.is_alive():
+                t.start()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+        stop.set()
+        t.join()
+    w, ids = mg().moe.route_experts(l, 8)
+    assert ids[T - 1].tolist() == list(range(8)) and torch.allclose(w, torch.full_like(w, 0.125))
