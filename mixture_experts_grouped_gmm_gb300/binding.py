@@ -617,7 +617,7 @@ def mgemm_balance_bwd(grad_loss, logits, slopes, scoring, grad_logits, offsets=N
     _check(lib().mgemm_balance_bwd(_p(grad_loss), _p(logits), int(logits.dtype == torch.bfloat16), logits.stride(0),
                                    _p(slopes), _p(offsets), 1 if offsets is None else offsets.numel() - 1, _p(mask), T, E,
                                    int(scoring), _p(grad_logits), grad_logits.stride(0), _stream(logits)),
-           "mgemm_balance_bwd", "mgemm_gmm_int4")
+           "mgemm_balance_bwd")
 
 
 def mgemm_quant_int4_groups(inp, group, codes, scales, zeros=None):
