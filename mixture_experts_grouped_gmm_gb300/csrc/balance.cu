@@ -5,6 +5,7 @@
 //   L_s  = sum_e (E c_se / (k n_s)) (sum_t p_te / n_s)   over a sequence's n_s tokens
 //   L    = scale times the mean of L_s over the sequences that have tokens
 //   dL/dl_te = p_te (a_se - sum_j p_tj a_sj) [sigmoid: times 1 - s_te],  a_se = scale' E c_se / (k n_s^2)
+//   (1 - s = e s with e = exp(-l): the difference itself has no bits left for large logits)
 //
 // Bound by instruction issue (147 warp instructions a row of 256 experts forward, 231 for the gradient: 65536 x 256
 // fp32 in 24 sequences 18.6 + 9.4 + 22 us, whose bytes take 10 + 0 + 10 and 10); small calls by their launches.  LPR
@@ -480,12 +481,22 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalanceBwdP
     for (int j = 0; j < V; ++j) v[j] = ahead[j];
     if constexpr (V <= 8)
       if (i + 1 < p.R) load(t + 1);
-    scores<LPR, V, SIGMOID>(v);
-    float sum = 0.f, dot = 0.f, f;
+    float sum = 0.f, dot = 0.f;
+    if constexpr (SIGMOID) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum += v[j], dot = fmaf(v[j], a[j], dot);
+      for (int j = 0; j < V; ++j) {
+        const float e = exp2_approx(v[j] * -kLog2e), s = rcp_approx(1.f + e);
+        sum += s, dot = fmaf(s, a[j], dot);
+        v[j] = s * fminf(e * s, 1.f);  // s (1 - s); (e may be infinite and s 0: their product, a NaN, becomes 1)
+      }
+    } else {
+      scores<LPR, V, false>(v);
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum += v[j], dot = fmaf(v[j], a[j], dot);
+    }
     sum = lanes_sum<LPR>(sum);
     dot = lanes_sum<LPR>(dot);
+    float f;
     const bool small = by_sum<V, SIGMOID>(sum, v, f);
     if (small) dot *= kUp;
     if (live) {
@@ -496,8 +507,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalanceBwdP
       } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = (a[j] - mean) * (v[j] * scale);
-          v[j] = SIGMOID ? fmaf(-d, small ? 0.f : v[j], d) : d;
+          v[j] = (a[j] - mean) * (v[j] * scale);
         }
       }
       store_row<LPR, V, VEC>((L *)p.grad + t * p.ld_grad, lane, E, v);

@@ -4,7 +4,8 @@ Not on the source pages.  Over the n counted tokens of a sequence, c_e of whose 
 expert e: L_s = sum_e (E c_e / (k n)) (sum_t p_te / n), p a token's softmax or its sigmoids
 over their sum, 0 for experts that are off; the loss is scale times the mean of L_s over the
 sequences with tokens.  The counts are constant in the gradient:
-  dL_s/dp_te = a_e = E c_e / (k n^2),  dL/dl = p (a - sum p a)  [sigmoid: times 1 - s].
+  dL_s/dp_te = a_e = E c_e / (k n^2),  dL/dl = p (a - sum p a)  [sigmoid: times 1 - s,
+which is 1 / (1 + e^l)].
 Float64 numpy, loops over sequences and tokens.
 """
 
@@ -24,6 +25,13 @@ def scores(l, scoring):
         s = np.where(on, np.exp(l - (np.max(l[on]) if on.any() else 0.0)), 0.0)
     total = s.sum()
     return (s / total if total != 0 else np.zeros_like(s)), s
+
+
+def score_rest(l, scoring):
+    """ds/dl / s of one token's logits: 1 - s for sigmoids without cancellation, else 1."""
+    l = np.asarray(l, dtype=np.float64)
+    with np.errstate(over="ignore"):
+        return 1.0 / (1.0 + np.exp(l)) if scoring == "sigmoid" else np.ones_like(l)
 
 
 def _tokens(T, offsets, mask):
@@ -67,8 +75,7 @@ def balance_grad(grad_loss, logits, ids, scoring, scale=1.0, offsets=None, mask=
             continue
         a = grad_loss * scale / present * E * counts(ids, E, rows) / (k * len(rows) ** 2)
         for t in rows:
-            p, s = scores(logits[t], scoring)
-            rest = 1.0 - s if scoring == "sigmoid" else 1.0
-            grad[t] = p * (a - np.sum(p * a)) * rest
+            p, _ = scores(logits[t], scoring)
+            grad[t] = p * (a - np.sum(p * a)) * score_rest(logits[t], scoring)
             size[t] = p * (np.abs(a) + np.sum(p * np.abs(a)))
     return grad, size

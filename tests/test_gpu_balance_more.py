@@ -1,9 +1,20 @@
 """GPU checks of the balance loss's gradient where a call is not the plain one: layouts that are
-mended before the launch, against the plain call bit for bit."""
+mended before the launch, against the plain call bit for bit; and logits far from 0, against
+oracle.balance (float64).
+
+The bound for sigmoids of logits up to L in magnitude, in units of u = 2^-24, relative.  e = 2^x of
+x = -l log2 e: the product's rounding and the constant's are off by L u each, 2^x by 4 u; s = 1 / (1 + e)
+adds 1 + 4: 2 L + 9.  p = s / sum: the sum is a mean of its terms' errors and at most 37 steps, its
+reciprocal 4, the product 1: 4 L + 60.  The mean of the slopes a over p: the same and 42 steps more, the
+difference a - mean 1, a itself 5: 4 L + 108 of |a| + sum p |a|.  1 - s = e s: 2 L + 10.  Four products.
+Together 10 L + 182 of p (|a| + sum p |a|) (1 - s); bf16 adds 2^-8 of the value.  The loss: 4 L + 60 for
+p, and at most 256 steps over the rows' sums here and 15 to the loss."""
 
 import numpy as np
 import pytest
 import torch
+
+from oracle import balance as ob
 
 pytestmark = pytest.mark.gpu
 DEV, BF, F32 = "cuda", torch.bfloat16, torch.float32
@@ -67,3 +78,35 @@ def test_gradient_of_rows_that_are_one(moe):
     moe.balance_loss(leaf.expand(30, 16), ids)[0].backward()
     # (30 equal terms: 29 sums of at most half a step each)
     assert torch.allclose(leaf.grad, 30 * got[:1], rtol=30 * 2.0 ** -24, atol=0)
+
+
+def near(moe, logits, ids, scoring="sigmoid", grad=1.0, offsets=None, mask=None):
+    """Loss and gradient within the bound above; the gradient."""
+    l64, i64 = logits.double().cpu().numpy(), ids.cpu().numpy()
+    dev = lambda a, t: None if a is None else torch.as_tensor(np.asarray(a), dtype=t, device=DEV)  # noqa: E731
+    o, m = dev(offsets, torch.int64), dev(mask, torch.bool)
+    L = float(np.max(np.abs(l64), initial=0.0, where=np.isfinite(l64)))
+    loss, counts, slopes = moe.balance_loss_forward(logits, ids, scoring, 1.0, o, m)
+    want, want_counts = ob.balance(l64, i64, scoring, 1.0, offsets, mask)
+    assert abs(float(loss) - want) <= (4 * L + 331) * 2.0 ** -24 * abs(want)
+    assert np.array_equal(counts.cpu().numpy().reshape(want_counts.shape), want_counts)
+    got = moe.balance_loss_backward(torch.tensor(grad, device=DEV), logits, slopes, scoring, o, m)
+    ref, size = ob.balance_grad(grad, l64, i64, scoring, 1.0, offsets, mask)
+    size = size * ob.score_rest(l64, scoring)
+    tol = (10 * L + 182) * 2.0 ** -24 * size + (2.0 ** -8 * np.abs(ref) if logits.dtype == BF else 0)
+    g64 = got.double().cpu().numpy()
+    assert np.all(np.abs(g64 - ref) <= tol + 2.0 ** -126)  # (less than a normal number may be 0)
+    return g64, ref
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,E,k", [(60, 24, 3), (50, 60, 4), (40, 100, 6), (30, 256, 8), (30, 513, 4), (20, 1024, 8)])
+def test_sigmoids_of_large_logits(moe, T, E, k, dtype):
+    """1 - s is as exact at 80 as at 0: the gradients there are small, and not 0."""
+    for center in (0.0, 5.0, 10.0, 14.0, 17.0, 25.0, 40.0, 60.0, 78.0, -10.0, -40.0):
+        logits, ids = inputs(T, E, k, int(abs(center)), dtype)
+        got, ref = near(moe, logits.clamp(-6, 6) + center, ids, grad=2.0 ** 60)
+        assert np.all((got != 0) == (ref != 0))
+    near(moe, (30 * logits).clamp(-80, 80), ids, grad=2.0 ** 60)  # all of it in one row
+    logits[:, 3] = float("inf")
+    near(moe, logits, ids)
