@@ -165,20 +165,19 @@ __device__ __forceinline__ void scores(float (&v)[V]) {
   }
 }
 
-// The reciprocal of a row's sum of scores, 0 where every expert is off.  Sigmoids can be
-// so small that it would pass float32: they are scaled first, and true is returned (1 - s
-// is 1 in such a row).
-constexpr float kSmallSum = 0x1p-100f, kUp = 0x1p100f;
-template <int V, bool SIGMOID>
-__device__ __forceinline__ bool by_sum(float sum, float (&v)[V], float &f) {
-  const bool small = SIGMOID && sum < kSmallSum;
-  if (small) {
+// The reciprocal of a row's sum of scores, 0 where every expert is off.
+__device__ __forceinline__ float by_sum(float sum) { return sum == 0.f ? 0.f : rcp_approx(sum); }
+
+// Sigmoids can be so small that the reciprocal of their sum, or its product with the loss's gradient, passes float32,
+// and the smallest of them or their products with the slopes its normal numbers.  Such a row (its sum is not 0) is read
+// again: its sigmoids are exp(l), here times 2^83 (between 2^-43 and 2^43 for the largest), and 1 - s is 1.
+constexpr float kSmallSum = 0x1p-40f;
+template <typename L, int LPR, int V, bool VEC>
+__device__ __forceinline__ void small_scores(const L *row, int lane, int E, bool small, float (&v)[V]) {
+  float l[V];
+  load_row<LPR, V, VEC>(row, lane, E, l);
 #pragma unroll
-    for (int j = 0; j < V; ++j) v[j] *= kUp;
-    sum *= kUp;
-  }
-  f = sum == 0.f ? 0.f : rcp_approx(sum);
-  return small;
+  for (int j = 0; j < V; ++j) v[j] = small ? exp2_approx(fmaf(l[j], kLog2e, 83.f)) : v[j];
 }
 
 __device__ __forceinline__ int64_t bound_of(const BalanceParams &p, int64_t s) {
@@ -352,8 +351,17 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(const BalanceParams p
 #pragma unroll
       for (int j = 0; j < V; ++j) sum += v[j];
       sum = lanes_sum<LPR>(sum);
-      float f;
-      by_sum<V, SIGMOID>(sum, v, f);
+      if constexpr (SIGMOID) {
+        const bool small = sum > 0.f && sum < kSmallSum;
+        if (__any_sync(kFull, small)) {
+          small_scores<L, LPR, V, VEC>((const L *)p.logits + (t < last ? t : first) * p.ld, lane, E, small, v);
+          sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < V; ++j) sum += v[j];
+          sum = lanes_sum<LPR>(sum);
+        }
+      }
+      const float f = by_sum(sum);
       if (live) {
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] = fmaf(v[j], f, acc[j]);
@@ -496,9 +504,19 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalanceBwdP
     }
     sum = lanes_sum<LPR>(sum);
     dot = lanes_sum<LPR>(dot);
-    float f;
-    const bool small = by_sum<V, SIGMOID>(sum, v, f);
-    if (small) dot *= kUp;
+    if constexpr (SIGMOID) {
+      const bool small = sum > 0.f && sum < kSmallSum;
+      if (__any_sync(kFull, small)) {
+        small_scores<L, LPR, V, VEC>((const L *)p.logits + (live ? t : 0) * p.ld, lane, E, small, v);
+        float sum2 = 0.f, dot2 = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum2 += v[j], dot2 = fmaf(v[j], a[j], dot2);
+        sum2 = lanes_sum<LPR>(sum2);
+        dot2 = lanes_sum<LPR>(dot2);
+        if (small) sum = sum2, dot = dot2;
+      }
+    }
+    const float f = by_sum(sum);
     if (live) {
       const float mean = dot * f, scale = f * factor;
       if (!counts) {

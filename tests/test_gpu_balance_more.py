@@ -110,3 +110,33 @@ def test_sigmoids_of_large_logits(moe, T, E, k, dtype):
     near(moe, (30 * logits).clamp(-80, 80), ids, grad=2.0 ** 60)  # all of it in one row
     logits[:, 3] = float("inf")
     near(moe, logits, ids)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,E,k", [(40, 64, 4), (30, 24, 3), (20, 700, 8)])
+def test_sigmoids_near_the_smallest_numbers(moe, T, E, k, dtype):
+    """Rows whose sigmoids are below 2^-100, some below 2^-126, beside others in the same warp; exp(l) times a power of
+    two is at most as far off as the sigmoid in the bound above."""
+    logits, ids = inputs(T, E, k, 5, dtype)
+    for center in (-72.0, -84.0, -86.2):
+        got, ref = near(moe, logits.clamp(-1.2, 1.2) + center, ids, grad=2.0 ** 40)
+        assert np.all((got != 0) == (ref != 0))
+    mixed = logits.clamp(-1.2, 1.2) - 86.2
+    mixed[::3] = logits[::3]
+    mixed[1, ::2] = -float("inf")
+    mixed[2, 1:] = torch.finfo(dtype).min
+    near(moe, mixed, ids, grad=2.0 ** 40)
+
+
+def test_small_sigmoids_of_many_tokens(moe):
+    """Slopes of 1 / n: their products with the sigmoids are no normal numbers."""
+    logits, ids = inputs(40000, 64, 2, 6)
+    far = logits.clamp(-1.2, 1.2) - 86.2
+    _, _, slopes = moe.balance_loss_forward(far, ids, "sigmoid")
+    got = moe.balance_loss_backward(torch.tensor(2.0 ** 40, device=DEV), far, slopes, "sigmoid").double().cpu().numpy()
+    # (the first rows: all of them have the slopes of the whole batch)
+    l64, a = far[:50].double().cpu().numpy(), slopes[:-1].double().cpu().numpy() * 2.0 ** 40
+    for t in range(50):
+        p, _ = ob.scores(l64[t], "sigmoid")
+        tol = (10 * 88 + 182) * 2.0 ** -24 * p * (a + np.sum(p * a))
+        assert np.all(np.abs(got[t] - p * (a - np.sum(p * a))) <= tol)
