@@ -221,7 +221,10 @@ def balance_loss(logits, topk_ids, scoring="softmax", scale=1.0, offsets=None, m
 
 
 def balance_loss_forward(logits, topk_ids, scoring="softmax", scale=1.0, offsets=None, mask=None):
-    """balance_loss and what its backward pass reads: (loss, counts, slopes float32 [S * E + 1])."""
+    """balance_loss and what its backward pass reads: (loss, counts, slopes float32 [S * E + 1]).  As balance_loss, the
+    loss has a gradient where the logits require one."""
+    if logits.requires_grad and torch.is_grad_enabled():
+        return BalanceLoss.apply(logits, topk_ids, scoring, scale, offsets, mask, True)
     return _balance(logits, topk_ids, scoring, scale, offsets, mask, True)
 
 
@@ -245,21 +248,25 @@ def balance_loss_backward(grad_loss, logits, slopes, scoring="softmax", offsets=
 
 class BalanceLoss(torch.autograd.Function):
     """balance_loss as an autograd op: ``BalanceLoss.apply(logits, topk_ids, scoring, scale,
-    offsets, mask)``.  The counts have no gradient."""
+    offsets, mask)``; with a further True the slopes come too.  Neither they nor the counts
+    have a gradient."""
 
     @staticmethod
-    def forward(ctx, logits, topk_ids, scoring="softmax", scale=1.0, offsets=None, mask=None):
+    def forward(ctx, logits, topk_ids, scoring="softmax", scale=1.0, offsets=None, mask=None, with_slopes=False):
         loss, counts, slopes = _balance(logits, topk_ids, scoring, scale, offsets, mask, True)
         ctx.save_for_backward(logits, slopes, offsets, mask)
         ctx.scoring = scoring
+        if with_slopes:
+            ctx.mark_non_differentiable(counts, slopes)
+            return loss, counts, slopes
         ctx.mark_non_differentiable(counts)
         return loss, counts
 
     @staticmethod
     @once_differentiable
-    def backward(ctx, grad_loss, _grad_counts):
+    def backward(ctx, grad_loss, *_):
         logits, slopes, offsets, mask = ctx.saved_tensors
-        return (balance_loss_backward(grad_loss, logits, slopes, ctx.scoring, offsets, mask),) + (None,) * 5
+        return (balance_loss_backward(grad_loss, logits, slopes, ctx.scoring, offsets, mask),) + (None,) * 6
 
 
 def route_align(gating_output, topk, renormalize, block=BLOCK):

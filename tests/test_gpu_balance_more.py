@@ -140,3 +140,21 @@ def test_small_sigmoids_of_many_tokens(moe):
         p, _ = ob.scores(l64[t], "sigmoid")
         tol = (10 * 88 + 182) * 2.0 ** -24 * p * (a + np.sum(p * a))
         assert np.all(np.abs(got[t] - p * (a - np.sum(p * a))) <= tol)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_explicit_form_keeps_the_gradient(moe, scoring):
+    """balance_loss_forward's loss has balance_loss's gradient where the logits require one."""
+    logits, ids = inputs(60, 20, 3, 8)
+    a, b = logits.clone().requires_grad_(), logits.clone().requires_grad_()
+    (5 * moe.balance_loss(a, ids, scoring, 0.5)[0]).backward()
+    loss, counts, slopes = moe.balance_loss_forward(b, ids, scoring, 0.5)
+    assert loss.requires_grad and not counts.requires_grad and not slopes.requires_grad
+    (5 * loss).backward()
+    assert torch.equal(a.grad, b.grad) and a.grad.any()
+    assert torch.equal(b.grad, moe.balance_loss_backward(torch.tensor(5.0, device=DEV), logits, slopes, scoring))
+    for no_grad in (True, False):
+        with torch.set_grad_enabled(not no_grad):
+            l = b if no_grad else b.detach()
+            again = moe.balance_loss_forward(l, ids, scoring, 0.5)
+            assert not again[0].requires_grad and torch.equal(again[0], loss.detach())
