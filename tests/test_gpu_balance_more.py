@@ -158,3 +158,21 @@ def test_explicit_form_keeps_the_gradient(moe, scoring):
             l = b if no_grad else b.detach()
             again = moe.balance_loss_forward(l, ids, scoring, 0.5)
             assert not again[0].requires_grad and torch.equal(again[0], loss.detach())
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k", [(7, 8, 2), (64, 64, 6), (700, 129, 8), (2600, 24, 2)])
+def test_masks_that_empty_sequences(moe, scoring, T, E, k):
+    """No row of any sequence, or none of some: their slopes are 0, and the mean leaves them out."""
+    logits, ids = inputs(T, E, k, 9)
+    cuts = [0, T // 5, T // 5, T // 2, T - 1, T]
+    for offsets in (cuts, [T // 2, T // 2 + 1, T], [0, 0, 0], [0, 0, T]):
+        none = np.zeros(T, dtype=bool)
+        got, ref = near(moe, logits, ids, scoring, offsets=offsets, mask=none)
+        assert not got.any() and not ref.any()
+    some = np.ones(T, dtype=bool)
+    some[T // 5:T // 2] = False  # all of the third, and one token of the last but one
+    some[T - 2] = False
+    near(moe, logits, ids, scoring, offsets=cuts, mask=some)
+    some[:T - 1] = False  # the last one's alone
+    near(moe, logits, ids, scoring, offsets=cuts, mask=some)
