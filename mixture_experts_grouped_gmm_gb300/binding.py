@@ -12,6 +12,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmgemm.so")
@@ -230,6 +231,16 @@ def _p(t):
 def _stream(t=None):
     # (torch.cuda.current_stream builds a Stream object; this is its handle alone)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if t is None else t.get_device())
+
+
+def differentiated(*ts):
+    """Whether a call on these tensors (or None) is to be differentiated: one of them requires a gradient and
+    gradients are on, or comes with a tangent (forward mode, which requires_grad does not tell of)."""
+    grads = torch.is_grad_enabled()
+    for t in ts:
+        if t is not None and ((grads and t.requires_grad) or unpack_dual(t).tangent is not None):
+            return True
+    return False
 
 
 def _check(rc, what):

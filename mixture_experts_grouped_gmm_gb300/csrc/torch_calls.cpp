@@ -53,6 +53,12 @@ bool beside(const at::Tensor *t, at::ScalarType type, const at::Tensor &other) {
   return on_gpu(t, type) && t->get_device() == other.get_device();
 }
 
+// Whether a call on the tensor is to be differentiated: it requires a gradient and gradients are on, or comes with a
+// tangent (forward mode).  The caller records or refuses such a call.
+bool differentiated(const at::Tensor *t, bool grads) {
+  return t && ((grads && t->requires_grad()) || t->_fw_grad(0).defined());
+}
+
 mgemm_stream_t stream_of(const at::Tensor &t) {
   return reinterpret_cast<mgemm_stream_t>(c10::cuda::getCurrentCUDAStream(t.get_device()).stream());
 }
@@ -150,7 +156,7 @@ PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     const at::Tensor *l = tensor(a[0]), *b = tensor(a[3]);
     const int type = logits_type(l);
-    if (type >= 0 && l->requires_grad() && c10::GradMode::is_enabled()) Py_RETURN_NONE;  // (a differentiable call)
+    if (type >= 0 && differentiated(l, c10::GradMode::is_enabled())) Py_RETURN_NONE;
     if (type < 0 || (a[3] != Py_None && !(beside(b, at::kFloat, *l) && b->numel() == l->size(1) && b->is_contiguous())))
       Py_RETURN_NONE;
     bool bad = false;
@@ -295,7 +301,7 @@ PyObject *gmm(PyObject *, PyObject *const *a, Py_ssize_t n) {
         !beside(g, at::kLong, *x) || !THPDevice_Check(a[4]) || reinterpret_cast<THPDevice *>(a[4])->device != x->device())
       Py_RETURN_NONE;
     const int64_t E = s[0], N = s[1], K = s[2], M = x->dim() == 2 ? x->size(0) : -1;
-    if (M < 0 || x->size(1) != K || (x->requires_grad() && a[6] == Py_True) || g->numel() != E || !g->is_contiguous())
+    if (M < 0 || x->size(1) != K || differentiated(x, a[6] == Py_True) || g->numel() != E || !g->is_contiguous())
       Py_RETURN_NONE;
     const int64_t ld = x->stride(0);
     if (x->stride(1) != 1 || ld < K || ld % 8 || reinterpret_cast<uintptr_t>(x->data_ptr()) % 16) Py_RETURN_NONE;
@@ -346,7 +352,7 @@ PyObject *norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!small(T) || !small(C) || !rows_of(*x, T, C, codes) || w->numel() != C || !w->is_contiguous()) Py_RETURN_NONE;
     if (codes && (C % 32 || reinterpret_cast<uintptr_t>(w->data_ptr()) % 16)) Py_RETURN_NONE;
     if (a[3] != Py_None && (rt < 0 || r->get_device() != x->get_device() || !rows_of(*r, T, C, codes))) Py_RETURN_NONE;
-    if (grads && (x->requires_grad() || w->requires_grad() || (r && r->requires_grad()))) Py_RETURN_NONE;
+    if (differentiated(x, grads) || differentiated(w, grads) || differentiated(r, grads)) Py_RETURN_NONE;
     at::Tensor out, h, q, sc;
     int rc;
     {
@@ -451,7 +457,7 @@ PyObject *balance(PyObject *, PyObject *const *a, Py_ssize_t n) {
   return guarded([&]() -> PyObject * {
     const at::Tensor *l = tensor(a[0]), *ids = tensor(a[1]);
     const int type = logits_type(l);
-    if (type < 0 || (l->requires_grad() && a[7] == Py_True) || !beside(ids, at::kInt, *l) || ids->dim() != 2 ||
+    if (type < 0 || differentiated(l, a[7] == Py_True) || !beside(ids, at::kInt, *l) || ids->dim() != 2 ||
         ids->size(0) != l->size(0) || !ids->is_contiguous())
       Py_RETURN_NONE;
     bool bad = false;
@@ -524,7 +530,7 @@ PyObject *gmm_int4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!w->is_contiguous() || sc->numel() != scales || !sc->is_contiguous() ||
         (z && (z->numel() != scales || !z->is_contiguous())))
       Py_RETURN_NONE;
-    if (!rows_of(*x, M, K, true) || (x->requires_grad() && a[6] == Py_True) || g->dim() != 1 || g->numel() != E ||
+    if (!rows_of(*x, M, K, true) || differentiated(x, a[6] == Py_True) || g->dim() != 1 || g->numel() != E ||
         !g->is_contiguous())
       Py_RETURN_NONE;
     at::Tensor out;

@@ -140,7 +140,7 @@ def gmm_fp4(x, w, group_sizes, out=None, workspace=None):
     E, N, K = w.shape
     if x.dtype != BF16 or x.dim() != 2 or x.shape[1] != K:
         raise B.MgemmError(f"gmm_fp4 takes bf16 x [M, {K}]")
-    if x.requires_grad and torch.is_grad_enabled():
+    if B.differentiated(x):
         raise B.MgemmError("gmm_fp4 has no gradient: call it under torch.no_grad() or on x.detach()")
     if group_sizes.dtype != torch.int64 or group_sizes.numel() != E or not group_sizes.is_contiguous():
         raise B.MgemmError("group_sizes must be contiguous int64 [E]")

@@ -109,7 +109,7 @@ def route_experts(logits, topk, scoring="softmax", bias=None, n_group=1, topk_gr
     if r is not None:
         return r if type(r) is tuple else B._check(r, "mgemm_route")
     # not the plain case: looked at, mended or refused here
-    if logits.requires_grad and torch.is_grad_enabled():
+    if B.differentiated(logits):
         return Router.apply(logits, topk, scoring, bias, n_group, topk_group, group_top, renormalize, scale)
     logits = _route_logits(logits, scoring)
     if bias is not None and (bias.dtype != torch.float32 or bias.numel() != logits.shape[1] or
@@ -177,10 +177,12 @@ def _balance_inputs(logits, scoring, offsets, mask):
 
 
 def _balance(logits, topk_ids, scoring, scale, offsets, mask, wanted):
-    """(loss, counts, slopes) of logits that need no gradient."""
-    r = B.calls().balance(logits, topk_ids, SCORES.get(scoring), scale, offsets, mask, wanted, False)
+    """(loss, counts, slopes) as ``BalanceLoss`` records it where the logits are to be differentiated."""
+    r = B.calls().balance(logits, topk_ids, SCORES.get(scoring), scale, offsets, mask, wanted, torch.is_grad_enabled())
     if r is not None:
         return r if type(r) is tuple else B._check(r, "mgemm_balance")
+    if B.differentiated(logits):
+        return BalanceLoss.apply(logits, topk_ids, scoring, scale, offsets, mask, wanted)
     # not the plain case: looked at, mended or refused here
     logits, offsets, mask = _balance_inputs(logits.detach(), scoring, offsets, mask)
     if topk_ids.dtype not in (torch.int32, torch.int64) or topk_ids.dim() != 2 or topk_ids.shape[0] != logits.shape[0] or \
@@ -215,16 +217,12 @@ def balance_loss(logits, topk_ids, scoring="softmax", scale=1.0, offsets=None, m
     the sequences that have tokens, and int64 [E] (with offsets [S, E]; [E] is the
     group_sizes of a grouped GEMM over the picks).  Logits that require a gradient go
     through ``BalanceLoss``."""
-    if logits.requires_grad and torch.is_grad_enabled():
-        return BalanceLoss.apply(logits, topk_ids, scoring, scale, offsets, mask)
     return _balance(logits, topk_ids, scoring, scale, offsets, mask, False)[:2]
 
 
 def balance_loss_forward(logits, topk_ids, scoring="softmax", scale=1.0, offsets=None, mask=None):
     """balance_loss and what its backward pass reads: (loss, counts, slopes float32 [S * E + 1]).  As balance_loss, the
     loss has a gradient where the logits require one."""
-    if logits.requires_grad and torch.is_grad_enabled():
-        return BalanceLoss.apply(logits, topk_ids, scoring, scale, offsets, mask, True)
     return _balance(logits, topk_ids, scoring, scale, offsets, mask, True)
 
 
@@ -412,7 +410,7 @@ def fused_experts_fp4(hidden_states, w1, w2, topk_weights, topk_ids):
     if topk_ids.dim() != 2 or topk_weights.shape != topk_ids.shape:
         raise B.MgemmError(f"fused_experts_fp4 takes topk_weights and topk_ids [T, top_k], not {tuple(topk_weights.shape)} "
                            f"and {tuple(topk_ids.shape)}")
-    if torch.is_grad_enabled() and (hidden_states.requires_grad or topk_weights.requires_grad):
+    if B.differentiated(hidden_states, topk_weights):
         raise B.MgemmError("the 4-bit layer has no gradient: call it under torch.no_grad() or on detached tensors")
     T, top_k = topk_ids.shape
     _check_tokens(hidden_states, T)

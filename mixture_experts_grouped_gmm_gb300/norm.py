@@ -92,10 +92,6 @@ def _norm(x, weight, eps, residual, code, wanted, what):
     return B._check(r, "mgemm_rms_norm") if type(r) is int else r
 
 
-def _wants_grad(*ts):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in ts)
-
-
 def rms_norm(x, weight, eps=1e-6, residual=None):
     """x / sqrt(mean(x^2) + eps) * weight of each row of x [T, C], in bf16; with a
     residual the norm of h = x + residual (rounded to the residual's type).
@@ -107,7 +103,7 @@ def rms_norm(x, weight, eps=1e-6, residual=None):
     if type(r) is not tuple:
         if r is not None:
             B._check(r, "mgemm_rms_norm")
-        if _wants_grad(x, weight, residual):
+        if B.differentiated(x, weight, residual):
             return RmsNorm.apply(x, weight, eps, residual)
         r = _norm(x, weight, eps, residual, B.MGEMM_BF16, True, "rms_norm")
     return r[0] if residual is None else r[:2]
@@ -126,7 +122,7 @@ def rms_norm_fp8(x, weight, fmt="rowwise", eps=1e-6, residual=None, with_bf16=Fa
     if type(r) is not tuple:
         if r is not None:
             B._check(r, "mgemm_rms_norm")
-        if _wants_grad(x, weight, residual):
+        if B.differentiated(x, weight, residual):
             raise B.MgemmError("rms_norm_fp8 has no gradient: call it under torch.no_grad() or on detached tensors")
         r = _norm(x, weight, eps, residual, code, bool(with_bf16), "rms_norm_fp8")
     out, h, codes, scales = r

@@ -18,7 +18,8 @@ def mg():
     from mixture_experts_grouped_gmm_gb300 import build
 
     build.build()
-    return m
+    yield m
+    torch.cuda.empty_cache()  # (the float64 weights' blocks: tests of failing allocations count on an empty cache)
 
 
 def values(w, e):
