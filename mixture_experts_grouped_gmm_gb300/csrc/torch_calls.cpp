@@ -530,8 +530,8 @@ PyObject *gmm_int4(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!w->is_contiguous() || sc->numel() != scales || !sc->is_contiguous() ||
         (z && (z->numel() != scales || !z->is_contiguous())))
       Py_RETURN_NONE;
-    if (!rows_of(*x, M, K, true) || differentiated(x, a[6] == Py_True) || g->dim() != 1 || g->numel() != E ||
-        !g->is_contiguous())
+    if (!rows_of(*x, M, K, true) || differentiated(x, a[6] == Py_True) || differentiated(sc, a[6] == Py_True) ||
+        g->dim() != 1 || g->numel() != E || !g->is_contiguous())
       Py_RETURN_NONE;
     at::Tensor out;
     int rc;

@@ -90,8 +90,8 @@ def gmm_int4(x, w, group_sizes, out=None, status=None):
     (E, N), K = w.codes.shape[:2], 2 * w.codes.shape[2]
     if x.dtype != BF16 or x.dim() != 2 or x.shape[1] != K:
         raise B.MgemmError(f"gmm_int4 takes bf16 x [M, {K}]")
-    if B.differentiated(x):
-        raise B.MgemmError("gmm_int4 has no gradient: call it under torch.no_grad() or on x.detach()")
+    if B.differentiated(x, w.scales):
+        raise B.MgemmError("gmm_int4 has no gradient: call it under torch.no_grad() or on detached x and scales")
     if group_sizes.dtype != torch.int64 or group_sizes.shape != (E,) or not group_sizes.is_contiguous():
         raise B.MgemmError(f"group_sizes must be contiguous int64 [{E}]")
     if status is not None and (status.dtype != torch.int32 or status.numel() != 1):

@@ -50,3 +50,18 @@ def test_long_contractions_of_many_tiles(mg, E, M, N, K, group):
                 tol = 2.0 ** -8 * (rows @ v.t()).abs() + 2.0 ** -16 * (rows.abs() @ v.abs().t())
                 assert bool(((got[first:first + n] - rows @ v.t()).abs() <= tol).all()), e
             first += n
+
+
+def test_scales_that_require_a_gradient(mg):
+    """They are no less refused than token rows: no gradient flows through the product."""
+    x, g = torch.ones(3, 64, dtype=BF, device=DEV), torch.tensor([3], device=DEV)
+    codes = torch.full((1, 8, 32), 0x99, dtype=torch.uint8, device=DEV)
+    leaf = torch.ones(1, 8, 1, dtype=BF, device=DEV).requires_grad_()
+    w = mg.Int4Tensor(codes, leaf, None, 64)
+    for kw in ({}, dict(out=torch.empty(3, 8, dtype=BF, device=DEV))):
+        with pytest.raises(mg.binding.MgemmError, match="no gradient"):
+            mg.gmm_int4(x, w, g, **kw)
+        with torch.no_grad():
+            assert bool((mg.gmm_int4(x, w, g, **kw) == 64).all())
+    w.scales = leaf.detach()
+    assert bool((mg.gmm_int4(x, w, g) == 64).all())
