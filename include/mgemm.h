@@ -846,7 +846,7 @@ int mgemm_gmm_fp4(const int64_t *group_sizes, int E, int fmt, const void *x, int
  * (% 8 == 0).  With zeros: lo = min(0, min), hi = max(0, max) of the group, scale =
  * bf16((hi / 2 - lo / 2) / 7.5), zero = clamp(rint(-lo / scale), 0, 15); without: scale =
  * bf16(max |w| / 7), zero 8.  A scale that is 0 becomes 1; q = clamp(rint(w / scale) + zero,
- * 0, 15).  A group that holds NaN or infinity gets a NaN scale.  K % group == 0.
+ * 0, 15).  A group that holds NaN or infinity gets a NaN scale.  K % group == 0, K up to 2^30.
  *
  * mgemm_gmm_int4 -- out[rows of group e] = x[rows of group e] . w[e]^T, each group's
  * products in float32, scaled and added in float32, rounded to bf16 once; the codes are
@@ -905,7 +905,7 @@ int mgemm_gmm_int4(const int64_t *group_sizes, int E, const void *x, int64_t ld_
  * Sums of rows are taken in a fixed order (the same bits on every call).
  *
  * mgemm_dequant_fp8 -- the values of such codes (code / s, code 2^(byte - 127)) in
- * bf16: exact, but past bf16's range.  codes [T, C] dense; out bf16 [T, C] dense.
+ * bf16: exact, but past bf16's range.  codes [T, C] dense, C up to 2^30; out bf16 [T, C] dense.
  */
 #define MGEMM_F32 4
 #define MGEMM_MXFP8 5

@@ -483,7 +483,7 @@ int launch_gmm_rows(const GmmParams &p, cudaStream_t s) {
   return (active > parts ? active : parts) * tiles_n <= few ? launch_gmm<2, 2, 1, 8, GROUP>(p, s) : launch_gmm<2, 2, 1, 4, GROUP>(p, s);
 }
 
-constexpr int kMaxRows = 1 << 24, kMaxSide = 1 << 26;
+constexpr int kMaxRows = 1 << 24, kMaxSide = 1 << 26, kMaxCastK = 1 << 30;  // (the cast's columns stay an int)
 
 }  // namespace
 }  // namespace mgemm
@@ -492,7 +492,7 @@ using namespace mgemm;
 
 extern "C" int mgemm_quant_int4_groups(const void *in, int64_t rows, int K, int64_t ld_in, int group, uint8_t *codes,
                                        void *scales, uint8_t *zeros, mgemm_stream_t stream) {
-  if (rows < 0 || K < 1 || ld_in < K || !group_ok(group)) return MGEMM_EINVAL;
+  if (rows < 0 || K < 1 || K > kMaxCastK || ld_in < K || !group_ok(group)) return MGEMM_EINVAL;
   if (K % group) return MGEMM_EALIGN;
   if (rows == 0) return MGEMM_OK;
   if (!in || !codes || !scales) return MGEMM_EINVAL;

@@ -447,6 +447,8 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float *__restri
   }
 }
 
+// (a column and the CTA's threads past it stay an int)
+constexpr int kMaxDequantColumns = 1 << 30;
 // 16 codes a thread, rows by threadIdx.y: the value of a code times a power of two, in bf16 (exact but past its range).
 __global__ void __launch_bounds__(256) dequant_fp8_kernel(const uint8_t *__restrict__ codes, const void *__restrict__ scales,
                                                           int mx, int64_t ld_sf, int64_t T, int C,
@@ -620,7 +622,7 @@ extern "C" int mgemm_rms_norm_bwd(const void *grad_out, int64_t ld_g, const void
 extern "C" int mgemm_dequant_fp8(const uint8_t *codes, const void *scales, int fmt, int64_t T, int C, int64_t ld_sf,
                                  void *out, mgemm_stream_t stream) {
   if (fmt != MGEMM_FP8_E4M3 && fmt != MGEMM_MXFP8) return MGEMM_EINVAL;
-  if (T < 0 || T >= (int64_t(1) << 31) || C < 1) return MGEMM_EINVAL;
+  if (T < 0 || T >= (int64_t(1) << 31) || C < 1 || C > kMaxDequantColumns) return MGEMM_EINVAL;
   if (fmt == MGEMM_MXFP8 && ld_sf < (C + 31) / 32) return MGEMM_EINVAL;
   if (T == 0) return MGEMM_OK;
   if (!codes || !scales || !out) return MGEMM_EINVAL;

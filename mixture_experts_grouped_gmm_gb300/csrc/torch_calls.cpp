@@ -421,7 +421,9 @@ PyObject *dequantize8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t fmt = integer(a[2], bad);
     const bool mx = fmt == MGEMM_MXFP8;
     if (bad || !on_gpu(q, at::kByte) || !beside(sc, mx ? at::kByte : at::kFloat, *q)) Py_RETURN_NONE;
-    if (q->dim() != 2 || !q->is_contiguous() || sc->size(0) != q->size(0) || !sc->is_contiguous()) Py_RETURN_NONE;
+    if (q->dim() != 2 || !small(q->size(1)) || !q->is_contiguous() || sc->dim() < 1 || sc->size(0) != q->size(0) ||
+        !sc->is_contiguous())
+      Py_RETURN_NONE;
     at::Tensor out;
     int rc;
     {

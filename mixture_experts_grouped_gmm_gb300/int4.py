@@ -56,9 +56,10 @@ def quantize_int4(w, group=128, zeros=False):
     row, and with ``zeros`` a zero point (else 8, levels -8 .. 7).  K % group == 0, N % 8 == 0."""
     if group not in GROUPS:
         raise B.MgemmError(f"quantize_int4 takes groups of {', '.join(map(str, GROUPS))} elements, not {group}")
-    if w.dtype != BF16 or w.dim() not in (2, 3) or w.numel() == 0 or w.shape[-1] % group or w.shape[-2] % 8:
-        raise B.MgemmError(f"quantize_int4 takes a bf16 [E, N, K] or [N, K], K a multiple of {group} and N of 8, not {w.dtype} "
-                           f"{tuple(w.shape)}")
+    if w.dtype != BF16 or w.dim() not in (2, 3) or w.numel() == 0 or w.shape[-1] % group or w.shape[-1] > 1 << 30 or \
+            w.shape[-2] % 8:
+        raise B.MgemmError(f"quantize_int4 takes a bf16 [E, N, K] or [N, K], K a multiple of {group} up to 2^30 and N of 8, "
+                           f"not {w.dtype} {tuple(w.shape)}")
     B._cuda(w)
     w = w if w.dim() == 3 else w[None]
     E, N, K = w.shape

@@ -138,7 +138,7 @@ def dequantize_fp8(q):
     r = B.calls().dequantize8(q.codes, q.scales, FORMATS[q.fmt])
     if r is None:
         B._cuda(q.codes, q.scales)
-        raise B.MgemmError("dequantize_fp8 takes contiguous codes and scales")
+        raise B.MgemmError("dequantize_fp8 takes contiguous codes and scales, rows of up to 2^30 elements")
     return B._check(r, "mgemm_dequant_fp8") if type(r) is int else r
 
 
