@@ -875,10 +875,10 @@ int mgemm_gmm_int4(const int64_t *group_sizes, int E, const void *x, int64_t ld_
  *   h = x + residual, rounded to the residual's type (without one, h = x)
  *   y = h / sqrt(mean(h^2) + eps) * weight
  * in float32; h is what the next layer reads, and the norm is that of the stored
- * values.  Rows whose squares pass float32's range are scaled first.
+ * values.  Rows whose squares, or their mean with eps, pass float32's range are scaled first.
  *   x         [T, C] of x_type (MGEMM_BF16 or MGEMM_F32), rows ld_x elements apart
  *   residual  [T, C] of r_type, rows ld_r apart, or NULL; MGEMM_F32 where x is
- *   weight    [C] of w_type, magnitudes below 2^60
+ *   weight    [C] of w_type, magnitudes below 2^60 (products h weight below 2^-126 lose bits)
  *   h         [T, C] of r_type (dense), with residual; else NULL
  *   out       bf16 [T, C] (dense): y rounded once; may be NULL where there are codes
  *   fmt       MGEMM_BF16: no codes.  MGEMM_FP8_E4M3: codes uint8 [T, C] = e4m3(y s),

@@ -166,8 +166,8 @@ __device__ __forceinline__ float2 row_reduce(float a, float b, float2 *part) {
   return v;
 }
 
-// A row whose squares pass float32's range is scaled by a power of two first: its largest value is 2^57 at least and
-// below 2^128, so what is left of it has squares between 2^-46 and 2^96, and eps is nothing beside them.
+// A row whose squares, or their mean with eps, pass float32's range is scaled by a power of two first: its largest value
+// is 2^57 at least and below 2^128, so what is left of it has squares between 2^-46 and 2^96; eps is scaled alike.
 constexpr float kDown = 0x1p-80f, kMostSquares = 0x1.fffffep127f;
 
 struct NormParams {
@@ -271,17 +271,17 @@ __global__ void __launch_bounds__(kMaxThreads, VEC && U == 1 ? 2 : 1) rms_norm_k
       return row_reduce<kMax>(ssq, most, part[flip]);
     };
     float2 all = reduce();
-    float eps = p.eps;
-    if (!(all.x <= kMostSquares)) {  // (the row's threads agree)
+    float square = __fdiv_rn(all.x, (float)C) + p.eps;
+    if (!(square <= kMostSquares)) {  // (the row's threads agree)
       if (blockDim.x > 32) __syncthreads();  // the buffer is read
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[u][i] *= kDown;
       all = reduce();
-      eps = 0.f;
+      square = __fdiv_rn(all.x, (float)C) + p.eps * kDown * kDown;
     }
-    const float r = __frsqrt_rn(__fdiv_rn(all.x, (float)C) + eps);
+    const float r = __frsqrt_rn(square);
     const float s = p.fmt == MGEMM_FP8_E4M3 ? pow2_scale_from_amax(all.y * r) : 1.f;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -380,8 +380,8 @@ __global__ void __launch_bounds__(kMaxThreads, VEC && U == 1 ? 2 : 1) rms_norm_b
       return row_reduce<kSum>(ssq, dot, part[flip]);
     };
     float2 all = reduce();
-    float eps = p.eps, down = 1.f;
-    if (!(all.x <= kMostSquares)) {
+    float square = __fdiv_rn(all.x, (float)C) + p.eps, down = 1.f;
+    if (!(square <= kMostSquares)) {
       if (blockDim.x > 32) __syncthreads();
       down = kDown;
 #pragma unroll
@@ -389,9 +389,9 @@ __global__ void __launch_bounds__(kMaxThreads, VEC && U == 1 ? 2 : 1) rms_norm_b
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[u][i] *= kDown;
       all = reduce();
-      eps = 0.f;
+      square = __fdiv_rn(all.x, (float)C) + p.eps * kDown * kDown;
     }
-    const float r = __frsqrt_rn(__fdiv_rn(all.x, (float)C) + eps);
+    const float r = __frsqrt_rn(square);
     const float across = __fdiv_rn(all.y, (float)C) * r;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
