@@ -176,3 +176,29 @@ def test_masks_that_empty_sequences(moe, scoring, T, E, k):
     near(moe, logits, ids, scoring, offsets=cuts, mask=some)
     some[:T - 1] = False  # the last one's alone
     near(moe, logits, ids, scoring, offsets=cuts, mask=some)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("T,E", [(60, 24), (300, 256), (200, 513)])
+def test_rows_that_do_not_count_may_hold_anything(moe, scoring, dtype, T, E):
+    """NaN, infinities and the largest values outside the mask and the sequences: the same bits as with zeros there."""
+    logits, ids = inputs(T, E, 3, 10, dtype)
+    mask = torch.ones(T, dtype=torch.bool, device=DEV)
+    mask[7::5] = False
+    o = torch.tensor([4, T // 2, T - 9], device=DEV)
+    counts = mask.clone()
+    counts[:4] = counts[T - 9:] = False
+    clean, dirty = logits.clone(), logits.clone()
+    clean[~counts] = 0
+    bad = torch.tensor([float("nan"), float("inf"), -float("inf"), torch.finfo(dtype).max, torch.finfo(dtype).min], device=DEV)
+    n = int((~counts).sum())
+    dirty[~counts] = bad[torch.arange(n * E, device=DEV).view(n, E) % 5].to(dtype)
+    dirty[3] = float("nan")
+    one, got = torch.ones((), device=DEV), []
+    for l in (clean, dirty):
+        loss, c, slopes = moe.balance_loss_forward(l, ids, scoring, 1.0, o, mask)
+        got.append((loss, c, slopes, moe.balance_loss_backward(one, l, slopes, scoring, o, mask)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert not got[1][3][~counts].any() and got[1][3][counts].any() and torch.isfinite(got[1][0])
