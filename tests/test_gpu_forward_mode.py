@@ -68,3 +68,19 @@ def test_layer_of_4_bit_experts(mg):
     w2 = mg.quantize_fp4(torch.randn(4, 128, 128, device=DEV).to(BF), "mxfp4")
     weights, ids = mg.moe.route_experts(torch.randn(6, 4, device=DEV), 2)
     refuses(lambda x, p: mg.moe.fused_experts_fp4(x, w1, w2, p, ids), x, weights)
+
+
+def test_transforms(mg):
+    """torch.func's transforms wrap tensors: each call raises, none computes on what is inside."""
+    x, w = torch.randn(4, 64, device=DEV), torch.randn(64, device=DEV)
+    logits, ids = torch.randn(9, 16, device=DEV), torch.zeros(9, 2, dtype=torch.int32, device=DEV)
+    sizes = torch.tensor([4], device=DEV)
+    wi = mg.quantize_int4(torch.randn(8, 64, device=DEV).to(BF), 64)
+    for call, t in ((lambda t: mg.rms_norm(t, w).float().sum(), x), (lambda t: mg.moe.balance_loss(t, ids)[0], logits),
+                    (lambda t: mg.moe.route_experts(t, 2)[0].sum(), logits),
+                    (lambda t: mg.gmm_int4(t.to(BF), wi, sizes).float().sum(), x)):
+        call(t)
+        for transform in (lambda: torch.func.grad(call)(t), lambda: torch.func.jvp(call, (t,), (t,)),
+                          lambda: torch.func.vmap(call)(t[None].repeat(2, 1, 1))):
+            with pytest.raises((RuntimeError, NotImplementedError)):
+                transform()
