@@ -169,15 +169,32 @@ __device__ __forceinline__ void scores(float (&v)[V]) {
 __device__ __forceinline__ float by_sum(float sum) { return sum == 0.f ? 0.f : rcp_approx(sum); }
 
 // Sigmoids can be so small that the reciprocal of their sum, or its product with the loss's gradient, passes float32,
-// and the smallest of them or their products with the slopes its normal numbers.  Such a row (its sum is not 0) is read
-// again: its sigmoids are exp(l), here times 2^83 (between 2^-43 and 2^43 for the largest), and 1 - s is 1.
-constexpr float kSmallSum = 0x1p-40f;
+// and the smallest of them or their products with the slopes its normal numbers.  A row where they are (no lane's part of
+// the sum reaches 2^-40; the vote runs beside the sum's reduction) is read again: its sigmoids are exp(l), here times
+// 2^126, its 1 - s are 1, and its scores are divided by their sum at once (the sum left is 1).
+constexpr float kSmallPart = 0x1p-40f;
+template <int LPR>
+__device__ __forceinline__ bool all_small(float part) {
+  const uint32_t low = __ballot_sync(kFull, part < kSmallPart);
+  if (LPR == 32) return low == kFull;
+  const uint32_t lanes = ((1u << (LPR & 31)) - 1) << (threadIdx.x & 31 & ~(LPR - 1));
+  return (low & lanes) == lanes;
+}
+// In any row of the warp.
+template <int LPR>
+__device__ __forceinline__ bool any_small(bool small) {
+  return LPR == 32 ? small : __any_sync(kFull, small);
+}
 template <typename L, int LPR, int V, bool VEC>
-__device__ __forceinline__ void small_scores(const L *row, int lane, int E, bool small, float (&v)[V]) {
-  float l[V];
-  load_row<LPR, V, VEC>(row, lane, E, l);
+__device__ __forceinline__ void small_scores(const L *row, int lane, int E, bool small, float (&v)[V], float &sum) {
+  float p[V], all = 0.f;
+  load_row<LPR, V, VEC>(row, lane, E, p);
 #pragma unroll
-  for (int j = 0; j < V; ++j) v[j] = small ? exp2_approx(fmaf(l[j], kLog2e, 83.f)) : v[j];
+  for (int j = 0; j < V; ++j) p[j] = exp2_approx(fmaf(p[j], kLog2e, 126.f)), all += p[j];
+  const float f = by_sum(lanes_sum<LPR>(all));
+#pragma unroll
+  for (int j = 0; j < V; ++j) v[j] = small ? p[j] * f : v[j];
+  sum = small ? 1.f : sum;
 }
 
 __device__ __forceinline__ int64_t bound_of(const BalanceParams &p, int64_t s) {
@@ -350,16 +367,11 @@ __global__ void __launch_bounds__(kThreads) balance_kernel(const BalanceParams p
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j) sum += v[j];
+      const bool small = SIGMOID && all_small<LPR>(sum);
       sum = lanes_sum<LPR>(sum);
       if constexpr (SIGMOID) {
-        const bool small = sum > 0.f && sum < kSmallSum;
-        if (__any_sync(kFull, small)) {
-          small_scores<L, LPR, V, VEC>((const L *)p.logits + (t < last ? t : first) * p.ld, lane, E, small, v);
-          sum = 0.f;
-#pragma unroll
-          for (int j = 0; j < V; ++j) sum += v[j];
-          sum = lanes_sum<LPR>(sum);
-        }
+        if (any_small<LPR>(small))
+          small_scores<L, LPR, V, VEC>((const L *)p.logits + (t < last ? t : first) * p.ld, lane, E, small, v, sum);
       }
       const float f = by_sum(sum);
       if (live) {
@@ -502,18 +514,17 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(const BalanceBwdP
 #pragma unroll
       for (int j = 0; j < V; ++j) sum += v[j], dot = fmaf(v[j], a[j], dot);
     }
+    const bool small = SIGMOID && all_small<LPR>(sum);
     sum = lanes_sum<LPR>(sum);
     dot = lanes_sum<LPR>(dot);
     if constexpr (SIGMOID) {
-      const bool small = sum > 0.f && sum < kSmallSum;
-      if (__any_sync(kFull, small)) {
-        small_scores<L, LPR, V, VEC>((const L *)p.logits + (live ? t : 0) * p.ld, lane, E, small, v);
-        float sum2 = 0.f, dot2 = 0.f;
+      if (any_small<LPR>(small)) {
+        small_scores<L, LPR, V, VEC>((const L *)p.logits + (live ? t : 0) * p.ld, lane, E, small, v, sum);
+        float again = 0.f;
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum2 += v[j], dot2 = fmaf(v[j], a[j], dot2);
-        sum2 = lanes_sum<LPR>(sum2);
-        dot2 = lanes_sum<LPR>(dot2);
-        if (small) sum = sum2, dot = dot2;
+        for (int j = 0; j < V; ++j) again = fmaf(v[j], a[j], again);
+        again = lanes_sum<LPR>(again);
+        if (small) dot = again;
       }
     }
     const float f = by_sum(sum);

@@ -118,7 +118,7 @@ def test_sigmoids_near_the_smallest_numbers(moe, T, E, k, dtype):
     """Rows whose sigmoids are below 2^-100, some below 2^-126, beside others in the same warp; exp(l) times a power of
     two is at most as far off as the sigmoid in the bound above."""
     logits, ids = inputs(T, E, k, 5, dtype)
-    for center in (-72.0, -84.0, -86.2):
+    for center in (-28.0, -72.0, -84.0, -86.2, -89.0, -130.0, -170.0):
         got, ref = near(moe, logits.clamp(-1.2, 1.2) + center, ids, grad=2.0 ** 40)
         assert np.all((got != 0) == (ref != 0))
     mixed = logits.clamp(-1.2, 1.2) - 86.2
