@@ -7,8 +7,11 @@
 //   dL/dl_te = p_te (a_se - sum_j p_tj a_sj) [sigmoid: times 1 - s_te],  a_se = scale' E c_se / (k n_s^2)
 //   (1 - s = e s with e = exp(-l): the difference itself has no bits left for large logits)
 //
-// Bound by instruction issue (147 warp instructions a row of 256 experts forward, 231 for the gradient: 65536 x 256
-// fp32 in 24 sequences 18.6 + 9.4 + 22 us, whose bytes take 10 + 0 + 10 and 10); small calls by their launches.  LPR
+// No unit is full: 65536 x 256 fp32 logits of sigmoids in 24 sequences take 18.6 + 9.4 us and 24.1 for the gradient, whose
+// bytes take 10 + 0 and 20.  A row of 256 experts has 200 warp instructions forward and 252 for the gradient (11 and 14 us
+// at full issue; 73% and 64% of the slots are used while an SM is busy), one row a warp at a time, so that its chain of
+// load, scores, five shuffles and products is partly waited for; a quarter and a sixth of the launches are their starts and
+// ends.  The second launch is a chain of loads and barriers.  Small calls are bound by their launches.  LPR
 // lanes take a row, V logits each, and keep the sums of p over their rows in registers.  A CTA owns R
 // consecutive rows; at each end of a sequence in them it writes its sums and counts to
 // a slot of its own, so that sums are taken in a fixed order: CTA b writes sequence s's

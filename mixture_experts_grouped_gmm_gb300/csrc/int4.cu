@@ -8,11 +8,15 @@
 // summed in float32 by mma.sync with the weights as its 16 rows and the tokens as its 8
 // columns, and the scale multiplies that sum: no rounding but float32's.
 //
-// Bound by instruction issue and the logic pipe (340 warp instructions for 32 rows by 128
-// elements, 152 of them the unpacking): 16 rows at 16 experts of 8192 x 5120 in groups of
-// 128 with zero points take 77 us, the stream of their 352 MB 52.  (On tcgen05 the unpacked
-// weights have to go through shared memory, and every group's sums back from tensor memory:
-// 128 rows over 8 experts of 6400 x 4096 took 94 us that way, 51 this way.)
+// No unit is full: 16 rows at 16 experts of 8192 x 5120 in groups of 128 with zero points
+// take 77 us, the stream of their 352 MB 52, and 325 warp instructions for 32 rows by 128
+// elements 43 at full issue (152 unpack, 16 are MMAs, 18 load from shared memory; the rest
+// copies, scales, addresses and loops).  65% of the issue slots and 53% of the logic pipe are
+// used, by 14 warps an SM that wait for their own chains: load from shared memory, unpack,
+// MMA, scaled sum.  (A form on tcgen05, with unpacked weights through shared memory and every
+// group's sums back from tensor memory, took 94 us for 128 rows over 8 experts of 6400 x 4096
+// when this one took 68; what bounded it was not found, and it had not the scale windows,
+// dropped columns and balanced passes that brought this one to 52.)
 //
 // A CTA's warps form crews of WK teams of WN warps.  A crew has a tile: WN x MT x 16 rows of
 // weights by NT x 8 tokens; its teams take the contraction's steps of 128 in turn and add up
@@ -56,8 +60,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], bool add, uint32_t a0, u
 // Codes to bf16.  Bits 0 .. 7 of a bf16 stand for their whole number times 2^-133 (subnormals, and the first normals,
 // which have the same step), so a pair of nibbles needs neither a shift to bit 0 nor an exponent: masked, it is q 2^-133
 // or, from the upper half of a byte, q 2^-129, and one fused multiply-add makes it (q - z) / 64, exactly.  (The 64 is
-// put back into the sums.  The logic pipe bounds the kernel: 5 of its instructions for 8 codes; with a shift and 128's
-// exponent for each pair it took 7, and 16 rows at 16 experts of 8192 x 5120 took 85 us, then 77.)
+// put back into the sums.  5 instructions of the logic pipe, the fullest one, for 8 codes; with a shift and 128's
+// exponent for each pair there were 7, and 16 rows at 16 experts of 8192 x 5120 took 85 us instead of 77.)
 __device__ __forceinline__ __nv_bfloat162 bits(uint32_t v) { return *reinterpret_cast<const __nv_bfloat162 *>(&v); }
 constexpr uint32_t kLow = 0x7F007F00u, kHigh = 0x7D007D00u;  // 2^127 and 2^123, twice
 template <uint32_t MASK, uint32_t FACTOR>
