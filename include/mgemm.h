@@ -690,6 +690,8 @@ int mgemm_route_bwd(const float *grad_weights, const void *logits, int logits_bf
  *   p_te = softmax(logits[t, :]) (MGEMM_SCORE_SOFTMAX), or the sigmoids over their sum
  *          (MGEMM_SCORE_SIGMOID); 0 for a logit at or below MGEMM_ROUTE_MASKED, and
  *          everywhere in a row whose scores are all 0 (sigmoids all below 2^-252)
+ *          (scores below 2^-126 beside larger ones, a softmax's relative to its largest, are
+ *          0: a p below 2^-86 may be, which no sum here notices)
  *   L_s  = sum_e (E c_e / (top_k n)) (sum_t p_te / n)
  *   loss = scale times the mean of L_s over the sequences with n > 0 (0 without any)
  *   logits    as for mgemm_route;  topk_ids  int32 [T, top_k] (ids outside [0, E) are not
