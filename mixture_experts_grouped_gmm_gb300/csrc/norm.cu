@@ -12,7 +12,7 @@
 // reduction.  The backward pass computes r again from h, which it reads anyway.
 //
 // Bound by the row's bytes: 16384 x 4096 bf16 with residual 86 us forward (268 MB in, 268
-// out: 6.2 TB/s) and 96 + 5 us backward (403 MB in, 134 out); small calls by their launch.
+// out: 6.2 TB/s) and 94 + 5 us backward (403 MB in, 134 out); small calls by their launch.
 // A row takes blockDim.x threads (a multiple of a warp) with U units of 8 elements each
 // and stays in registers, so each byte is read once; CTAs stay, and a row is asked for
 // while the one before is worked on (109 us forward without).  Rows of one warp share a
